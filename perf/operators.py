@@ -259,7 +259,7 @@ def _log_softmax(z):
 
 def _plain_logprobs(st):
     c, z, t = st["case"], st["z"].float(), st["t"]
-    logp, p, _ = _log_softmax(z)
+    logp, p, lse = _log_softmax(z)
     real = (t >= 0) & (t < c["V"])
     at = torch.where(real, t, torch.zeros_like(t)).unsqueeze(1)
     picked = torch.where(real, logp.gather(1, at).squeeze(1), torch.zeros_like(logp[:, 0]))
@@ -269,7 +269,8 @@ def _plain_logprobs(st):
         order = torch.sort(z, dim=1, descending=True, stable=True)[1][:, : c["top"]]
         out.update(top_logprob=logp.gather(1, order), top_index=order)
     if c["grad"]:
-        gl = torch.where(real, st["g_logprob"], torch.zeros_like(h)).unsqueeze(1)
+        alive = lse.squeeze(1) > -math.inf   # a row that is all -inf has no gradient
+        gl = torch.where(real & alive, st["g_logprob"], torch.zeros_like(h)).unsqueeze(1)
         gh = st["g_entropy"].unsqueeze(1)
         d = torch.where(p > 0, -p * (gl + gh * (logp + h.unsqueeze(1))), torch.zeros_like(p))
         d.scatter_add_(1, at, gl)
@@ -279,14 +280,14 @@ def _plain_logprobs(st):
 
 def _plain_distill(st):
     c, z = st["case"], st["z"].float() / st["case"]["temperature"]
-    logp, p, _ = _log_softmax(z)
+    logp, p, lse = _log_softmax(z)
     real = (st["idx"] >= 0) & (st["idx"] < c["V"])
     at = torch.where(real, st["idx"], torch.zeros_like(st["idx"]))
     logq, q, _ = _log_softmax(torch.where(real, st["val"].float() / c["temperature"], torch.full_like(st["val"], -math.inf)))
     loss = torch.where(q > 0, q * (logq - logp.gather(1, at)), torch.zeros_like(q)).sum(1)
     d = p * (q.sum(1, keepdim=True) > 0)
     d.scatter_add_(1, at, -q)
-    d *= (st["weight"] / c["temperature"]).unsqueeze(1)
+    d *= torch.where(lse > -math.inf, (st["weight"] / c["temperature"]).unsqueeze(1), torch.zeros_like(lse))
     return {"loss": loss, "dlogits": d.to(st["z"].dtype)}
 
 
