@@ -29,6 +29,10 @@ EXPORTED = (
     "qlora_lora_grads_group_workspace_bytes", "qlora_lora_grads_group",
     "qlora_linear_group_workspace_bytes", "qlora_linear_fwd_group",
     "qlora_lora_down_shared", "qlora_lora_dA_shared_workspace_bytes", "qlora_lora_dA_shared",
+    "qlora_mx4_sizes", "qlora_mx4_quantize", "qlora_mx4_dequantize", "qlora_mx4_matmul",
+    "qlora_mx4_linear_workspace_bytes", "qlora_mx4_linear_fwd", "qlora_mx4_linear_bwd",
+    "qlora_vocab_workspace_bytes", "qlora_token_logprobs", "qlora_token_logprobs_bwd",
+    "qlora_distill_fwd", "qlora_distill_bwd", "qlora_distill",
     "qlora_dropout_mask", "qlora_dropout_apply", "qlora_nf4_matmul_dx_dropout",
     "qlora_linear_dropout_workspace_bytes", "qlora_linear_fwd_dropout", "qlora_linear_bwd_dropout",
 )
@@ -106,10 +110,39 @@ class LoraGradsDescStruct(ctypes.Structure):
     ]
 
 
+class MX4ArrayStruct(ctypes.Structure):
+    _fields_ = [
+        ("codes", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p),
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+    ]
+
+
+class LogitsStruct(ctypes.Structure):
+    _fields_ = [
+        ("z", ctypes.c_void_p),
+        ("type", ctypes.c_int32),
+        ("rows", ctypes.c_int64),
+        ("words", ctypes.c_int64),
+        ("pitch", ctypes.c_int64),
+    ]
+
+
+class TeacherStruct(ctypes.Structure):
+    _fields_ = [
+        ("index", ctypes.c_void_p),
+        ("logit", ctypes.c_void_p),
+        ("count", ctypes.c_int32),
+        ("temperature", ctypes.c_float),
+    ]
+
+
 _lib = None
 
 _vp, _i64, _i32, _sz, _f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t, ctypes.c_float
 _wp = ctypes.POINTER(NF4WeightStruct)
+_mp, _lp, _tp = ctypes.POINTER(MX4ArrayStruct), ctypes.POINTER(LogitsStruct), ctypes.POINTER(TeacherStruct)
 
 _SIGS = {
     "qlora_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -148,6 +181,20 @@ _SIGS = {
     "qlora_lora_dA_shared_workspace_bytes": (_sz, [_i64, _i64, ctypes.c_int, ctypes.POINTER(_i32)]),
     "qlora_lora_dA_shared": (ctypes.c_int, [_vp, _i64, _i64, ctypes.c_int, ctypes.POINTER(_vp), ctypes.POINTER(_i32),
                                             ctypes.POINTER(_vp), _vp, _sz, _vp]),
+    "qlora_mx4_sizes": (ctypes.c_int, [_i64, _i64, ctypes.POINTER(_i64), ctypes.POINTER(_i64)]),
+    "qlora_mx4_quantize": (ctypes.c_int, [_vp, _i32, _mp, _vp]),
+    "qlora_mx4_dequantize": (ctypes.c_int, [_mp, _vp, _vp]),
+    "qlora_mx4_matmul": (ctypes.c_int, [_mp, _mp, _vp, _vp, _i32, _vp, _vp]),
+    "qlora_mx4_linear_workspace_bytes": (_sz, [_i64, _i64, _i64, _i32, ctypes.c_int]),
+    "qlora_mx4_linear_fwd": (ctypes.c_int, [_vp, _i64, _mp, _vp, _vp, _i32, _f32, _vp, _vp, _vp, _sz, _vp]),
+    "qlora_mx4_linear_bwd": (ctypes.c_int, [_vp, _vp, _vp, _i64, _mp, _vp, _vp, _i32, _f32, _vp, _vp, _vp,
+                                            _vp, _sz, _vp]),
+    "qlora_vocab_workspace_bytes": (_sz, [_i32, _i64, _i64, _i32]),
+    "qlora_token_logprobs": (ctypes.c_int, [_lp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "qlora_token_logprobs_bwd": (ctypes.c_int, [_lp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp]),
+    "qlora_distill_fwd": (ctypes.c_int, [_lp, _tp, _vp, _vp, _vp, _sz, _vp]),
+    "qlora_distill_bwd": (ctypes.c_int, [_lp, _tp, _vp, _vp, _vp, _i64, _vp]),
+    "qlora_distill": (ctypes.c_int, [_lp, _tp, _vp, _vp, _vp, _vp, _i64, _vp, _sz, _vp]),
     "qlora_dropout_mask": (ctypes.c_int, [_vp, _i64, _i64, _f32, ctypes.c_uint64, _vp, _vp, _vp]),
     "qlora_dropout_apply": (ctypes.c_int, [_vp, _i64, _i64, _vp, _vp, _vp]),
     "qlora_nf4_matmul_dx_dropout": (ctypes.c_int, [_vp, _i64, _wp, _vp, _vp, _i32, _vp, _vp, _vp]),

@@ -8,17 +8,12 @@
 #include <mutex>
 
 #include "../../include/qlora.h"
+#include "capi_util.h"
 #include "launch.h"
 
 using namespace qlora;
 
 namespace {
-
-constexpr int64_t kMaxElems = (int64_t{1} << 31) - 1;  // kernels index rows * cols in int32 where safe
-
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 int check_weight(const qlora_nf4_weight *w) {
   if (!w) return QLORA_ERR_INVALID_ARG;
@@ -43,9 +38,6 @@ int check_linear_shape(int64_t M, const qlora_nf4_weight *w, int32_t r, float sc
   return QLORA_OK;
 }
 
-bool bf16_ok(const void *p) { return p && aligned(p, 16); }
-bool bf16_opt(const void *p) { return !p || aligned(p, 16); }
-
 // Shape rules of the products from a dequantized weight Wd [N, K]: those of
 // the fused kernels, and N % 64 == 0 for dX (its contraction over N has no
 // zero-padded tail on this route).
@@ -57,17 +49,11 @@ int check_deq_shape(int64_t M, const uint16_t *Wd, int64_t N, int64_t K, int32_t
   if (M > 0 && (M > kMaxElems / std::max(N, K))) return QLORA_ERR_UNSUPPORTED_SHAPE;
   return QLORA_OK;
 }
-// A tensor with M rows: at M = 0 it has no storage and its pointer may be NULL.
-bool rows_ok(const void *p, int64_t M) { return M == 0 ? bf16_opt(p) : bf16_ok(p); }
 
 NF4View view_of(const qlora_nf4_weight *w) {
   return NF4View{w->packed, w->code8, w->c2, w->mean, static_cast<int>(w->rows), static_cast<int>(w->cols),
                  static_cast<int>(w->qtype)};
 }
-
-int from_hip(hipError_t e) { return e == hipSuccess ? QLORA_OK : QLORA_ERR_HIP; }
-
-size_t bf16_bytes(int64_t n) { return round_up(static_cast<size_t>(n) * 2, 256); }
 
 // Workspace of the forward pass.  M <= small_m_max(): the fp32 partials of
 // the down-projection (always needed), and where the streaming path applies
@@ -81,23 +67,6 @@ size_t fwd_ws(int64_t M, int64_t N, int64_t K, int32_t r) {
     return b;
   }
   return bf16_bytes(M * r);
-}
-
-// Workspace of the backward pass: T (recompute) | G | dA partials | dB partials.
-struct BwdWs {
-  size_t t, g, bt, pa, pb, total;
-};
-// Workspace of the backward pass: T (recompute) | G | B^T | dA partials | dB partials.
-BwdWs bwd_ws(int64_t M, int64_t N, int64_t K, int32_t r) {
-  BwdWs w;
-  w.t = bf16_bytes(M * r);
-  w.g = bf16_bytes(M * r);
-  w.bt = lora_grad_in_ws_bytes(static_cast<int>(N), r);
-  const int m = static_cast<int>(M), n = static_cast<int>(N), k = static_cast<int>(K);
-  w.pa = round_up(lora_grad_pair_ws_bytes(m, k, k, n, r), 256);
-  w.pb = round_up(lora_grad_pair_ws_bytes(m, n, k, n, r), 256);
-  w.total = w.t + w.g + w.bt + w.pa + w.pb;
-  return w;
 }
 
 }  // namespace

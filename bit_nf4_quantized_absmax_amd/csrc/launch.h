@@ -221,4 +221,53 @@ size_t lora_grad_pair_ws_bytes(int M, int D, int K, int N, int r);
 hipError_t launch_lora_grad_w(const uint16_t *P, const uint16_t *Q, int M, int D, int r, bool out_r_major,
                               uint16_t *out, void *ws, hipStream_t s);
 
+// ---- MX4 arrays: codec -----------------------------------------------------------
+// codes [rows][Kp / 2], scales [Kp / 256][rows][8], Kp = cols filled up to a
+// multiple of 256; cols % 32 == 0.
+struct Mx4View {
+  uint8_t *codes;
+  uint8_t *scales;
+  int64_t rows;
+  int64_t cols;
+};
+inline int64_t mx4_slabs(int64_t cols) { return (cols + 255) / 256; }
+hipError_t launch_mx4_quantize(const void *X, int in_type, const Mx4View &a, hipStream_t s);
+hipError_t launch_mx4_dequantize(const Mx4View &a, uint16_t *out, hipStream_t s);
+
+// ---- MX4 products: Y [M, N] = X W^T + T B^T (T, B null at r = 0) -------------------
+// 256 x 256 or 128 x 128 tiles, any M and N.
+hipError_t launch_mx4_matmul(const Mx4View &X, const Mx4View &W, const uint16_t *T, const uint16_t *B, int r,
+                             uint16_t *Y, hipStream_t s);
+
+// ---- losses over the vocabulary -----------------------------------------------------
+// Logits Z [M, V] with row pitch ld, of type 0 fp32, 1 bf16, 2 fp16.
+struct Logits {
+  const void *z;
+  int type;
+  int64_t M;
+  int64_t V;
+  int64_t ld;
+};
+constexpr int kTopMax = 64;        // alternatives of a token
+constexpr int kDistillMax = 256;   // teacher logits of a token
+size_t vocab_ws_bytes(int64_t M, int64_t V, int type, int top);
+hipError_t launch_token_logprobs(const Logits &l, const int64_t *target, int top, float *logprob, float *entropy,
+                                 float *lse, float *top_logprob, int64_t *top_index, void *ws, hipStream_t s);
+hipError_t launch_token_logprobs_bwd(const Logits &l, const int64_t *target, const float *lse, const float *entropy,
+                                     const float *g_logprob, const float *g_entropy, void *dz, int64_t ldd,
+                                     hipStream_t s);
+// The teacher's list: idx, val [M, K] (an index outside [0, V) is no entry).
+struct Teacher {
+  const int64_t *idx;
+  const float *val;
+  int K;
+  float temperature;
+};
+hipError_t launch_distill_fwd(const Logits &l, const Teacher &t, float *loss, float *lse, void *ws, hipStream_t s);
+hipError_t launch_distill_bwd(const Logits &l, const Teacher &t, const float *lse, const float *weight, void *dz,
+                              int64_t ldd, hipStream_t s);
+// Loss and gradient at once; rows up to distill_fused_max(type) words are read once.
+hipError_t launch_distill(const Logits &l, const Teacher &t, const float *weight, float *loss, float *lse, void *dz,
+                          int64_t ldd, void *ws, hipStream_t s);
+
 }  // namespace qlora

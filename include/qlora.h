@@ -507,6 +507,147 @@ int qlora_linear_bwd_dropout(const uint16_t *dY, const uint16_t *X, const uint16
                              float p, const uint32_t *keep, uint16_t *dX, uint16_t *dA, uint16_t *dB, void *ws,
                              size_t ws_bytes, void *stream);
 
+/* ---- MX4: microscaled 4-bit floating point ----------------------------------
+ * A fourth 4-bit form of a frozen weight beside NF4 and its comparison tables
+ * (automatone.win, "QLoRA paper explained", 4-bit NormalFloat; Results, FP4 vs
+ * NF4), the one gfx950's matrix instructions multiply directly: nothing is
+ * expanded, so the activations are rounded to it as well.  Blocks of 32
+ * consecutive elements of a row share a scale 2^s, held as the byte s + 127,
+ * and hold E2M1 codes (bit 3 the sign; magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6):
+ *   s    = max(floor(log2(max |x|)) - 2, -127)
+ *   code = x / 2^s to the nearest level, ties to the even code, clipped to 6
+ * A block with a NaN or an infinity gets the byte 255 and zero codes; all its
+ * elements are then NaN.  4.25 bits an element. */
+
+/* An MX4 array [rows, cols], cols % 32 == 0.  Rows are filled up to Kp, the
+ * next multiple of 256, with zero codes and zero scale bytes:
+ *   codes   [rows][Kp / 2]       element 2j in the low half of byte j, 2j + 1 in the high half
+ *   scales  [Kp / 256][rows][8]  the scale bytes of the 8 blocks of a 256-wide slab of a row
+ * both 16-byte aligned.  rows may be 0 (no tokens) except for a weight.  A
+ * user who fills an array by other means writes the fill too: the product
+ * reads it. */
+typedef struct {
+  uint8_t *codes;
+  uint8_t *scales;
+  int64_t rows;
+  int64_t cols;
+} qlora_mx4_array;
+
+/* Storage sizes of an array; any output pointer may be NULL.  Host-only. */
+int qlora_mx4_sizes(int64_t rows, int64_t cols, int64_t *code_bytes, int64_t *scale_bytes);
+
+/* X [out->rows, out->cols] (in_type 0: fp32, else QLORA_IN_BF16 or
+ * QLORA_IN_FP16) into *out, fill included.  Exact in the rules above. */
+int qlora_mx4_quantize(const void *X, int32_t in_type, const qlora_mx4_array *out, void *stream);
+
+/* The values of *a as bf16 [rows, cols]: exact (a level has two significant bits). */
+int qlora_mx4_dequantize(const qlora_mx4_array *a, uint16_t *out_bf16, void *stream);
+
+/* Y [M, N] = X W^T + T B^T from two MX4 arrays X [M, K] and W [N, K] and,
+ * with r > 0, T [M, r] and B [N, r] in bf16 (r = 0: T and B unused).
+ * Products are exact, sums fp32, Y rounded once to bf16.  Any M >= 0 and
+ * N >= 1, 0 <= r <= 128.  A NaN block makes the sums it enters NaN. */
+int qlora_mx4_matmul(const qlora_mx4_array *X, const qlora_mx4_array *W, const uint16_t *T, const uint16_t *B, int32_t r,
+                     uint16_t *Y, void *stream);
+
+/* Workspace bytes of the two passes below (0 at M = 0 or for an unsupported shape). */
+size_t qlora_mx4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t r, int is_bwd);
+
+/* qlora_linear_fwd on an MX4 weight W [N, K]:
+ *   Y [M, N] = Q(X) W^T + T B^T,   T = scale X A^T
+ * X [M, K] bf16 is rounded to MX4 (Q) for the frozen product; the LoRA branch
+ * reads it as it is.  r = 0: no LoRA pair (A, B and T_out unused).  T_out
+ * (nullable) receives T.  K % 32 == 0, any N; M * max(N, K) < 2^31 with a
+ * LoRA pair. */
+int qlora_mx4_linear_fwd(const uint16_t *X, int64_t M, const qlora_mx4_array *W, const uint16_t *A, const uint16_t *B,
+                         int32_t r, float scale, uint16_t *Y, uint16_t *T_out, void *ws, size_t ws_bytes, void *stream);
+
+/* qlora_linear_bwd on an MX4 weight: dX = dY W + G A, dA = G^T X, dB = dY^T T,
+ * G = scale dY B.  The rounding of X passes its gradient straight through,
+ * and dA reads the unrounded X, which the LoRA branch read.  dX multiplies
+ * W's bf16 values (expanded into the workspace).  r >= 1, K % 64 == 0,
+ * N % 8 == 0 and, for dX, N % 64 == 0; outputs and T nullable as there. */
+int qlora_mx4_linear_bwd(const uint16_t *dY, const uint16_t *X, const uint16_t *T, int64_t M, const qlora_mx4_array *W,
+                         const uint16_t *A, const uint16_t *B, int32_t r, float scale, uint16_t *dX, uint16_t *dA,
+                         uint16_t *dB, void *ws, size_t ws_bytes, void *stream);
+
+/* ---- Losses over the vocabulary ------------------------------------------------
+ * What a tuned model's last linear (its output head) is trained and scored
+ * by; dz below is the dY of that linear's backward pass.  (The pages tune on
+ * instruction data and compare models by their answers: automatone.win,
+ * "QLoRA paper explained", Results.)
+ *
+ * A row of logits z has p = softmax(z).  A word that is masked out is -inf.
+ * In a row that is all -inf: log probabilities -inf, entropy 0, gradients 0.
+ * A NaN or +inf makes its row's numbers NaN (the alternatives' indices stay
+ * inside the row).  Sums are fp32 over at most 16384 words, joined in 64
+ * bits; gradients are rounded once to the logits' type. */
+
+/* Logits [rows, words] of `type` (0: fp32, else QLORA_IN_BF16 or
+ * QLORA_IN_FP16), row m at z + m * pitch elements (pitch >= words: padded
+ * vocabularies, columns of a larger matrix).  z needs only its element's
+ * alignment; rows that start on 16 bytes are fastest. */
+typedef struct {
+  const void *z;
+  int32_t type;
+  int64_t rows;
+  int64_t words;
+  int64_t pitch;
+} qlora_logits;
+
+/* Workspace bytes of the calls below that take one (top: 0 for the distillation). */
+size_t qlora_vocab_workspace_bytes(int32_t type, int64_t rows, int64_t words, int32_t top);
+
+/* Per row m, with lse = log sum_j e^z_j:
+ *   logprob [rows]  z_t - lse of the word t = target[m]; 0 if t is outside
+ *                   [0, words) (a position without a target, such as -100)
+ *   entropy [rows]  -sum_j p_j log p_j
+ *   lse     [rows][2]  the pair (max z, log sum_j e^(z_j - max z)), whose sum
+ *                   it is (at logits of large size the sum would lose the second)
+ *   top_logprob, top_index [rows, top]  the `top` most likely words in
+ *                   falling order, the lower index first among equal logits
+ * 0 <= top <= min(64, words) (else UNSUPPORTED_SHAPE; top = 0: both unused). */
+int qlora_token_logprobs(const qlora_logits *l, const int64_t *target, int32_t top, float *logprob, float *entropy,
+                         float *lse, float *top_logprob, int64_t *top_index, void *ws, size_t ws_bytes, void *stream);
+
+/* dz_j = g_logprob ([j = t] - p_j) - g_entropy p_j (log p_j + entropy) from
+ * that call's lse and entropy; either gradient [rows] may be NULL (0).  A
+ * row without a target takes no g_logprob.  dz has the logits' type and its
+ * own pitch; dz == z with the same pitch is allowed. */
+int qlora_token_logprobs_bwd(const qlora_logits *l, const int64_t *target, const float *lse, const float *entropy,
+                             const float *g_logprob, const float *g_entropy, void *dz, int64_t dz_pitch, void *stream);
+
+/* A teacher's most likely words: index, logit [rows, count], 1 <= count <=
+ * 256.  An index outside [0, words) is no entry (short lists); an index that
+ * is listed twice counts twice.  temperature > 0 divides both sides' logits. */
+typedef struct {
+  const int64_t *index;
+  const float *logit;
+  int32_t count;
+  float temperature;
+} qlora_teacher;
+
+/* Distillation from the teacher's top logits.  Per row, with q = softmax(logit
+ * / temperature) over the listed words and p = softmax(z / temperature) over
+ * all words:
+ *   loss [rows] = sum_i q_i (log q_i - log p_index(i))
+ *   lse  [rows][2] = (max z, log sum_j e^((z_j - max z) / temperature))
+ * A row without entries has loss 0 and gradient 0; a listed word of p = 0
+ * and q > 0 makes the loss +inf. */
+int qlora_distill_fwd(const qlora_logits *l, const qlora_teacher *t, float *loss, float *lse, void *ws, size_t ws_bytes,
+                      void *stream);
+
+/* dz_j = weight (p_j - sum of the q_i listed for j) / temperature from that
+ * call's lse; weight [rows] (NULL: 1) is the gradient of the loss.  dz as in
+ * qlora_token_logprobs_bwd. */
+int qlora_distill_bwd(const qlora_logits *l, const qlora_teacher *t, const float *lse, const float *weight, void *dz,
+                      int64_t dz_pitch, void *stream);
+
+/* Both at once, for a training step whose loss is sum weight * loss: the
+ * logits are read once where a row fits a workgroup's registers. */
+int qlora_distill(const qlora_logits *l, const qlora_teacher *t, const float *weight, float *loss, float *lse, void *dz,
+                  int64_t dz_pitch, void *ws, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -19,6 +19,8 @@ Sources (web pages on QLoRA, arXiv 2305.14314):
 Modules:
   nf4     -- NF4 levels, the 8-bit constant table, quantize / dequantize.
   linear  -- forward and backward of Y = X deq(W)^T + s (X A^T) B^T in fp64.
+  mx4     -- MX4 (blocks of 32 E2M1 codes under a power-of-two scale): quantize / values.
+  vocab   -- log probabilities, entropy and top-logit distillation, with gradients, in fp64.
   bf16    -- fp32 -> bf16 round-to-nearest-even and bf16 -> fp64 decoding.
 
 Every function is pinned by tests under ``tests/test_oracle_*.py`` against
