@@ -45,7 +45,7 @@ int check_teacher(const qlora_teacher *t, int64_t M) {
 Logits view_of(const qlora_logits *l) { return Logits{l->z, l->type, l->rows, l->words, l->pitch}; }
 Teacher view_of(const qlora_teacher *t) { return Teacher{t->index, t->logit, t->count, t->temperature}; }
 
-bool ws_ok(const void *ws, size_t have, size_t need) { return ws && aligned(ws, 16) && have >= need; }
+bool ws_ok(const void *ws, size_t have, size_t need) { return need == 0 || (ws && aligned(ws, 16) && have >= need); }
 
 }  // namespace
 

@@ -37,6 +37,9 @@ class MX4Tensor:
         slabs = (self.cols + 255) // 256
         _need(self.codes, torch.uint8, "codes", (self.rows, 128 * slabs))
         _need(self.scales, torch.uint8, "scales", (slabs, self.rows, 8))
+        return self._unchecked()
+
+    def _unchecked(self):
         return MX4ArrayStruct(self.codes.data_ptr(), self.scales.data_ptr(), self.rows, self.cols)
 
     @classmethod
@@ -55,9 +58,11 @@ class MX4Tensor:
         rows, cols = _mat(X, "X", X.dtype)
         if out is None:
             out = cls.empty(rows, cols, X.device)
-        elif out.shape != (rows, cols):
-            raise ValueError("out has shape %s, expected %s" % (out.shape, (rows, cols)))
-        st = out.struct()
+            st = out._unchecked()
+        else:
+            if out.shape != (rows, cols):
+                raise ValueError("out has shape %s, expected %s" % (out.shape, (rows, cols)))
+            st = out.struct()
         check(lib().qlora_mx4_quantize(_ptr(X), in_type, ctypes.byref(st), _stream(X)), "qlora_mx4_quantize")
         return out
 

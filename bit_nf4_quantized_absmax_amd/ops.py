@@ -20,11 +20,12 @@ from ._capi import DeqMatmulFwdDescStruct, LoraGradsDescStruct, MatmulFwdDescStr
 
 
 def _stream(t):
-    return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+    # the handle of torch.cuda.current_stream(t.device), without the Stream object (0.2 us a call instead of 2.2)
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _ptr(t):
-    return ctypes.c_void_p(t.data_ptr()) if t is not None else ctypes.c_void_p(0)
+    return t.data_ptr() if t is not None else None
 
 
 def _need(t, dtype, name, shape=None):
@@ -36,7 +37,7 @@ def _need(t, dtype, name, shape=None):
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
 
 

@@ -595,7 +595,8 @@ typedef struct {
   int64_t pitch;
 } qlora_logits;
 
-/* Workspace bytes of the calls below that take one (top: 0 for the distillation). */
+/* Workspace bytes of the calls below that take one (top: 0 for the
+ * distillation); 0 where a row is finished by one workgroup, and ws may then be NULL. */
 size_t qlora_vocab_workspace_bytes(int32_t type, int64_t rows, int64_t words, int32_t top);
 
 /* Per row m, with lse = log sum_j e^z_j:

@@ -322,7 +322,7 @@ def test_refusals():
         with pytest.raises(ValueError):
             q.token_logprobs(z, t, top)
     with pytest.raises(ValueError):
-        q.token_logprobs(z, t, workspace=torch.empty(4, dtype=torch.uint8, device=DEV))
+        q.token_logprobs(torch.zeros(4, 200000, device=DEV), t, workspace=torch.empty(4, dtype=torch.uint8, device=DEV))
     with pytest.raises(ValueError):
         q.token_logprobs_bwd(z, t, torch.zeros(4, device=DEV), torch.zeros(4, device=DEV))
     with pytest.raises(ValueError):
