@@ -11,10 +11,12 @@ using namespace qlora;
 
 namespace {
 
+constexpr int64_t kMaxCols = int64_t{1} << 24;   // 256 rows of codes stay within 32-bit offsets
+
 // Rows and columns of an MX4 array; rows = 0 (no tokens) only where allowed.
 int check_mx4_shape(int64_t rows, int64_t cols, bool empty_ok) {
   if (rows < (empty_ok ? 0 : 1) || cols < 1) return QLORA_ERR_INVALID_ARG;
-  if (cols % 32 != 0 || rows > kMaxElems || cols > kMaxElems - 256) return QLORA_ERR_UNSUPPORTED_SHAPE;
+  if (cols % 32 != 0 || rows > kMaxElems || cols > kMaxCols) return QLORA_ERR_UNSUPPORTED_SHAPE;
   if ((rows + 7) / 8 > kMaxElems / mx4_slabs(cols)) return QLORA_ERR_UNSUPPORTED_SHAPE;   // the codec's grid
   return QLORA_OK;
 }
@@ -46,13 +48,14 @@ int check_shape(int64_t M, int64_t N, int64_t K, int32_t r, bool bwd) {
   return QLORA_OK;
 }
 
-// Workspace of the forward pass: T (when the caller keeps none) | X's codes | X's scales.
+// Workspace of the forward pass: T (when the caller keeps none; at few tokens
+// its partial sums) | X's codes | X's scales.
 struct FwdWs {
   size_t t, codes, total;
 };
 FwdWs fwd_ws(int64_t M, int64_t K, int32_t r) {
   FwdWs w;
-  w.t = bf16_bytes(M * r);
+  w.t = mx4_small_ok(M) ? round_up(mx4_small_ws_bytes(M, K, r), 256) : bf16_bytes(M * r);
   w.codes = round_up(code_bytes(M, K), 256);
   w.total = w.t + w.codes + round_up(scale_bytes(M, K), 256);
   return w;
@@ -96,6 +99,8 @@ int qlora_mx4_matmul(const qlora_mx4_array *X, const qlora_mx4_array *W, const u
   if (st) return st;
   if (!rows_ok(Y, X->rows) || (r > 0 && (!rows_ok(T, X->rows) || !bf16_ok(B)))) return QLORA_ERR_INVALID_ARG;
   if (X->rows == 0) return QLORA_OK;
+  if (mx4_small_ok(X->rows))
+    return from_hip(launch_mx4_small_matmul(view_of(X), view_of(W), T, B, r, Y, static_cast<hipStream_t>(stream)));
   return from_hip(launch_mx4_matmul(view_of(X), view_of(W), T, B, r, Y, static_cast<hipStream_t>(stream)));
 }
 
@@ -117,8 +122,11 @@ int qlora_mx4_linear_fwd(const uint16_t *X, int64_t M, const qlora_mx4_array *W,
   if (!ws || !aligned(ws, 16) || ws_bytes < L.total) return QLORA_ERR_WORKSPACE;
   hipStream_t s = static_cast<hipStream_t>(stream);
   uint8_t *base = static_cast<uint8_t *>(ws);
-  uint16_t *T = r > 0 && T_out ? T_out : reinterpret_cast<uint16_t *>(base);
   const Mx4View x{base + L.t, base + L.t + L.codes, M, W->cols};
+  if (mx4_small_ok(M))
+    return from_hip(launch_mx4_small_linear(X, view_of(W), A, B, r, scale, Y, r > 0 ? T_out : nullptr,
+                                            reinterpret_cast<float *>(base), x, s));
+  uint16_t *T = r > 0 && T_out ? T_out : reinterpret_cast<uint16_t *>(base);
   if (r > 0 && launch_lora_down(X, static_cast<int>(M), static_cast<int>(W->cols), A, r, scale, T, s) != hipSuccess)
     return QLORA_ERR_HIP;
   if (launch_mx4_quantize(X, QLORA_IN_BF16, x, s) != hipSuccess) return QLORA_ERR_HIP;

@@ -239,6 +239,16 @@ hipError_t launch_mx4_dequantize(const Mx4View &a, uint16_t *out, hipStream_t s)
 hipError_t launch_mx4_matmul(const Mx4View &X, const Mx4View &W, const uint16_t *T, const uint16_t *B, int r,
                              uint16_t *Y, hipStream_t s);
 
+// M <= kMx4SmallMax.  P: mx4_small_ws_bytes(M, K, r), the LoRA partial sums;
+// Xq: storage for X in MX4 (written from 17 tokens on).
+constexpr int64_t kMx4SmallMax = 64;
+bool mx4_small_ok(int64_t M);
+size_t mx4_small_ws_bytes(int64_t M, int64_t K, int r);
+hipError_t launch_mx4_small_matmul(const Mx4View &X, const Mx4View &W, const uint16_t *T, const uint16_t *B, int r,
+                                   uint16_t *Y, hipStream_t s);
+hipError_t launch_mx4_small_linear(const uint16_t *X, const Mx4View &W, const uint16_t *A, const uint16_t *B, int r,
+                                   float scale, uint16_t *Y, uint16_t *Tout, float *P, const Mx4View &Xq, hipStream_t s);
+
 // ---- losses over the vocabulary -----------------------------------------------------
 // Logits Z [M, V] with row pitch ld, of type 0 fp32, 1 bf16, 2 fp16.
 struct Logits {

@@ -15,8 +15,20 @@
 //  * Scales: 8 bytes a row and step.  A lane shifts its row's words by 8 (l /
 //    32) bits; bytes 0 and 2 of the first word are then its blocks' scales in
 //    sub-steps 0 and 1, of the second in 2 and 3, picked by the instruction.
+//  * Operands of sub-step s + 1 are read while sub-step s multiplies; part of
+//    a step's last products run after its barrier, over the first reads of
+//    the next step.
 //  * The LoRA term is one (r <= 64) or two more steps on bf16 MFMA into the
-//    same accumulators.
+//    same accumulators.  At r = 64 its rows are as long as a slab's, and the
+//    step is one more of the DMA pipeline.
+//  * A workgroup takes tiles until none is left; the last step of a tile
+//    already fetches the first of the next, and the tile is stored over it.
+//    W is the matrix instruction's left operand, so that a lane's
+//    accumulators run along a row of Y: two half-wave swaps make 16-byte
+//    stores of them, without a pass through LDS.
+#include <algorithm>
+#include <type_traits>
+
 #include "common.h"
 #include "launch.h"
 #include "lds_dma.h"
@@ -30,7 +42,9 @@ typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 
 constexpr int kMxMmThreads = 512;
-constexpr int kMxBand = 4;   // tile rows of a band (see tile_of)
+constexpr int kMxBand = 4;   // tile rows of a band (see Tiles)
+constexpr int kCUs = 256;
+constexpr int kXcds = 8;
 
 struct Mx4Args {
   const uint8_t *xc, *xs, *wc, *ws;
@@ -41,61 +55,86 @@ struct Mx4Args {
   int trows, tcols;
 };
 
-// 4 bytes a lane, global -> LDS (see dma16).
-__device__ __forceinline__ void dma4(const void *src, uint32_t dst) {
-  asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(src), "{m0}"(dst) : "memory");
-}
+// The tiles of a workgroup.  Workgroups go to the 8 XCDs in turn; each XCD has
+// a run of consecutive tiles and its workgroups take them in turn (as many
+// tiles as workgroups: one each).  Tiles are numbered in bands of kMxBand tile
+// rows, column by column, so that the tiles an XCD has in work share rows of
+// X and of W in its L2.
+struct Tiles {
+  int next, end, step;
+  __device__ __forceinline__ explicit Tiles(int tiles) {
+    const int x = blockIdx.x % kXcds, each = tiles / kXcds, over = tiles % kXcds;
+    const int begin = x * each + min(x, over);
+    next = begin + blockIdx.x / kXcds;
+    end = begin + each + (x < over ? 1 : 0);
+    step = (gridDim.x - x + kXcds - 1) / kXcds;   // workgroups of this XCD
+  }
+  __device__ __forceinline__ static void place(const Mx4Args &a, int id, int bm, int bn, int &m0, int &n0) {
+    const int band = id / (kMxBand * a.tcols);
+    const int h = min(kMxBand, a.trows - band * kMxBand);
+    const int j = id - band * kMxBand * a.tcols;
+    n0 = j / h * bn;
+    m0 = (band * kMxBand + j % h) * bm;
+  }
+};
 
-// Consecutive workgroups go to the 8 XCDs in turn; consecutive tiles are
-// given to one XCD, in bands of kMxBand tile rows, column by column, so that
-// the tiles an XCD runs together share rows of X and of W in its L2.
-__device__ __forceinline__ void tile_of(const Mx4Args &a, int &tr, int &tc) {
-  int id = blockIdx.x;
-  const int nt = gridDim.x;
-  if ((nt & 7) == 0) id = (blockIdx.x & 7) * (nt >> 3) + (blockIdx.x >> 3);
-  const int band = id / (kMxBand * a.tcols);
-  const int h = min(kMxBand, a.trows - band * kMxBand);
-  const int j = id - band * kMxBand * a.tcols;
-  tc = j / h;
-  tr = band * kMxBand + j % h;
-}
-
-// Codes of rows row0 .. row0 + kRows - 1 (past the last: that row again, its
-// results are not stored) of one slab into a swizzled stage.
+// kRows rows of 128 bytes, `pitch` apart, from src (the tile's first) into a
+// swizzled stage at LDS address `stage`; rows past `last` repeat it (their
+// results are not stored).
 template <int kRows>
-__device__ __forceinline__ void dma_codes(uint8_t *stage, const uint8_t *codes, int64_t pitch, int row0, int rows, int kt,
-                                          int wave, int lane) {
+__device__ __forceinline__ void dma_rows(uint32_t stage, const uint8_t *src, uint32_t pitch, int last, int wave, int lane) {
 #pragma unroll
   for (int j = 0; j < kRows / 64; ++j) {
     const int u = wave * (kRows / 64) + j;
     const int row = u * 8 + (lane >> 3);
     const int chunk = (lane & 7) ^ ((row & 7) ^ ((row >> 3) & 1));
-    const uint32_t dst = __builtin_amdgcn_readfirstlane(lds_addr(stage) + u * 1024);
-    dma16(codes + static_cast<int64_t>(min(row0 + row, rows - 1)) * pitch + kt * 128 + chunk * 16, dst);
+    dma16(src, static_cast<uint32_t>(min(row, last)) * pitch + chunk * 16,
+          __builtin_amdgcn_readfirstlane(stage + u * 1024));
   }
 }
 
-// Their scales: 8 bytes a row, 32 rows a wave instruction.
-__device__ __forceinline__ void dma_scales(uint8_t *stage, const uint8_t *scales, int row0, int rows, int kt, int u,
-                                           int lane) {
-  const int row = min(row0 + 32 * u + (lane >> 1), rows - 1);
-  const uint32_t dst = __builtin_amdgcn_readfirstlane(lds_addr(stage) + u * 256);
-  dma4(scales + (static_cast<int64_t>(kt) * rows + row) * 8 + 4 * (lane & 1), dst);
+// Scales of rows 32 u .. 32 u + 31: 8 bytes a row.
+__device__ __forceinline__ void dma_scales(uint32_t stage, const uint8_t *src, int last, int u, int lane) {
+  dma4(src, min(32 * u + (lane >> 1), last) * 8 + 4 * (lane & 1), __builtin_amdgcn_readfirstlane(stage + u * 256));
 }
 
 __device__ __forceinline__ i32x8_t widen(i32x4_t v) { return __builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1); }
 
-// One 32 x 32 x 64 product; s: sub-step (its scale byte), sa, sb: the words.
+// One 32 x 32 x 64 product under the scales in byte kByte of sa and sb.
 template <int kByte>
 __device__ __forceinline__ f32x16_t mfma4(i32x4_t a, i32x4_t b, f32x16_t c, uint32_t sa, uint32_t sb) {
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(widen(a), widen(b), c, 4, 4, kByte, static_cast<int>(sa), kByte,
                                                          static_cast<int>(sb));
 }
 
+// Operands of a sub-step (a: X or T rows, b: W or B rows) and a step's scales.
+template <int kFM, int kFN>
+struct Ops {
+  i32x4_t a[kFM], b[kFN];
+};
 template <int kFM, int kFN>
 struct Scales {
   uint2 a[kFM], b[kFN];
 };
+
+// Product of one pair of fragments in sub-step s under scale words sa, sb.
+template <bool kLora>
+__device__ __forceinline__ f32x16_t mul1(i32x4_t a, i32x4_t b, uint32_t sa, uint32_t sb, int s, f32x16_t acc) {
+  if constexpr (kLora)
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, b), __builtin_bit_cast(bf16x8_t, a), acc, 0, 0,
+                                                   0);
+  return (s & 1) ? mfma4<2>(b, a, acc, sb, sa) : mfma4<0>(b, a, acc, sb, sa);
+}
+
+// Products of row fragments i0 .. i1 - 1 of sub-step s.
+template <int i0, int i1, bool kLora, int kFM, int kFN>
+__device__ __forceinline__ void mul(const Ops<kFM, kFN> &o, const Scales<kFM, kFN> &sc, int s, f32x16_t (&acc)[kFM][kFN]) {
+#pragma unroll
+  for (int i = i0; i < i1; ++i)
+#pragma unroll
+    for (int j = 0; j < kFN; ++j)
+      acc[i][j] = mul1<kLora>(o.a[i], o.b[j], s < 2 ? sc.a[i].x : sc.a[i].y, s < 2 ? sc.b[j].x : sc.b[j].y, s, acc[i][j]);
+}
 
 // Narrow bf16 [rows, r] (T or B), columns j0 .. j0 + 63, into a 128-byte-row
 // stage of kRows rows; zero past r and past `rows`.
@@ -120,148 +159,228 @@ __device__ __forceinline__ void stage_narrow(uint8_t *stage, const uint16_t *src
   }
 }
 
+// Swaps the upper half-wave of a with the lower one of b.
+__device__ __forceinline__ void swap_halves(uint32_t &a, uint32_t &b) {
+  typedef unsigned int pair_t __attribute__((ext_vector_type(2)));
+  const pair_t r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+
+typedef uint4 __attribute__((aligned(2))) uint4_any;   // rows of an odd N start anywhere
+
 }  // namespace
 
-template <int kFM, int kFN>
+// kPiped: r == 64, the LoRA step runs in the pipeline.
+template <int kFM, int kFN, bool kPiped>
 __global__ __launch_bounds__(kMxMmThreads) void k_mx4_matmul(const Mx4Args args) {
   constexpr int kBM = 64 * kFM, kBN = 128 * kFN;
-  __shared__ __attribute__((aligned(16))) uint8_t sX[2][kBM * 128];
-  __shared__ __attribute__((aligned(16))) uint8_t sW[2][kBN * 128];
-  __shared__ __attribute__((aligned(16))) uint8_t sSx[2][kBM * 8];
-  __shared__ __attribute__((aligned(16))) uint8_t sSw[2][kBN * 8];
+  constexpr int kHold = kFM / 2;                 // row fragments whose last products run after the barrier
+  // Stages: X codes | W codes (two each, a power of two apart) | scales.
+  constexpr uint32_t kStX = kBM * 128, kStW = kBN * 128, kOffW = 2 * kStX, kOffS = kOffW + 2 * kStW;
+  constexpr uint32_t kStS = (kBM + kBN) * 8;
+  static_assert((kOffW & kStX) == 0 && (kOffW & kStW) == 0 && (kOffS % kStS) == 0, "stages toggle by one bit");
+  __shared__ __attribute__((aligned(128))) uint8_t smem[kOffS + 2 * kStS];
 
-  int tr, tc;
-  tile_of(args, tr, tc);
   const int M = args.M, N = args.N, r = args.r, KT = args.KT;
-  const int64_t pitch = static_cast<int64_t>(KT) * 128;
-  const int m0 = tr * kBM, n0 = tc * kBN;
+  const int steps = KT + (kPiped ? 1 : 0);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 2, wn = wave & 3;
   const int lr = lane & 31, lh = lane >> 5;
+  const uint32_t base = lds_addr(smem);
 
-  auto dma = [&](int st, int kt) __attribute__((always_inline)) {
-    dma_codes<kBM>(sX[st], args.xc, pitch, m0, M, kt, wave, lane);
-    dma_codes<kBN>(sW[st], args.wc, pitch, n0, N, kt, wave, lane);
+  Tiles tiles(args.trows * args.tcols);
+  if (tiles.next >= tiles.end) return;   // the whole workgroup
+
+  auto dma = [&](uint32_t st, int m0, int n0, int kt) __attribute__((always_inline)) {
+    const uint32_t x = base + (st ? kStX : 0), w = base + kOffW + (st ? kStW : 0), sc = base + kOffS + (st ? kStS : 0);
+    const int lastm = M - 1 - m0, lastn = N - 1 - n0;
+    if (kPiped && kt == KT) {
+      dma_rows<kBM>(x, reinterpret_cast<const uint8_t *>(args.T) + static_cast<int64_t>(m0) * 128, 128, lastm, wave, lane);
+      dma_rows<kBN>(w, reinterpret_cast<const uint8_t *>(args.B) + static_cast<int64_t>(n0) * 128, 128, lastn, wave, lane);
+      return;
+    }
+    const uint32_t pitch = static_cast<uint32_t>(KT) * 128;
+    dma_rows<kBM>(x, args.xc + static_cast<int64_t>(m0) * pitch + kt * 128, pitch, lastm, wave, lane);
+    dma_rows<kBN>(w, args.wc + static_cast<int64_t>(n0) * pitch + kt * 128, pitch, lastn, wave, lane);
 #pragma unroll
     for (int u = wave; u < (kBM + kBN) / 32; u += 8) {
       if (u < kBM / 32)
-        dma_scales(sSx[st], args.xs, m0, M, kt, u, lane);
+        dma_scales(sc, args.xs + (static_cast<int64_t>(kt) * M + m0) * 8, lastm, u, lane);
       else
-        dma_scales(sSw[st], args.ws, n0, N, kt, u - kBM / 32, lane);
+        dma_scales(sc + kBM * 8, args.ws + (static_cast<int64_t>(kt) * N + n0) * 8, lastn, u - kBM / 32, lane);
     }
   };
-  uint32_t xo[4], wo[4];
-#pragma unroll
-  for (int s = 0; s < 4; ++s) {
-    xo[s] = static_cast<uint32_t>(swz128(32 * kFM * wm + lr, 2 * s + lh));
-    wo[s] = static_cast<uint32_t>(swz128(32 * kFN * wn + lr, 2 * s + lh));
-  }
-  f32x16_t acc[kFM][kFN];
-#pragma unroll
-  for (int i = 0; i < kFM; ++i)
-#pragma unroll
-    for (int j = 0; j < kFN; ++j)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+  // Operand reads of sub-step 0 of the current stage; fragment i adds 4096 i,
+  // sub-step s turns bits 5 and 6 (chunk 2 s + lh of the swizzled row).
+  uint32_t xo = static_cast<uint32_t>(swz128(32 * kFM * wm + lr, lh));
+  uint32_t wo = kOffW + static_cast<uint32_t>(swz128(32 * kFN * wn + lr, lh));
+  uint32_t so = kOffS + (32 * kFM * wm + lr) * 8, to = kOffS + (kBM + 32 * kFN * wn + lr) * 8;
 
-  dma(0, 0);
-  raw_barrier<wait_imm(0, 0)>();
-  for (int kt = 0; kt < KT; ++kt) {
-    const int st = kt & 1;
-    if (kt + 1 < KT) dma(st ^ 1, kt + 1);
-    Scales<kFM, kFN> sc;
+  f32x16_t acc[kFM][kFN];
+  Ops<kFM, kFN> fa, fb;
+  Scales<kFM, kFN> sc;
+  auto clear = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < kFM; ++i)
+#pragma unroll
+      for (int j = 0; j < kFN; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+    // the first step has no products held back: zeros under the smallest scale
 #pragma unroll
     for (int i = 0; i < kFM; ++i) {
-      const uint2 v = *reinterpret_cast<const uint2 *>(sSx[st] + (32 * kFM * wm + 32 * i + lr) * 8);
-      sc.a[i] = make_uint2(v.x >> (8 * lh), v.y >> (8 * lh));
+      fb.a[i] = i32x4_t{0, 0, 0, 0};
+      sc.a[i] = make_uint2(0, 0);
     }
 #pragma unroll
     for (int j = 0; j < kFN; ++j) {
-      const uint2 v = *reinterpret_cast<const uint2 *>(sSw[st] + (32 * kFN * wn + 32 * j + lr) * 8);
-      sc.b[j] = make_uint2(v.x >> (8 * lh), v.y >> (8 * lh));
+      fb.b[j] = i32x4_t{0, 0, 0, 0};
+      sc.b[j] = make_uint2(0, 0);
+    }
+  };
+  auto read = [&](Ops<kFM, kFN> &o, int s) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < kFN; ++j) o.b[j] = *reinterpret_cast<const i32x4_t *>(smem + (wo ^ (32u * s)) + 4096 * j);
+#pragma unroll
+    for (int i = 0; i < kFM; ++i) o.a[i] = *reinterpret_cast<const i32x4_t *>(smem + (xo ^ (32u * s)) + 4096 * i);
+  };
+  // One step on the current stage while the next one (of this tile or the
+  // next) is fetched into the other: fetch issues it.
+  auto step = [&](auto lora, auto fetch) __attribute__((always_inline)) {
+    constexpr bool kLora = decltype(lora)::value;
+    uint32_t ha[kHold], hb[kFN];   // scales of the products held back (sub-step 3)
+#pragma unroll
+    for (int i = 0; i < kHold; ++i) ha[i] = sc.a[kFM - kHold + i].y;
+#pragma unroll
+    for (int j = 0; j < kFN; ++j) hb[j] = sc.b[j].y;
+    read(fa, 0);
+    if constexpr (!kLora) {
+#pragma unroll
+      for (int i = 0; i < kFM; ++i) sc.a[i] = *reinterpret_cast<const uint2 *>(smem + so + 256 * i);
+#pragma unroll
+      for (int j = 0; j < kFN; ++j) sc.b[j] = *reinterpret_cast<const uint2 *>(smem + to + 256 * j);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < kHold; ++i)
+#pragma unroll
+      for (int j = 0; j < kFN; ++j) {
+        f32x16_t &c = acc[kFM - kHold + i][j];
+        c = mul1<false>(fb.a[kFM - kHold + i], fb.b[j], ha[i], hb[j], 3, c);
+      }
+    fetch();
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (!kLora) {
+#pragma unroll
+      for (int i = 0; i < kFM; ++i) sc.a[i] = make_uint2(sc.a[i].x >> (8 * lh), sc.a[i].y >> (8 * lh));
+#pragma unroll
+      for (int j = 0; j < kFN; ++j) sc.b[j] = make_uint2(sc.b[j].x >> (8 * lh), sc.b[j].y >> (8 * lh));
     }
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      i32x4_t a[kFM], b[kFN];
+      Ops<kFM, kFN> &cur = (s & 1) ? fb : fa;
+      Ops<kFM, kFN> &nxt = (s & 1) ? fa : fb;
+      mul<0, 1, kLora>(cur, sc, s, acc);
+      __builtin_amdgcn_sched_barrier(0);
+      if (s < 3) read(nxt, s + 1);
+      mul<1, kFM - kHold, kLora>(cur, sc, s, acc);
+      __builtin_amdgcn_sched_barrier(0);
+      if (s < 3) mul<kFM - kHold, kFM, kLora>(cur, sc, s, acc);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    xo ^= kStX;
+    wo ^= kStW;
+    so ^= kStS;
+    to ^= kStS;
+    raw_barrier<wait_imm(0, 0)>();
+  };
+
+  int m0, n0;
+  Tiles::place(args, tiles.next, kBM, kBN, m0, n0);
+  uint32_t st = 0;
+  dma(0, m0, n0, 0);
+  raw_barrier<wait_imm(0, 0)>();
+  for (;;) {
+    clear();
+    tiles.next += tiles.step;
+    const bool more = tiles.next < tiles.end;
+    int m1 = 0, n1 = 0;
+    if (more) Tiles::place(args, tiles.next, kBM, kBN, m1, n1);
+    auto fetch = [&](int kt) __attribute__((always_inline)) {
+      st ^= 1;
+      if (kt + 1 < steps)
+        dma(st, m0, n0, kt + 1);
+      else if (more)
+        dma(st, m1, n1, 0);
+    };
+    for (int kt = 0; kt < KT; ++kt) step(std::false_type(), [&]() __attribute__((always_inline)) { fetch(kt); });
+    if constexpr (kPiped) {
+      step(std::true_type(), [&]() __attribute__((always_inline)) { fetch(KT); });
+      mul<kFM - kHold, kFM, true>(fb, sc, 3, acc);
+    } else {
+      mul<kFM - kHold, kFM, false>(fb, sc, 3, acc);
+      // The stage just consumed takes T and B; the other one is being filled.
+      for (int j0 = 0; j0 < r; j0 += 64) {
+        stage_narrow<kBM>(smem + (st ? 0 : kStX), args.T, r, m0, M, j0);
+        stage_narrow<kBN>(smem + kOffW + (st ? 0 : kStW), args.B, r, n0, N, j0);
+        __syncthreads();
+        xo ^= kStX;
+        wo ^= kStW;
 #pragma unroll
-      for (int i = 0; i < kFM; ++i) a[i] = *reinterpret_cast<const i32x4_t *>(sX[st] + xo[s] + 4096 * i);
+        for (int s = 0; s < 4; ++s) {
+          read(fa, s);
+          mul<0, kFM, true>(fa, sc, s, acc);
+        }
+        xo ^= kStX;
+        wo ^= kStW;
+        __syncthreads();
+      }
+    }
+
+    // Accumulator layout: lane l holds row m = l % 32 of Y; element e is
+    // column 8 (e / 4) + 4 (l / 32) + e % 4.
 #pragma unroll
-      for (int j = 0; j < kFN; ++j) b[j] = *reinterpret_cast<const i32x4_t *>(sW[st] + wo[s] + 4096 * j);
+    for (int i = 0; i < kFM; ++i) {
+      const int m = m0 + 32 * (kFM * wm + i) + lr;
+      uint16_t *row = args.Y + static_cast<int64_t>(m) * N;
 #pragma unroll
-      for (int i = 0; i < kFM; ++i)
+      for (int j = 0; j < kFN; ++j)
 #pragma unroll
-        for (int j = 0; j < kFN; ++j) {
-          const uint32_t sa = s < 2 ? sc.a[i].x : sc.a[i].y, sb = s < 2 ? sc.b[j].x : sc.b[j].y;
-          acc[i][j] = (s & 1) ? mfma4<2>(a[i], b[j], acc[i][j], sa, sb) : mfma4<0>(a[i], b[j], acc[i][j], sa, sb);
+        for (int q = 0; q < 2; ++q) {
+          uint32_t p[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) p[e] = pack_bf16x2(acc[i][j][8 * q + 2 * e], acc[i][j][8 * q + 2 * e + 1]);
+          swap_halves(p[0], p[2]);
+          swap_halves(p[1], p[3]);
+          const int n = n0 + 32 * (kFN * wn + j) + 16 * q + 8 * lh;
+          if (m < M && n + 8 <= N) {
+            *reinterpret_cast<uint4_any *>(row + n) = make_uint4(p[0], p[1], p[2], p[3]);
+          } else if (m < M) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (n + e < N) row[n + e] = static_cast<uint16_t>(p[e >> 1] >> (16 * (e & 1)));
+          }
         }
     }
-    raw_barrier<wait_imm(0, 0)>();
-  }
-  for (int j0 = 0; j0 < r; j0 += 64) {
-    stage_narrow<kBM>(sX[0], args.T, r, m0, M, j0);
-    stage_narrow<kBN>(sW[0], args.B, r, n0, N, j0);
-    __syncthreads();
-#pragma unroll
-    for (int s = 0; s < 4; ++s)
-#pragma unroll
-      for (int i = 0; i < kFM; ++i)
-#pragma unroll
-        for (int j = 0; j < kFN; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-              *reinterpret_cast<const bf16x8_t *>(sX[0] + xo[s] + 4096 * i),
-              *reinterpret_cast<const bf16x8_t *>(sW[0] + wo[s] + 4096 * j), acc[i][j], 0, 0, 0);
-    __syncthreads();
-  }
-
-  // Epilogue: the wave's block as bf16 through its own part of the stages (no
-  // wave reads them any more), 16 bytes a lane to memory.  Accumulator layout:
-  // lane l holds column l % 32, element e row 8 (e / 4) + 4 (l / 32) + e % 4.
-  constexpr int kRowBytes = 64 * kFN;                  // the wave's 32 kFN columns
-  constexpr int kChunks = kRowBytes / 16;
-  uint8_t *region = &sX[0][0] + wave * (32 * kFM * kRowBytes);
-  static_assert(8 * 32 * kFM * kRowBytes <= 2 * kBM * 128 || kFM * kFN == 8, "");
-  if constexpr (kFM * kFN == 8) region = (wave < 4 ? &sX[0][0] : &sW[0][0]) + (wave & 3) * (32 * kFM * kRowBytes);
-#pragma unroll
-  for (int i = 0; i < kFM; ++i)
-#pragma unroll
-    for (int j = 0; j < kFN; ++j)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int rr = 32 * i + 8 * (e >> 2) + 4 * lh + (e & 3);
-        const int cc = 32 * j + lr;
-        *reinterpret_cast<uint16_t *>(region + rr * kRowBytes + 16 * ((cc >> 3) ^ (rr & (kChunks - 1))) + 2 * (cc & 7)) =
-            f32_to_bf16(acc[i][j][e]);
-      }
-  __builtin_amdgcn_s_waitcnt(wait_imm(63, 0));
-  const bool vec = (N & 7) == 0;
-#pragma unroll 4
-  for (int t = 0; t < 32 * kFM * kChunks / 64; ++t) {
-    const int idx = t * 64 + lane;
-    const int rr = idx / kChunks, c = idx % kChunks;
-    const uint4 v = *reinterpret_cast<const uint4 *>(region + rr * kRowBytes + 16 * (c ^ (rr & (kChunks - 1))));
-    const int gr = m0 + 32 * kFM * wm + rr, gc = n0 + 32 * kFN * wn + 8 * c;
-    if (gr >= M) continue;
-    uint16_t *p = args.Y + static_cast<int64_t>(gr) * N + gc;
-    if (vec) {
-      if (gc < N) *reinterpret_cast<uint4 *>(p) = v;
-    } else {
-      const uint32_t h[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (gc + e < N) p[e] = static_cast<uint16_t>(h[e >> 1] >> (16 * (e & 1)));
-    }
+    if (!more) return;
+    m0 = m1;
+    n0 = n1;
   }
 }
 
 namespace {
 
 template <int kFM, int kFN>
-hipError_t launch_tiles(Mx4Args a, hipStream_t s) {
+hipError_t launch_tiles(Mx4Args a, int per_cu, hipStream_t s) {
   a.trows = (a.M + 64 * kFM - 1) / (64 * kFM);
   a.tcols = (a.N + 128 * kFN - 1) / (128 * kFN);
-  hipLaunchKernelGGL((k_mx4_matmul<kFM, kFN>), dim3(static_cast<uint32_t>(a.trows) * a.tcols), dim3(kMxMmThreads), 0, s,
-                     a);
+  const dim3 grid(static_cast<uint32_t>(std::min<int64_t>(static_cast<int64_t>(a.trows) * a.tcols, kCUs * per_cu)));
+  if (a.r == 64)
+    hipLaunchKernelGGL((k_mx4_matmul<kFM, kFN, true>), grid, dim3(kMxMmThreads), 0, s, a);
+  else
+    hipLaunchKernelGGL((k_mx4_matmul<kFM, kFN, false>), grid, dim3(kMxMmThreads), 0, s, a);
   return hipGetLastError();
 }
 
@@ -283,7 +402,7 @@ hipError_t launch_mx4_matmul(const Mx4View &X, const Mx4View &W, const uint16_t 
   a.KT = static_cast<int>(mx4_slabs(X.cols));
   // The small tile where the large one leaves compute units without work.
   const int64_t large = ((X.rows + 255) / 256) * ((W.rows + 255) / 256);
-  return large >= 256 ? launch_tiles<4, 2>(a, s) : launch_tiles<2, 1>(a, s);
+  return large >= kCUs ? launch_tiles<4, 2>(a, 1, s) : launch_tiles<2, 1>(a, 2, s);
 }
 
 }  // namespace qlora

@@ -519,7 +519,7 @@ int qlora_linear_bwd_dropout(const uint16_t *dY, const uint16_t *X, const uint16
  * A block with a NaN or an infinity gets the byte 255 and zero codes; all its
  * elements are then NaN.  4.25 bits an element. */
 
-/* An MX4 array [rows, cols], cols % 32 == 0.  Rows are filled up to Kp, the
+/* An MX4 array [rows, cols], cols % 32 == 0, cols <= 2^24.  Rows are filled up to Kp, the
  * next multiple of 256, with zero codes and zero scale bytes:
  *   codes   [rows][Kp / 2]       element 2j in the low half of byte j, 2j + 1 in the high half
  *   scales  [Kp / 256][rows][8]  the scale bytes of the 8 blocks of a 256-wide slab of a row
