@@ -5,16 +5,16 @@
 // pass before the first product, and there are two launches at most.
 //
 // k_mx4_prep: partial sums P of X A^T, one workgroup per (slice of the
-//   columns, 32 adapter rows, 32 or 16 tokens); its 16 waves split the slice
-//   and are summed in LDS in wave order.  From 17 tokens on, further
-//   workgroups of the same launch round X to MX4.
-// k_mx4_small: one workgroup per 16 weight rows, its 8 waves take slabs of 256
+//   columns, 16 adapter rows, 16 tokens); its 16 waves split the slice and are
+//   summed in LDS in wave order.  Further workgroups of the same launch round
+//   X to MX4.
+// k_mx4_small: one workgroup per 16 weight rows, its waves take slabs of 256
 //   columns in turn: v_mfma_scale_f32_16x16x128 with W as the left operand
 //   (lane l: row l % 16, block l / 16 of 128 columns) and 16 tokens a product
-//   as the right one.  Up to 16 tokens a lane rounds the block of X that it
-//   supplies itself, 32 bf16 of one token: the block's maximum needs no other
-//   lane, and no third launch is made.  The waves' sums meet in LDS in wave
-//   order; T B^T is added there from the partials' sum.
+//   as the right one.  The waves' sums meet in LDS in wave order; T B^T is
+//   added there, T from the partials' sum.  Without a LoRA pair and with few
+//   workgroups a lane rounds the block of X that it supplies itself, 32 bf16
+//   of one token: the block's maximum needs no other lane.
 #include <algorithm>
 
 #include "common.h"
@@ -29,10 +29,9 @@ typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
 
 constexpr int kPrepWaves = 16;
-constexpr int kPrepRows = 32;         // adapter rows of a workgroup
-constexpr int kMainWaves = 8;
 constexpr int kMainRows = 16;         // weight rows of a workgroup
-constexpr int kFusedMax = 16;         // tokens up to which the main kernel rounds X itself
+constexpr int kFusedTokens = 16;      // see fused_ok
+constexpr int kFusedGrid = 256;
 
 struct SmallArgs {
   const uint16_t *X;                  // [M, K] bf16 (fused)
@@ -80,10 +79,11 @@ __device__ __forceinline__ uint32_t round_block(const uint32_t (&x)[16], i32x4_t
 
 }  // namespace
 
-// kMT: token tiles of 16 of a workgroup.  Workgroups from `downs` on round X.
-template <int kMT>
+// kSteps: 32-column steps of a wave, all loaded before the first product.
+// Workgroups from `downs` on round X.
+template <int kSteps>
 __global__ __launch_bounds__(kPrepWaves * 64) void k_mx4_prep(const SmallArgs a, int downs, uint8_t *xc, uint8_t *xs) {
-  __shared__ float red[kPrepWaves][2 * kMT][256];
+  __shared__ float red[kPrepWaves][256];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (static_cast<int>(blockIdx.x) >= downs) {
@@ -114,63 +114,109 @@ __global__ __launch_bounds__(kPrepWaves * 64) void k_mx4_prep(const SmallArgs a,
     xs[(static_cast<int64_t>(slab) * a.M + row) * 8 + b] = static_cast<uint8_t>(byte);
     return;
   }
-  const int jts = (a.r + kPrepRows - 1) / kPrepRows, mts = (a.M + 16 * kMT - 1) / (16 * kMT);
+  const int jts = (a.r + 15) / 16, mts = (a.M + 15) / 16;
   const int jt = blockIdx.x % jts, mt = blockIdx.x / jts % mts, s = blockIdx.x / (jts * mts);
   const int nl = lane & 15, g = lane >> 4;
-  const int per = a.slice / kPrepWaves;               // columns of a wave: 64 or 128
-  const int k0 = s * a.slice + wave * per;
-  f32x4_t acc[2][kMT];
+  const int k0 = s * a.slice + wave * (32 * kSteps);
+  const uint16_t *ar = a.A + static_cast<int64_t>(min(16 * jt + nl, a.r - 1)) * a.K;
+  const uint16_t *xr = a.X + static_cast<int64_t>(min(16 * mt + nl, a.M - 1)) * a.K;
+  bf16x8_t av[kSteps], xv[kSteps];
 #pragma unroll
-  for (int j = 0; j < 2; ++j)
-#pragma unroll
-    for (int m = 0; m < kMT; ++m) acc[j][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  const uint16_t *ar[2], *xr[kMT];
-#pragma unroll
-  for (int j = 0; j < 2; ++j) ar[j] = a.A + static_cast<int64_t>(min(kPrepRows * jt + 16 * j + nl, a.r - 1)) * a.K;
-#pragma unroll
-  for (int m = 0; m < kMT; ++m) xr[m] = a.X + static_cast<int64_t>(min(16 * (kMT * mt + m) + nl, a.M - 1)) * a.K;
-  for (int k = k0; k < min(k0 + per, a.K); k += 64) {   // K % 32 == 0: a 32-wide step is whole or absent
-    bf16x8_t av[2][2], xv[2][kMT];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int c = min(k + 32 * h, a.K - 32) + 8 * g;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) av[h][j] = *reinterpret_cast<const bf16x8_t *>(ar[j] + c);
-#pragma unroll
-      for (int m = 0; m < kMT; ++m) xv[h][m] = *reinterpret_cast<const bf16x8_t *>(xr[m] + c);
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      if (k + 32 * h < a.K) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int m = 0; m < kMT; ++m)
-            acc[j][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av[h][j], xv[h][m], acc[j][m], 0, 0, 0);
-      }
+  for (int h = 0; h < kSteps; ++h) {
+    const int c = min(k0 + 32 * h, a.K - 32) + 8 * g;   // K % 32 == 0: a step is whole or absent
+    av[h] = *reinterpret_cast<const bf16x8_t *>(ar + c);
+    xv[h] = *reinterpret_cast<const bf16x8_t *>(xr + c);
   }
-  // lane l holds adapter rows 4 (l / 16) + e of token l % 16
+  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int j = 0; j < 2; ++j)
-#pragma unroll
-    for (int m = 0; m < kMT; ++m)
-      *reinterpret_cast<f32x4_t *>(&red[wave][j * kMT + m][4 * lane]) = acc[j][m];
+  for (int h = 0; h < kSteps; ++h)
+    if (k0 + 32 * h < a.K) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av[h], xv[h], acc, 0, 0, 0);
+  *reinterpret_cast<f32x4_t *>(&red[wave][4 * lane]) = acc;   // adapter rows 4 (l / 16) + e of token l % 16
   __syncthreads();
-  for (int i = threadIdx.x; i < 2 * kMT * 256; i += kPrepWaves * 64) {
-    float v = 0.f;
+  if (threadIdx.x >= 256) return;
+  float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < kPrepWaves; ++w) v += red[w][i >> 8][i & 255];
-    const int l = (i & 255) >> 2, e = i & 3, t = i >> 8;
-    const int j = kPrepRows * jt + 16 * (t / kMT) + 4 * (l >> 4) + e, m = 16 * (kMT * mt + t % kMT) + (l & 15);
-    if (j < a.r && m < a.M) a.P[(static_cast<int64_t>(s) * a.M + m) * a.r + j] = v;
+  for (int w = 0; w < kPrepWaves; ++w) v += red[w][threadIdx.x];
+  const int l = threadIdx.x >> 2, e = threadIdx.x & 3;
+  const int j = 16 * jt + 4 * (l >> 4) + e, m = 16 * mt + (l & 15);
+  if (j < a.r && m < a.M) a.P[(static_cast<int64_t>(s) * a.M + m) * a.r + j] = v;
+}
+
+namespace {
+
+// What a wave loads for a slab.
+template <int kMB, bool kFused>
+struct Pass {
+  i32x4_t w[2];
+  uint2 wb;
+  i32x4_t x[kMB][2];       // not fused
+  uint2 xb[kMB];
+  uint32_t raw[2][16];     // fused
+};
+
+// T [M, r] as bf16 into LDS, zero up to the next 32 columns: given, or the
+// scaled sum of the partials, kPlanes slices' loads at a time.
+template <int kMB, int kThreads, int kPlanes>
+__device__ __forceinline__ void put_T(const SmallArgs &a, uint16_t (*sT)[136]) {
+  const int rp = (a.r + 31) / 32 * 32, quads = rp / 4;
+  const bool vec = (a.r & 3) == 0;
+  for (int i = threadIdx.x; i < 16 * kMB * quads; i += kThreads) {
+    const int m = i / quads, j = 4 * (i - m * quads);
+    float t[4] = {0.f, 0.f, 0.f, 0.f};
+    uint16_t v[4] = {0, 0, 0, 0};
+    if (m < a.M && j < a.r) {
+      if (a.T && (a.r & 3) == 0) {
+        const uint2 q = *reinterpret_cast<const uint2 *>(a.T + static_cast<int64_t>(m) * a.r + j);
+        v[0] = static_cast<uint16_t>(q.x);
+        v[1] = static_cast<uint16_t>(q.x >> 16);
+        v[2] = static_cast<uint16_t>(q.y);
+        v[3] = static_cast<uint16_t>(q.y >> 16);
+      } else if (a.T) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (j + e < a.r) v[e] = a.T[static_cast<int64_t>(m) * a.r + j + e];
+      } else {
+        const float *p = a.P + static_cast<int64_t>(m) * a.r + j;
+        const int64_t plane = static_cast<int64_t>(a.M) * a.r;
+        for (int s0 = 0; s0 < a.S; s0 += kPlanes) {
+          float q[kPlanes][4];
+#pragma unroll
+          for (int s = 0; s < kPlanes; ++s) {
+            const float *ps = p + plane * min(s0 + s, a.S - 1);
+            if (vec) {
+              const float4 f = *reinterpret_cast<const float4 *>(ps);
+              q[s][0] = f.x;
+              q[s][1] = f.y;
+              q[s][2] = f.z;
+              q[s][3] = f.w;
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) q[s][e] = j + e < a.r ? ps[e] : 0.f;
+            }
+          }
+#pragma unroll
+          for (int s = 0; s < kPlanes; ++s)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) t[e] += s0 + s < a.S ? q[s][e] : 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[e] = f32_to_bf16(a.scale * t[e]);
+          if (blockIdx.x == 0 && a.Tout && j + e < a.r) a.Tout[static_cast<int64_t>(m) * a.r + j + e] = v[e];
+        }
+      }
+    }
+    *reinterpret_cast<uint2 *>(&sT[m][j]) = make_uint2(v[0] | static_cast<uint32_t>(v[1]) << 16, v[2] | static_cast<uint32_t>(v[3]) << 16);
   }
 }
 
+}  // namespace
+
 // kMB: tiles of 16 tokens.  kFused: X is bf16 and rounded here (kMB == 1).
-template <int kMB, bool kFused>
-__global__ __launch_bounds__(kMainWaves * 64) void k_mx4_small(const SmallArgs a) {
-  constexpr int kU = kMB > 2 ? 1 : 2;                // slabs of a pass
-  __shared__ float red[kMainWaves][kMB][256];
+// kWaves waves take the slabs in turn.
+template <int kMB, bool kFused, int kWaves>
+__global__ __launch_bounds__(kWaves * 64, 4) void k_mx4_small(const SmallArgs a) {
+  __shared__ float red[kWaves][kMB][256];
   __shared__ __attribute__((aligned(16))) uint16_t sT[16 * kMB][136];   // T, 128 columns and a skew
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -180,97 +226,79 @@ __global__ __launch_bounds__(kMainWaves * 64) void k_mx4_small(const SmallArgs a
   const int wrow = min(n0 + nl, a.N - 1);
   const uint8_t *wc = a.wc + static_cast<int64_t>(wrow) * slabs * 128 + 16 * g;
   const uint8_t *ws = a.ws + static_cast<int64_t>(wrow) * 8;
+  typedef Pass<kMB, kFused> pass_t;
 
   f32x4_t acc[kMB];
 #pragma unroll
   for (int m = 0; m < kMB; ++m) acc[m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  for (int sl = wave * kU; sl < slabs; sl += kMainWaves * kU) {
-    i32x4_t wv[kU][2], xv[kU][kMB][2];
-    uint2 wb[kU], xb[kU][kMB];
-    uint32_t raw[kFused ? kU : 1][2][16];
+  auto load = [&](pass_t &p, int slab) __attribute__((always_inline)) {
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int slab = min(sl + u, slabs - 1);
+    for (int h = 0; h < 2; ++h) p.w[h] = *reinterpret_cast<const i32x4_t *>(wc + slab * 128 + 64 * h);
+    p.wb = *reinterpret_cast<const uint2 *>(ws + static_cast<int64_t>(slab) * a.N * 8);
+    if constexpr (kFused) {
+      const uint16_t *x = a.X + static_cast<int64_t>(min(nl, a.M - 1)) * a.K;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) wv[u][h] = *reinterpret_cast<const i32x4_t *>(wc + slab * 128 + 64 * h);
-      wb[u] = *reinterpret_cast<const uint2 *>(ws + static_cast<int64_t>(slab) * a.N * 8);
-      if constexpr (kFused) {
-        const uint16_t *x = a.X + static_cast<int64_t>(min(nl, a.M - 1)) * a.K;
+      for (int h = 0; h < 2; ++h) {
+        const uint4 *q = reinterpret_cast<const uint4 *>(x + 32 * min(slab * 8 + 4 * h + g, blocks - 1));
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint4 *p = reinterpret_cast<const uint4 *>(x + 32 * min(slab * 8 + 4 * h + g, blocks - 1));
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint4 v = p[i];
-            raw[u][h][4 * i] = v.x;
-            raw[u][h][4 * i + 1] = v.y;
-            raw[u][h][4 * i + 2] = v.z;
-            raw[u][h][4 * i + 3] = v.w;
-          }
+        for (int i = 0; i < 4; ++i) {
+          const uint4 v = q[i];
+          p.raw[h][4 * i] = v.x;
+          p.raw[h][4 * i + 1] = v.y;
+          p.raw[h][4 * i + 2] = v.z;
+          p.raw[h][4 * i + 3] = v.w;
         }
+      }
+    } else {
+#pragma unroll
+      for (int m = 0; m < kMB; ++m) {
+        const int row = min(16 * m + nl, a.M - 1);
+        const uint8_t *c = a.xc + (static_cast<int64_t>(row) * slabs + slab) * 128 + 16 * g;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) p.x[m][h] = *reinterpret_cast<const i32x4_t *>(c + 64 * h);
+        p.xb[m] = *reinterpret_cast<const uint2 *>(a.xs + (static_cast<int64_t>(slab) * a.M + row) * 8);
+      }
+    }
+  };
+  auto multiply = [&](const pass_t &p, int slab) __attribute__((always_inline)) {
+    if (slab >= slabs) return;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int sw = static_cast<int>((h ? p.wb.y : p.wb.x) >> (8 * g));
+      if constexpr (kFused) {
+        i32x4_t x;
+        uint32_t byte = round_block(p.raw[h], x);
+        if (slab * 8 + 4 * h + g >= blocks) {   // past the row: W's fill is zero there, and so is X's
+          x = i32x4_t{0, 0, 0, 0};
+          byte = 0;
+        }
+        acc[0] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(p.w[h]), widen(x), acc[0], 4, 4, 0, sw, 0,
+                                                                  static_cast<int>(byte));
       } else {
 #pragma unroll
         for (int m = 0; m < kMB; ++m) {
-          const int row = min(16 * m + nl, a.M - 1);
-          const uint8_t *c = a.xc + (static_cast<int64_t>(row) * slabs + slab) * 128 + 16 * g;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) xv[u][m][h] = *reinterpret_cast<const i32x4_t *>(c + 64 * h);
-          xb[u][m] = *reinterpret_cast<const uint2 *>(a.xs + (static_cast<int64_t>(slab) * a.M + row) * 8);
+          const int sx = static_cast<int>((h ? p.xb[m].y : p.xb[m].x) >> (8 * g));
+          acc[m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(p.w[h]), widen(p.x[m][h]), acc[m], 4, 4, 0, sw, 0,
+                                                                    sx);
         }
       }
     }
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      if (sl + u >= slabs) continue;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t sw = (h ? wb[u].y : wb[u].x) >> (8 * g);
-        if constexpr (kFused) {
-          uint32_t byte = round_block(raw[u][h], xv[u][0][h]);
-          if ((sl + u) * 8 + 4 * h + g >= blocks) {   // past the row: W's fill is zero there, and so is X's
-            xv[u][0][h] = i32x4_t{0, 0, 0, 0};
-            byte = 0;
-          }
-          acc[0] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(wv[u][h]), widen(xv[u][0][h]), acc[0], 4, 4, 0,
-                                                                    static_cast<int>(sw), 0, static_cast<int>(byte));
-        } else {
-#pragma unroll
-          for (int m = 0; m < kMB; ++m) {
-            const uint32_t sx = (h ? xb[u][m].y : xb[u][m].x) >> (8 * g);
-            acc[m] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(wv[u][h]), widen(xv[u][m][h]), acc[m], 4, 4, 0,
-                                                                      static_cast<int>(sw), 0, static_cast<int>(sx));
-          }
-        }
-      }
-    }
+  };
+  pass_t p;
+  load(p, min(wave, slabs - 1));     // a wave without slabs reads the last one and multiplies nothing
+  if (!kFused && a.r > 0) put_T<kMB, kWaves * 64, 6>(a, sT);   // its loads come behind the first pass's
+  multiply(p, wave);
+  for (int slab = wave + kWaves; slab < slabs; slab += kWaves) {
+    load(p, slab);
+    multiply(p, slab);
   }
 #pragma unroll
   for (int m = 0; m < kMB; ++m) *reinterpret_cast<f32x4_t *>(&red[wave][m][4 * lane]) = acc[m];
-
-  if (a.r > 0) {
-    // T [M, r] into LDS, zero up to the next 32 columns
-    const int rp = (a.r + 31) / 32 * 32;
-    for (int i = threadIdx.x; i < 16 * kMB * rp; i += kMainWaves * 64) {
-      const int m = i / rp, j = i - m * rp;
-      uint16_t v = 0;
-      if (m < a.M && j < a.r) {
-        if (a.T) {
-          v = a.T[static_cast<int64_t>(m) * a.r + j];
-        } else {
-          float t = 0.f;
-          for (int s = 0; s < a.S; ++s) t += a.P[(static_cast<int64_t>(s) * a.M + m) * a.r + j];
-          v = f32_to_bf16(a.scale * t);
-          if (blockIdx.x == 0 && a.Tout) a.Tout[static_cast<int64_t>(m) * a.r + j] = v;
-        }
-      }
-      sT[m][j] = v;
-    }
-  }
   __syncthreads();
   if (wave >= kMB) return;
   f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int w = 0; w < kMainWaves; ++w) sum += *reinterpret_cast<const f32x4_t *>(&red[w][wave][4 * lane]);
+  for (int w = 0; w < kWaves; ++w) sum += *reinterpret_cast<const f32x4_t *>(&red[w][wave][4 * lane]);
   for (int j = 0; j < a.r; j += 32) {
     const bf16x8_t b = load8(a.B + static_cast<int64_t>(wrow) * a.r, j + 8 * g, a.r, (a.r & 7) == 0);
     const bf16x8_t t = *reinterpret_cast<const bf16x8_t *>(&sT[16 * wave + nl][j + 8 * g]);
@@ -291,21 +319,40 @@ __global__ __launch_bounds__(kMainWaves * 64) void k_mx4_small(const SmallArgs a
 
 namespace {
 
-int slice_of(int M) { return M <= kFusedMax ? 1024 : 2048; }
+// Columns of a slice of the LoRA partial sums.  A compute unit fetches some 30
+// KB/us, so many small workgroups make them; but every workgroup of the main
+// kernel sums the slices of all of T, so more tokens take longer slices.
+int steps_of(int64_t M) { return M <= 16 ? 2 : 4; }
+int slice_of(int64_t M) { return kPrepWaves * 32 * steps_of(M); }
+
+template <int kMB>
+hipError_t launch_waves(const SmallArgs &a, hipStream_t s) {
+  const int grid = (a.N + kMainRows - 1) / kMainRows;
+  // up to two workgroups a CU: 16 waves; more: 8, of which more share a CU
+  if (grid <= 512)
+    hipLaunchKernelGGL((k_mx4_small<kMB, false, 16>), dim3(grid), dim3(1024), 0, s, a);
+  else
+    hipLaunchKernelGGL((k_mx4_small<kMB, false, 8>), dim3(grid), dim3(512), 0, s, a);
+  return hipGetLastError();
+}
+
+// Without a LoRA pair and with a workgroup a CU at most, the main kernel rounds
+// X itself and is the only launch: 1 x 4096 x 4096 takes 4.6 us, against 3.0
+// + 3.9 us in two.  More workgroups would each round all of X again (1 x 11008
+// x 4096: 12 us against 4.3 + 6.7), and T needs a launch before it anyway.
+bool fused_ok(const SmallArgs &a) {
+  return a.r == 0 && a.M <= kFusedTokens && (a.N + kMainRows - 1) / kMainRows <= kFusedGrid;
+}
 
 template <bool kFused>
 hipError_t launch_main(const SmallArgs &a, hipStream_t s) {
-  const dim3 grid((a.N + kMainRows - 1) / kMainRows), block(kMainWaves * 64);
   if constexpr (kFused) {
-    hipLaunchKernelGGL((k_mx4_small<1, true>), grid, block, 0, s, a);
-  } else if (a.M <= 16) {
-    hipLaunchKernelGGL((k_mx4_small<1, false>), grid, block, 0, s, a);
-  } else if (a.M <= 32) {
-    hipLaunchKernelGGL((k_mx4_small<2, false>), grid, block, 0, s, a);
-  } else {
-    hipLaunchKernelGGL((k_mx4_small<4, false>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((k_mx4_small<1, true, 16>), dim3((a.N + kMainRows - 1) / kMainRows), dim3(1024), 0, s, a);
+    return hipGetLastError();
   }
-  return hipGetLastError();
+  if (a.M <= 16) return launch_waves<1>(a, s);
+  if (a.M <= 32) return launch_waves<2>(a, s);
+  return launch_waves<4>(a, s);
 }
 
 }  // namespace
@@ -313,8 +360,7 @@ hipError_t launch_main(const SmallArgs &a, hipStream_t s) {
 bool mx4_small_ok(int64_t M) { return M <= kMx4SmallMax; }
 
 size_t mx4_small_ws_bytes(int64_t M, int64_t K, int r) {
-  const int64_t S = (K + slice_of(static_cast<int>(M)) - 1) / slice_of(static_cast<int>(M));
-  return static_cast<size_t>(S) * M * r * sizeof(float);
+  return static_cast<size_t>((K + slice_of(M) - 1) / slice_of(M)) * M * r * sizeof(float);
 }
 
 hipError_t launch_mx4_small_matmul(const Mx4View &X, const Mx4View &W, const uint16_t *T, const uint16_t *B, int r,
@@ -354,17 +400,16 @@ hipError_t launch_mx4_small_linear(const uint16_t *X, const Mx4View &W, const ui
   a.slice = slice_of(a.M);
   a.S = (a.K + a.slice - 1) / a.slice;
   a.scale = scale;
-  const bool fused = a.M <= kFusedMax;
-  const int mt = fused ? 1 : 2;
-  const int downs = r > 0 ? a.S * ((r + kPrepRows - 1) / kPrepRows) * ((a.M + 16 * mt - 1) / (16 * mt)) : 0;
+  const bool fused = fused_ok(a);
+  const int downs = r > 0 ? a.S * ((r + 15) / 16) * ((a.M + 15) / 16) : 0;
   const int64_t blocks = fused ? 0 : static_cast<int64_t>(a.M) * mx4_slabs(a.K) * 8;
   const int64_t rounds = (blocks + kPrepWaves * 64 - 1) / (kPrepWaves * 64);
   const dim3 grid(static_cast<uint32_t>(downs + rounds)), block(kPrepWaves * 64);
   if (grid.x > 0) {
-    if (fused)
-      hipLaunchKernelGGL(k_mx4_prep<1>, grid, block, 0, s, a, downs, Xq.codes, Xq.scales);
-    else
+    if (steps_of(a.M) == 2)
       hipLaunchKernelGGL(k_mx4_prep<2>, grid, block, 0, s, a, downs, Xq.codes, Xq.scales);
+    else
+      hipLaunchKernelGGL(k_mx4_prep<4>, grid, block, 0, s, a, downs, Xq.codes, Xq.scales);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
