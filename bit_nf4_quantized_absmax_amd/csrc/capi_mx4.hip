@@ -127,9 +127,13 @@ int qlora_mx4_linear_fwd(const uint16_t *X, int64_t M, const qlora_mx4_array *W,
     return from_hip(launch_mx4_small_linear(X, view_of(W), A, B, r, scale, Y, r > 0 ? T_out : nullptr,
                                             reinterpret_cast<float *>(base), x, s));
   uint16_t *T = r > 0 && T_out ? T_out : reinterpret_cast<uint16_t *>(base);
-  if (r > 0 && launch_lora_down(X, static_cast<int>(M), static_cast<int>(W->cols), A, r, scale, T, s) != hipSuccess)
-    return QLORA_ERR_HIP;
-  if (launch_mx4_quantize(X, QLORA_IN_BF16, x, s) != hipSuccess) return QLORA_ERR_HIP;
+  if (r > 0 && r <= kMx4RowsMax) {
+    if (launch_mx4_rows(X, x, A, r, scale, T, s) != hipSuccess) return QLORA_ERR_HIP;
+  } else {
+    if (r > 0 && launch_lora_down(X, static_cast<int>(M), static_cast<int>(W->cols), A, r, scale, T, s) != hipSuccess)
+      return QLORA_ERR_HIP;
+    if (launch_mx4_quantize(X, QLORA_IN_BF16, x, s) != hipSuccess) return QLORA_ERR_HIP;
+  }
   return from_hip(launch_mx4_matmul(x, view_of(W), T, B, r, Y, s));
 }
 

@@ -234,6 +234,12 @@ inline int64_t mx4_slabs(int64_t cols) { return (cols + 255) / 256; }
 hipError_t launch_mx4_quantize(const void *X, int in_type, const Mx4View &a, hipStream_t s);
 hipError_t launch_mx4_dequantize(const Mx4View &a, uint16_t *out, hipStream_t s);
 
+// Xq = Q(X) and T [M, r] = bf16(scale X A^T) in one pass over X [M, K] bf16;
+// 1 <= r <= kMx4RowsMax.
+constexpr int kMx4RowsMax = 64;
+hipError_t launch_mx4_rows(const uint16_t *X, const Mx4View &Xq, const uint16_t *A, int r, float scale, uint16_t *T,
+                           hipStream_t s);
+
 // ---- MX4 products: Y [M, N] = X W^T + T B^T (T, B null at r = 0) -------------------
 // 256 x 256 or 128 x 128 tiles, any M and N.
 hipError_t launch_mx4_matmul(const Mx4View &X, const Mx4View &W, const uint16_t *T, const uint16_t *B, int r,

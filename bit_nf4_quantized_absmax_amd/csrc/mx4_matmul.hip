@@ -24,8 +24,8 @@
 //  * A workgroup takes tiles until none is left; the last step of a tile
 //    already fetches the first of the next, and the tile is stored over it.
 //    W is the matrix instruction's left operand, so that a lane's
-//    accumulators run along a row of Y: two half-wave swaps make 16-byte
-//    stores of them, without a pass through LDS.
+//    accumulators run along a row of Y: two half-wave swaps make 16 bytes of
+//    them, which cross the wave's own part of a free stage.
 #include <algorithm>
 #include <type_traits>
 
@@ -340,11 +340,14 @@ __global__ __launch_bounds__(kMxMmThreads) void k_mx4_matmul(const Mx4Args args)
     }
 
     // Accumulator layout: lane l holds row m = l % 32 of Y; element e is
-    // column 8 (e / 4) + 4 (l / 32) + e % 4.
+    // column 8 (e / 4) + 4 (l / 32) + e % 4.  Each 32 rows go through the part
+    // of the consumed stage that this wave's own next fetch fills, so that a
+    // store instruction covers whole row segments (16 bytes of 32 rows each
+    // would take twice the address cycles).
+    constexpr int kChunks = 4 * kFN, kRowsOnce = 64 / kChunks;   // 16-byte chunks of the wave's columns
+    uint8_t *part = smem + (st ? 0 : kStX) + wave * (kBM * 16);
 #pragma unroll
     for (int i = 0; i < kFM; ++i) {
-      const int m = m0 + 32 * (kFM * wm + i) + lr;
-      uint16_t *row = args.Y + static_cast<int64_t>(m) * N;
 #pragma unroll
       for (int j = 0; j < kFN; ++j)
 #pragma unroll
@@ -354,15 +357,27 @@ __global__ __launch_bounds__(kMxMmThreads) void k_mx4_matmul(const Mx4Args args)
           for (int e = 0; e < 4; ++e) p[e] = pack_bf16x2(acc[i][j][8 * q + 2 * e], acc[i][j][8 * q + 2 * e + 1]);
           swap_halves(p[0], p[2]);
           swap_halves(p[1], p[3]);
-          const int n = n0 + 32 * (kFN * wn + j) + 16 * q + 8 * lh;
-          if (m < M && n + 8 <= N) {
-            *reinterpret_cast<uint4_any *>(row + n) = make_uint4(p[0], p[1], p[2], p[3]);
-          } else if (m < M) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (n + e < N) row[n + e] = static_cast<uint16_t>(p[e >> 1] >> (16 * (e & 1)));
-          }
+          const int c = 4 * j + 2 * q + lh;
+          *reinterpret_cast<uint4 *>(part + 16 * (lr * kChunks + (c ^ (lr & (kChunks - 1))))) =
+              make_uint4(p[0], p[1], p[2], p[3]);
         }
+      __builtin_amdgcn_s_waitcnt(wait_imm(63, 0));
+#pragma unroll
+      for (int t = 0; t < 32 / kRowsOnce; ++t) {
+        const int rr = t * kRowsOnce + lane / kChunks, c = lane % kChunks;
+        const uint4 v = *reinterpret_cast<const uint4 *>(part + 16 * (rr * kChunks + (c ^ (rr & (kChunks - 1)))));
+        const int m = m0 + 32 * (kFM * wm + i) + rr, n = n0 + 32 * kFN * wn + 8 * c;
+        uint16_t *y = args.Y + static_cast<int64_t>(m) * N + n;
+        if (m < M && n + 8 <= N) {
+          *reinterpret_cast<uint4_any *>(y) = v;
+        } else if (m < M) {
+          const uint32_t h[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (n + e < N) y[e] = static_cast<uint16_t>(h[e >> 1] >> (16 * (e & 1)));
+        }
+      }
+      __builtin_amdgcn_s_waitcnt(wait_imm(63, 0));   // read before the next 32 rows, or the next fetch, write there
     }
     if (!more) return;
     m0 = m1;

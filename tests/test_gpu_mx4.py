@@ -211,8 +211,9 @@ def test_linear_backward(M, N, K, r):
     got = q.mx4_linear_bwd(dYd, Xd, T, w, Ad, Bd, scale)
     for name, a, b in zip(("dX", "dA", "dB"), got, want):
         assert_close(as_f64(a), b, name)
-    again = q.mx4_linear_bwd(dYd, Xd, None, w, Ad, Bd, scale)      # T recomputed
-    assert all(torch.equal(a, b) for a, b in zip(got, again))
+    again = q.mx4_linear_bwd(dYd, Xd, None, w, Ad, Bd, scale)      # T recomputed, its sums in another order
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+    assert_close(as_f64(again[2]), want[2], "dB, T recomputed")
     only = q.mx4_linear_bwd(dYd, Xd, T, w, Ad, Bd, scale, need_dX=False, need_dB=False)
     assert only[0] is None and only[2] is None
     assert_close(as_f64(only[1]), want[1], "dA alone")
