@@ -193,17 +193,18 @@ __global__ __launch_bounds__(kMxMmThreads) void k_mx4_matmul(const Mx4Args args)
   Tiles tiles(args.trows * args.tcols);
   if (tiles.next >= tiles.end) return;   // the whole workgroup
 
-  auto dma = [&](uint32_t st, int m0, int n0, int kt) __attribute__((always_inline)) {
+  auto dma = [&](uint32_t st, int m0, int n0, int kt, int part) __attribute__((always_inline)) {
     const uint32_t x = base + (st ? kStX : 0), w = base + kOffW + (st ? kStW : 0), sc = base + kOffS + (st ? kStS : 0);
     const int lastm = M - 1 - m0, lastn = N - 1 - n0;
     if (kPiped && kt == KT) {
-      dma_rows<kBM>(x, reinterpret_cast<const uint8_t *>(args.T) + static_cast<int64_t>(m0) * 128, 128, lastm, wave, lane);
-      dma_rows<kBN>(w, reinterpret_cast<const uint8_t *>(args.B) + static_cast<int64_t>(n0) * 128, 128, lastn, wave, lane);
+      if (part & 1) dma_rows<kBM>(x, reinterpret_cast<const uint8_t *>(args.T) + static_cast<int64_t>(m0) * 128, 128, lastm, wave, lane);
+      if (part & 2) dma_rows<kBN>(w, reinterpret_cast<const uint8_t *>(args.B) + static_cast<int64_t>(n0) * 128, 128, lastn, wave, lane);
       return;
     }
     const uint32_t pitch = static_cast<uint32_t>(KT) * 128;
-    dma_rows<kBM>(x, args.xc + static_cast<int64_t>(m0) * pitch + kt * 128, pitch, lastm, wave, lane);
-    dma_rows<kBN>(w, args.wc + static_cast<int64_t>(n0) * pitch + kt * 128, pitch, lastn, wave, lane);
+    if (part & 1) dma_rows<kBM>(x, args.xc + static_cast<int64_t>(m0) * pitch + kt * 128, pitch, lastm, wave, lane);
+    if (part & 2) dma_rows<kBN>(w, args.wc + static_cast<int64_t>(n0) * pitch + kt * 128, pitch, lastn, wave, lane);
+    if (part & 1)
 #pragma unroll
     for (int u = wave; u < (kBM + kBN) / 32; u += 8) {
       if (u < kBM / 32)
@@ -270,7 +271,7 @@ __global__ __launch_bounds__(kMxMmThreads) void k_mx4_matmul(const Mx4Args args)
         f32x16_t &c = acc[kFM - kHold + i][j];
         c = mul1<false>(fb.a[kFM - kHold + i], fb.b[j], ha[i], hb[j], 3, c);
       }
-    fetch();
+    fetch(1);
     __builtin_amdgcn_sched_barrier(0);
     if constexpr (!kLora) {
 #pragma unroll
@@ -288,6 +289,7 @@ __global__ __launch_bounds__(kMxMmThreads) void k_mx4_matmul(const Mx4Args args)
       mul<1, kFM - kHold, kLora>(cur, sc, s, acc);
       __builtin_amdgcn_sched_barrier(0);
       if (s < 3) mul<kFM - kHold, kFM, kLora>(cur, sc, s, acc);
+      if (s == 0) fetch(2);
       __builtin_amdgcn_sched_barrier(0);
     }
     xo ^= kStX;
@@ -300,7 +302,7 @@ __global__ __launch_bounds__(kMxMmThreads) void k_mx4_matmul(const Mx4Args args)
   int m0, n0;
   Tiles::place(args, tiles.next, kBM, kBN, m0, n0);
   uint32_t st = 0;
-  dma(0, m0, n0, 0);
+  dma(0, m0, n0, 0, 3);
   raw_barrier<wait_imm(0, 0)>();
   for (;;) {
     clear();
@@ -308,16 +310,16 @@ __global__ __launch_bounds__(kMxMmThreads) void k_mx4_matmul(const Mx4Args args)
     const bool more = tiles.next < tiles.end;
     int m1 = 0, n1 = 0;
     if (more) Tiles::place(args, tiles.next, kBM, kBN, m1, n1);
-    auto fetch = [&](int kt) __attribute__((always_inline)) {
-      st ^= 1;
+    auto fetch = [&](int kt, int part) __attribute__((always_inline)) {
+      if (part & 1) st ^= 1;
       if (kt + 1 < steps)
-        dma(st, m0, n0, kt + 1);
+        dma(st, m0, n0, kt + 1, part);
       else if (more)
-        dma(st, m1, n1, 0);
+        dma(st, m1, n1, 0, part);
     };
-    for (int kt = 0; kt < KT; ++kt) step(std::false_type(), [&]() __attribute__((always_inline)) { fetch(kt); });
+    for (int kt = 0; kt < KT; ++kt) step(std::false_type(), [&](int part) __attribute__((always_inline)) { fetch(kt, part); });
     if constexpr (kPiped) {
-      step(std::true_type(), [&]() __attribute__((always_inline)) { fetch(KT); });
+      step(std::true_type(), [&](int part) __attribute__((always_inline)) { fetch(KT, part); });
       mul<kFM - kHold, kFM, true>(fb, sc, 3, acc);
     } else {
       mul<kFM - kHold, kFM, false>(fb, sc, 3, acc);
