@@ -541,15 +541,19 @@ struct Slices {
   int threads;
 };
 
-// One workgroup a row where it fits and there are rows enough, or it is short
-// enough, that cutting it would not pay for the second launch (one row of
-// 32000 words: 12 us in one launch, 16 us as 16 slices and a join).
-Slices slices_of(int64_t M, int64_t V, int type, bool aligned) {
+// One workgroup a row where it fits: of 512 threads (one row of 32000 words in
+// bf16, 5 alternatives: 9.6 us, as slices and a join 13.3; 128 rows: 13.1 and
+// 20.3), or of 1024 (128 rows of 50000: logprobs 22.1 and 23.5, distill 16.9 and
+// 24.8; 2048 rows: distill 133 and 147).  But 1024 threads are a workgroup a
+// CU, with nothing to run beside its search for alternatives, so with those
+// and more than a row a CU the row is cut (512 rows of 50000: 33.6 us, whole
+// 40.5; 2048 rows: 88, whole 136).
+Slices slices_of(int64_t M, int64_t V, int type, int top, bool aligned) {
   const int n = type == 0 ? 4 : 8;
   // a row that starts inside 16 bytes may touch one vector more
   const int nv = static_cast<int>((V + n - 1 + (aligned ? 0 : n - 1)) / n);
   constexpr int kSlice = kVThreads * kVecs;
-  if (nv <= 2 * kSlice || (nv <= 4 * kSlice && M >= 512))
+  if (nv <= 2 * kSlice || (nv <= 4 * kSlice && (top == 0 || M <= 256)))
     return Slices{1, nv, nv <= kSlice ? 256 : nv <= 2 * kSlice ? 512 : 1024};
   // slices enough for two workgroups a CU, of one vector a thread at least,
   // and whole vectors for every thread
@@ -559,9 +563,9 @@ Slices slices_of(int64_t M, int64_t V, int type, bool aligned) {
   return Slices{(nv + per - 1) / per, per, kVThreads};
 }
 
-Slices slices_of(const Logits &l) {
+Slices slices_of(const Logits &l, int top) {
   const bool aligned = (reinterpret_cast<uintptr_t>(l.z) & 15) == 0 && (l.M == 1 || l.ld % (l.type == 0 ? 4 : 8) == 0);
-  return slices_of(l.M, l.V, l.type, aligned);
+  return slices_of(l.M, l.V, l.type, top, aligned);
 }
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
@@ -574,7 +578,7 @@ size_t slices_bytes(int64_t M, const Slices &sl, int top) {
 }  // namespace
 
 size_t vocab_ws_bytes(int64_t M, int64_t V, int type, int top) {   // wherever the rows start
-  return std::max(slices_bytes(M, slices_of(M, V, type, true), top), slices_bytes(M, slices_of(M, V, type, false), top));
+  return std::max(slices_bytes(M, slices_of(M, V, type, top, true), top), slices_bytes(M, slices_of(M, V, type, top, false), top));
 }
 
 // One workgroup: one slice of one row.
@@ -646,40 +650,45 @@ __global__ __launch_bounds__(kTop ? kVThreads : 64) void k_logprobs_join(const T
   if (threadIdx.x == 0) put_logprobs(out, Z + m * ld, V, m, target[m], o);
   if constexpr (kTop) {
     __shared__ uint64_t cand[kJoinMax];
-    __shared__ uint64_t sh[2][kVThreads / 64];
+    __shared__ uint64_t smax[kVThreads];
     __shared__ int count;
     const uint64_t *k = keys + m * S * top;
-    // Two bounds that `top` keys reach: the best list's last key, and the
-    // lowest of the lists' ceil(top / S)-th keys.
-    const int each = (top + S - 1) / S;
-    uint64_t b0 = 0, b1 = ~uint64_t{0};
-    for (int i = threadIdx.x; i < S; i += kVThreads) {
-      b0 = max(b0, k[i * top + top - 1]);
-      b1 = min(b1, k[i * top + each - 1]);
-    }
-#pragma unroll
-    for (int w = 32; w >= 1; w >>= 1) {
-      b0 = max(b0, static_cast<uint64_t>(__shfl_xor(b0, w, 64)));
-      b1 = min(b1, static_cast<uint64_t>(__shfl_xor(b1, w, 64)));
-    }
-    if ((threadIdx.x & 63) == 0) {
-      sh[0][threadIdx.x >> 6] = b0;
-      sh[1][threadIdx.x >> 6] = b1;
-    }
-    if (threadIdx.x == 0) count = 0;
+    const int tid = static_cast<int>(threadIdx.x);
+    // As in block_top, on whole keys: a bound that `top` threads' best keys
+    // reach and not many more.  Entry q of list s goes to thread s + q odd: the
+    // lists' first entries to different threads, and so those of one list.
+    const int odd = S | 1, places = odd * top;
+    auto entry = [&](int i) { return i % odd < S ? k[i % odd * top + i / odd] : uint64_t{0}; };
+    uint64_t mine = 0;
+    for (int i = tid; i < places; i += kVThreads) mine = max(mine, entry(i));
+    smax[tid] = mine;
+    if (tid == 0) count = 0;
     __syncthreads();
-    for (int w = 0; w < kVThreads / 64; ++w) {
-      b0 = max(b0, sh[0][w]);
-      b1 = min(b1, sh[1][w]);
-    }
-    const uint64_t bound = max(max(b0, b1), uint64_t{1});   // 0 is no key
-    for (int i = threadIdx.x; i < S * top; i += kVThreads) {
-      const uint64_t key = k[i];
-      if (key >= bound) {
-        const int at = atomicAdd(&count, 1);
-        if (at < kJoinMax) cand[at] = key;
+    uint64_t g[kVThreads / 64];
+#pragma unroll
+    for (int w = 0; w < kVThreads / 64; ++w) g[w] = smax[64 * w + (tid & 63)];
+    uint64_t lo = 0, hi = ~uint64_t{0};   // as many as `top` reach lo, fewer reach hi
+    while (hi - lo > 1) {
+      const uint64_t mid = lo + (hi - lo) / 2;
+      int r = 0;
+#pragma unroll
+      for (int w = 0; w < kVThreads / 64; ++w) r += __popcll(__ballot(g[w] >= mid));
+      if (r >= top) {
+        lo = mid;
+        if (r <= top + top / 4) break;
+      } else {
+        hi = mid;
       }
     }
+    const uint64_t bound = max(lo, uint64_t{1});   // 0 is no key
+    if (mine >= bound)
+      for (int i = tid; i < places; i += kVThreads) {
+        const uint64_t key = entry(i);
+        if (key >= bound) {
+          const int at = atomicAdd(&count, 1);
+          if (at < kJoinMax) cand[at] = key;
+        }
+      }
     __syncthreads();
     const int found = count;
     if (found <= kJoinMax) {
@@ -690,8 +699,8 @@ __global__ __launch_bounds__(kTop ? kVThreads : 64) void k_logprobs_join(const T
         if (place < top) put_top(out, m * top + place, key, o);
       }
     } else {
-      // Rows of more than kJoinMax / top slices, sorted against them: a key's
-      // place is its place in its own list and, in every other, the number
+      // More keys above the bound (rows whose best words lie in few slices): a
+      // key's place is its place in its own list and, in every other, the number
       // of better keys there.
       for (int i = threadIdx.x; i < S * top; i += kVThreads) {
         const uint64_t key = k[i];
@@ -1052,7 +1061,7 @@ hipError_t launch_slice(const Logits &l, const Slices &sl, float c, int top, Par
 
 template <typename T, bool kTop>
 hipError_t logprobs_as(const Logits &l, const int64_t *target, int top, const LogprobOut &out, void *ws, hipStream_t s) {
-  const Slices sl = slices_of(l);
+  const Slices sl = slices_of(l, top);
   const T *z = static_cast<const T *>(l.z);
   const int V = static_cast<int>(l.V);
   const dim3 rows(static_cast<uint32_t>(l.M));
@@ -1107,7 +1116,7 @@ hipError_t distill_row_as(const Logits &l, const Teacher &t, const Slices &sl, c
 
 template <typename T>
 hipError_t distill_fwd_as(const Logits &l, const Teacher &t, float *loss, float *lse, void *ws, hipStream_t s) {
-  const Slices sl = slices_of(l);
+  const Slices sl = slices_of(l, 0);
   if (sl.S == 1) return distill_row_as<T, false>(l, t, sl, nullptr, loss, lse, nullptr, 0, s);
   const float c = scaled_log2e(t.temperature);
   Partial *part = static_cast<Partial *>(ws);
@@ -1136,7 +1145,7 @@ hipError_t distill_bwd_as(const Logits &l, const Teacher &t, const float *lse, c
 template <typename T>
 hipError_t distill_as(const Logits &l, const Teacher &t, const float *weight, float *loss, float *lse, void *dz, int64_t ldd,
                       void *ws, hipStream_t s) {
-  const Slices sl = slices_of(l);
+  const Slices sl = slices_of(l, 0);
   if (sl.S == 1) return distill_row_as<T, true>(l, t, sl, weight, loss, lse, dz, ldd, s);
   const hipError_t e = distill_fwd_as<T>(l, t, loss, lse, ws, s);
   return e != hipSuccess ? e : distill_bwd_as<T>(l, t, lse, weight, dz, ldd, s);

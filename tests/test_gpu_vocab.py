@@ -152,6 +152,30 @@ def test_distill(dtype, M, V, pitch, shift):
         _check_distill(z, idx, val, temperature, 4)
 
 
+@pytest.mark.parametrize("dtype,M,V", [(FP32, 12, 37902), (BF16, 300, 50001), (BF16, 9, 70000), (FP16, 5, 131073)])
+def test_alternatives_wherever_they_lie(dtype, M, V):
+    """The best words in one slice, in few, at the end, at equal steps, or too few."""
+    g = np.random.default_rng(V)
+    z = g.standard_normal((M, V))
+    ramp = np.linspace(-8.0, 8.0, V)
+    z[0] = ramp
+    z[1] = -ramp
+    z[2, V // 2 : V // 2 + 64] += 20.0
+    z[3, V - 70 :] += 20.0
+    z[4] = -np.inf
+    z[4, V - 30 :] = ramp[:30]                   # the others follow in the order of their indices
+    if M > 8:
+        z[5, :: V // 64] += 20.0
+        z[6, :300] += 15.0
+        z[6, V // 3 : V // 3 + 300] += 15.0
+        z[7, g.permutation(V)[:40]] += 30.0
+        z[8] = 1.0
+    v = _rows(z, dtype, V + 3, 1)
+    t = torch.from_numpy(g.integers(0, V, M)).to(DEV)
+    for top in (1, 5, 64):
+        _check_logprobs(v, t, top)
+
+
 @pytest.mark.parametrize("M", [1, 40, 700])
 def test_equal_words_and_flat_rows(M):
     """Few distinct logits: the lower index first, over slices and threads."""
