@@ -48,16 +48,26 @@ int check_shape(int64_t M, int64_t N, int64_t K, int32_t r, bool bwd) {
   return QLORA_OK;
 }
 
-// Workspace of the forward pass: T (when the caller keeps none; at few tokens
-// its partial sums) | X's codes | X's scales.
+// How X's rounding and T are made, by measurement (r = 64): one pass over X
+// with 32 tokens a workgroup from kMx4RowsMin tokens on; below, where those
+// are too few to fetch X fast, partial sums from many workgroups (75 x 8224: 9.4
+// us and 41 in one pass; 1024 x 4096: 15 and 26; 2048 x 4096: 23 and 26; 4096 x
+// 4096: 42 and 27).  More adapter rows than the one pass holds: the LoRA
+// kernels' product and the codec.
+bool by_partials(int64_t M, int32_t r) { return r > 0 && (mx4_small_ok(M) || (r <= kMx4RowsMax && M < kMx4RowsMin)); }
+
+// Workspace of the forward pass: T (when the caller keeps none) | partial sums
+// of T | X's codes | X's scales | the product's split tiles.
 struct FwdWs {
-  size_t t, codes, total;
+  size_t t, p, codes, scales, total;
 };
-FwdWs fwd_ws(int64_t M, int64_t K, int32_t r) {
+FwdWs fwd_ws(int64_t M, int64_t N, int64_t K, int32_t r) {
   FwdWs w;
-  w.t = mx4_small_ok(M) ? round_up(mx4_small_ws_bytes(M, K, r), 256) : bf16_bytes(M * r);
+  w.t = mx4_small_ok(M) ? 0 : bf16_bytes(M * r);
+  w.p = by_partials(M, r) ? round_up(mx4_small_ws_bytes(M, K, r), 256) : 0;
   w.codes = round_up(code_bytes(M, K), 256);
-  w.total = w.t + w.codes + round_up(scale_bytes(M, K), 256);
+  w.scales = round_up(scale_bytes(M, K), 256);
+  w.total = w.t + w.p + w.codes + w.scales + (mx4_small_ok(M) ? 0 : mx4_split_ws_bytes(M, N, K));
   return w;
 }
 
@@ -101,12 +111,12 @@ int qlora_mx4_matmul(const qlora_mx4_array *X, const qlora_mx4_array *W, const u
   if (X->rows == 0) return QLORA_OK;
   if (mx4_small_ok(X->rows))
     return from_hip(launch_mx4_small_matmul(view_of(X), view_of(W), T, B, r, Y, static_cast<hipStream_t>(stream)));
-  return from_hip(launch_mx4_matmul(view_of(X), view_of(W), T, B, r, Y, static_cast<hipStream_t>(stream)));
+  return from_hip(launch_mx4_matmul(view_of(X), view_of(W), T, B, r, Y, nullptr, static_cast<hipStream_t>(stream)));
 }
 
 size_t qlora_mx4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t r, int is_bwd) {
   if (M == 0 || check_shape(M, N, K, r, is_bwd != 0)) return 0;
-  if (!is_bwd) return fwd_ws(M, K, r).total;
+  if (!is_bwd) return fwd_ws(M, N, K, r).total;
   return bf16_bytes(N * K) + bwd_ws(M, N, K, r).total;
 }
 
@@ -118,23 +128,27 @@ int qlora_mx4_linear_fwd(const uint16_t *X, int64_t M, const qlora_mx4_array *W,
   if (!rows_ok(X, M) || !rows_ok(Y, M)) return QLORA_ERR_INVALID_ARG;
   if (r > 0 && (!bf16_ok(A) || !bf16_ok(B) || !bf16_opt(T_out) || !isfinite(scale))) return QLORA_ERR_INVALID_ARG;
   if (M == 0) return QLORA_OK;
-  const FwdWs L = fwd_ws(M, W->cols, r);
+  const FwdWs L = fwd_ws(M, W->rows, W->cols, r);
   if (!ws || !aligned(ws, 16) || ws_bytes < L.total) return QLORA_ERR_WORKSPACE;
   hipStream_t s = static_cast<hipStream_t>(stream);
   uint8_t *base = static_cast<uint8_t *>(ws);
-  const Mx4View x{base + L.t, base + L.t + L.codes, M, W->cols};
+  float *P = reinterpret_cast<float *>(base + L.t);
+  uint8_t *codes = base + L.t + L.p;
+  const Mx4View x{codes, codes + L.codes, M, W->cols};
   if (mx4_small_ok(M))
-    return from_hip(launch_mx4_small_linear(X, view_of(W), A, B, r, scale, Y, r > 0 ? T_out : nullptr,
-                                            reinterpret_cast<float *>(base), x, s));
+    return from_hip(launch_mx4_small_linear(X, view_of(W), A, B, r, scale, Y, r > 0 ? T_out : nullptr, P, x, s));
   uint16_t *T = r > 0 && T_out ? T_out : reinterpret_cast<uint16_t *>(base);
-  if (r > 0 && r <= kMx4RowsMax) {
-    if (launch_mx4_rows(X, x, A, r, scale, T, s) != hipSuccess) return QLORA_ERR_HIP;
+  hipError_t e = hipSuccess;
+  if (by_partials(M, r)) {
+    e = launch_mx4_prep(X, x, A, r, scale, T, P, s);
+  } else if (r > 0 && r <= kMx4RowsMax) {
+    e = launch_mx4_rows(X, x, A, r, scale, T, s);
   } else {
-    if (r > 0 && launch_lora_down(X, static_cast<int>(M), static_cast<int>(W->cols), A, r, scale, T, s) != hipSuccess)
-      return QLORA_ERR_HIP;
-    if (launch_mx4_quantize(X, QLORA_IN_BF16, x, s) != hipSuccess) return QLORA_ERR_HIP;
+    if (r > 0) e = launch_lora_down(X, static_cast<int>(M), static_cast<int>(W->cols), A, r, scale, T, s);
+    if (e == hipSuccess) e = launch_mx4_quantize(X, QLORA_IN_BF16, x, s);
   }
-  return from_hip(launch_mx4_matmul(x, view_of(W), T, B, r, Y, s));
+  if (e != hipSuccess) return QLORA_ERR_HIP;
+  return from_hip(launch_mx4_matmul(x, view_of(W), T, B, r, Y, codes + L.codes + L.scales, s));
 }
 
 int qlora_mx4_linear_bwd(const uint16_t *dY, const uint16_t *X, const uint16_t *T, int64_t M, const qlora_mx4_array *W,

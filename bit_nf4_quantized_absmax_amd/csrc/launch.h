@@ -237,18 +237,25 @@ hipError_t launch_mx4_dequantize(const Mx4View &a, uint16_t *out, hipStream_t s)
 // Xq = Q(X) and T [M, r] = bf16(scale X A^T) in one pass over X [M, K] bf16;
 // 1 <= r <= kMx4RowsMax.
 constexpr int kMx4RowsMax = 64;
+constexpr int64_t kMx4RowsMin = 2048;   // tokens from which its 32-token workgroups suffice
 hipError_t launch_mx4_rows(const uint16_t *X, const Mx4View &Xq, const uint16_t *A, int r, float scale, uint16_t *T,
                            hipStream_t s);
 
 // ---- MX4 products: Y [M, N] = X W^T + T B^T (T, B null at r = 0) -------------------
 // 256 x 256 or 128 x 128 tiles, any M and N.
+// ws (nullable): mx4_split_ws_bytes, for few tiles of a long contraction.
+size_t mx4_split_ws_bytes(int64_t M, int64_t N, int64_t K);
 hipError_t launch_mx4_matmul(const Mx4View &X, const Mx4View &W, const uint16_t *T, const uint16_t *B, int r,
-                             uint16_t *Y, hipStream_t s);
+                             uint16_t *Y, void *ws, hipStream_t s);
 
 // M <= kMx4SmallMax.  P: mx4_small_ws_bytes(M, K, r), the LoRA partial sums;
 // Xq: storage for X in MX4 (written from 17 tokens on).
 constexpr int64_t kMx4SmallMax = 64;
 bool mx4_small_ok(int64_t M);
+// Xq = Q(X) and T = bf16(scale X A^T) for any M by way of P, mx4_small_ws_bytes:
+// for few tokens, where launch_mx4_rows has too few workgroups.
+hipError_t launch_mx4_prep(const uint16_t *X, const Mx4View &Xq, const uint16_t *A, int r, float scale, uint16_t *T,
+                           float *P, hipStream_t s);
 size_t mx4_small_ws_bytes(int64_t M, int64_t K, int r);
 hipError_t launch_mx4_small_matmul(const Mx4View &X, const Mx4View &W, const uint16_t *T, const uint16_t *B, int r,
                                    uint16_t *Y, hipStream_t s);

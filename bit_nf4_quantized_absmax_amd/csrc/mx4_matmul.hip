@@ -42,7 +42,7 @@ typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 
 constexpr int kMxMmThreads = 512;
-constexpr int kMxBand = 4;   // tile rows of a band (see Tiles)
+constexpr int kMxBand = 4;   // tile rows of a band (see Tiles); 8192 x 11008 x 4096: 206 us, in bands of one 218
 constexpr int kCUs = 256;
 constexpr int kXcds = 8;
 
@@ -53,6 +53,8 @@ struct Mx4Args {
   int M, N, r;
   int KT;            // slabs
   int trows, tcols;
+  float *part;       // split: partial tiles [splits][tiles], else unused
+  int splits;
 };
 
 // The tiles of a workgroup.  Workgroups go to the 8 XCDs in turn; each XCD has
@@ -62,6 +64,7 @@ struct Mx4Args {
 // X and of W in its L2.
 struct Tiles {
   int next, end, step;
+  __device__ __forceinline__ Tiles(int n, int e, int s) : next(n), end(e), step(s) {}
   __device__ __forceinline__ explicit Tiles(int tiles) {
     const int x = blockIdx.x % kXcds, each = tiles / kXcds, over = tiles % kXcds;
     const int begin = x * each + min(x, over);
@@ -171,8 +174,10 @@ typedef uint4 __attribute__((aligned(2))) uint4_any;   // rows of an odd N start
 
 }  // namespace
 
-// kPiped: r == 64, the LoRA step runs in the pipeline.
-template <int kFM, int kFN, bool kPiped>
+// kPiped: r == 64, the LoRA step runs in the pipeline.  kSplit: a workgroup has
+// one tile and a part of the contraction, and leaves its fp32 sums (the last
+// part's with the LoRA term) for k_mx4_join.
+template <int kFM, int kFN, bool kPiped, bool kSplit>
 __global__ __launch_bounds__(kMxMmThreads) void k_mx4_matmul(const Mx4Args args) {
   constexpr int kBM = 64 * kFM, kBN = 128 * kFN;
   constexpr int kHold = kFM / 2;                 // row fragments whose last products run after the barrier
@@ -183,7 +188,10 @@ __global__ __launch_bounds__(kMxMmThreads) void k_mx4_matmul(const Mx4Args args)
   __shared__ __attribute__((aligned(128))) uint8_t smem[kOffS + 2 * kStS];
 
   const int M = args.M, N = args.N, r = args.r, KT = args.KT;
-  const int steps = KT + (kPiped ? 1 : 0);
+  const int tile = kSplit ? blockIdx.x / args.splits : 0, split = kSplit ? blockIdx.x % args.splits : 0;
+  const int k0 = kSplit ? KT * split / args.splits : 0, k1 = kSplit ? KT * (split + 1) / args.splits : KT;
+  const bool last = !kSplit || split == args.splits - 1;   // takes the LoRA steps
+  const int steps = k1 + (kPiped && last ? 1 : 0);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 2, wn = wave & 3;
@@ -191,6 +199,7 @@ __global__ __launch_bounds__(kMxMmThreads) void k_mx4_matmul(const Mx4Args args)
   const uint32_t base = lds_addr(smem);
 
   Tiles tiles(args.trows * args.tcols);
+  if constexpr (kSplit) tiles = Tiles{tile, tile + 1, 1};
   if (tiles.next >= tiles.end) return;   // the whole workgroup
 
   auto dma = [&](uint32_t st, int m0, int n0, int kt, int part) __attribute__((always_inline)) {
@@ -302,7 +311,7 @@ __global__ __launch_bounds__(kMxMmThreads) void k_mx4_matmul(const Mx4Args args)
   int m0, n0;
   Tiles::place(args, tiles.next, kBM, kBN, m0, n0);
   uint32_t st = 0;
-  dma(0, m0, n0, 0, 3);
+  dma(0, m0, n0, k0, 3);
   raw_barrier<wait_imm(0, 0)>();
   for (;;) {
     clear();
@@ -315,16 +324,16 @@ __global__ __launch_bounds__(kMxMmThreads) void k_mx4_matmul(const Mx4Args args)
       if (kt + 1 < steps)
         dma(st, m0, n0, kt + 1, part);
       else if (more)
-        dma(st, m1, n1, 0, part);
+        dma(st, m1, n1, k0, part);
     };
-    for (int kt = 0; kt < KT; ++kt) step(std::false_type(), [&](int part) __attribute__((always_inline)) { fetch(kt, part); });
-    if constexpr (kPiped) {
+    for (int kt = k0; kt < k1; ++kt) step(std::false_type(), [&](int part) __attribute__((always_inline)) { fetch(kt, part); });
+    if (kPiped && last) {
       step(std::true_type(), [&](int part) __attribute__((always_inline)) { fetch(KT, part); });
       mul<kFM - kHold, kFM, true>(fb, sc, 3, acc);
     } else {
       mul<kFM - kHold, kFM, false>(fb, sc, 3, acc);
       // The stage just consumed takes T and B; the other one is being filled.
-      for (int j0 = 0; j0 < r; j0 += 64) {
+      for (int j0 = 0; !kPiped && last && j0 < r; j0 += 64) {
         stage_narrow<kBM>(smem + (st ? 0 : kStX), args.T, r, m0, M, j0);
         stage_narrow<kBN>(smem + kOffW + (st ? 0 : kStW), args.B, r, n0, N, j0);
         __syncthreads();
@@ -339,6 +348,20 @@ __global__ __launch_bounds__(kMxMmThreads) void k_mx4_matmul(const Mx4Args args)
         wo ^= kStW;
         __syncthreads();
       }
+    }
+
+    if constexpr (kSplit) {
+      float4 *out = reinterpret_cast<float4 *>(args.part) +
+                    ((static_cast<int64_t>(split) * args.trows * args.tcols + tile) * 8 + wave) * (kFM * kFN * 256) + lane;
+#pragma unroll
+      for (int i = 0; i < kFM; ++i)
+#pragma unroll
+        for (int j = 0; j < kFN; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            out[((i * kFN + j) * 4 + q) * 64] = make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
+                                                            acc[i][j][4 * q + 3]);
+      return;
     }
 
     // Accumulator layout: lane l holds row m = l % 32 of Y; element e is
@@ -387,24 +410,94 @@ __global__ __launch_bounds__(kMxMmThreads) void k_mx4_matmul(const Mx4Args args)
   }
 }
 
+// One workgroup: one wave's part of a tile, its splits' sums added in order.
+template <int kFM, int kFN>
+__global__ __launch_bounds__(kFM * kFN * 256) void k_mx4_join(const Mx4Args args) {
+  const int lane = threadIdx.x & 63, part = threadIdx.x >> 6;     // part: fragment and quarter of its elements
+  const int tile = blockIdx.x >> 3, wave = blockIdx.x & 7;
+  const int64_t plane = static_cast<int64_t>(args.trows) * args.tcols * 8 * (kFM * kFN * 256);
+  const float4 *p = reinterpret_cast<const float4 *>(args.part) + static_cast<int64_t>(blockIdx.x) * (kFM * kFN * 256) + threadIdx.x;
+  float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int z = 0; z < args.splits; ++z) {
+    const float4 v = p[z * plane];
+    t.x += v.x;
+    t.y += v.y;
+    t.z += v.z;
+    t.w += v.w;
+  }
+  int m0, n0;
+  Tiles::place(args, tile, 64 * kFM, 128 * kFN, m0, n0);
+  const int f = part >> 2, q = part & 3;
+  const int m = m0 + 32 * (kFM * (wave >> 2) + f / kFN) + (lane & 31);
+  const int n = n0 + 32 * (kFN * (wave & 3) + f % kFN) + 8 * q + 4 * (lane >> 5);
+  if (m >= args.M) return;
+  uint16_t *y = args.Y + static_cast<int64_t>(m) * args.N + n;
+  const uint32_t a = pack_bf16x2(t.x, t.y), b = pack_bf16x2(t.z, t.w);
+  typedef uint2 __attribute__((aligned(2))) uint2_any;
+  if (n + 4 <= args.N) {
+    *reinterpret_cast<uint2_any *>(y) = make_uint2(a, b);
+  } else {
+    const uint32_t h[2] = {a, b};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (n + e < args.N) y[e] = static_cast<uint16_t>(h[e >> 1] >> (16 * (e & 1)));
+  }
+}
+
 namespace {
+
+int64_t small_tiles(int64_t M, int64_t N) { return (M + 127) / 128 * ((N + 127) / 128); }
+
+// Parts of the contraction for few small tiles, four steps or more each.  A
+// step of a lone workgroup waits for its fetch, some 0.7 us; partial tiles and
+// join cost about 20 such steps.  Whole and split, with the join:
+//   128 x 4096 x 11008   32.3   16.3 us   (10 parts: 38 steps saved)
+//   512 x 4096 x 11008   32.8   28.2      (3 parts: 28)
+//   512 x 4096 x 6144    19.2   21.2      (3 parts: 16)
+//   256 x 11008 x 8192   25.4   28.0      (2 parts: 16)
+int splits_of(int64_t M, int64_t N, int64_t K) {
+  const int64_t KT = mx4_slabs(K);
+  const int64_t z = std::max<int64_t>(1, std::min(KT / 4, 384 / small_tiles(M, N)));
+  return KT - KT / z >= 20 ? static_cast<int>(z) : 1;
+}
 
 template <int kFM, int kFN>
 hipError_t launch_tiles(Mx4Args a, int per_cu, hipStream_t s) {
   a.trows = (a.M + 64 * kFM - 1) / (64 * kFM);
   a.tcols = (a.N + 128 * kFN - 1) / (128 * kFN);
-  const dim3 grid(static_cast<uint32_t>(std::min<int64_t>(static_cast<int64_t>(a.trows) * a.tcols, kCUs * per_cu)));
+  const int64_t tiles = static_cast<int64_t>(a.trows) * a.tcols;
+  const dim3 block(kMxMmThreads);
+  if constexpr (kFM == 2) {
+    if (a.splits > 1) {
+      const dim3 grid(static_cast<uint32_t>(tiles * a.splits));
+      if (a.r == 64)
+        hipLaunchKernelGGL((k_mx4_matmul<kFM, kFN, true, true>), grid, block, 0, s, a);
+      else
+        hipLaunchKernelGGL((k_mx4_matmul<kFM, kFN, false, true>), grid, block, 0, s, a);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+      hipLaunchKernelGGL((k_mx4_join<kFM, kFN>), dim3(static_cast<uint32_t>(tiles * 8)), dim3(kFM * kFN * 256), 0, s, a);
+      return hipGetLastError();
+    }
+  }
+  const dim3 grid(static_cast<uint32_t>(std::min<int64_t>(tiles, kCUs * per_cu)));
   if (a.r == 64)
-    hipLaunchKernelGGL((k_mx4_matmul<kFM, kFN, true>), grid, dim3(kMxMmThreads), 0, s, a);
+    hipLaunchKernelGGL((k_mx4_matmul<kFM, kFN, true, false>), grid, block, 0, s, a);
   else
-    hipLaunchKernelGGL((k_mx4_matmul<kFM, kFN, false>), grid, dim3(kMxMmThreads), 0, s, a);
+    hipLaunchKernelGGL((k_mx4_matmul<kFM, kFN, false, false>), grid, block, 0, s, a);
   return hipGetLastError();
 }
 
 }  // namespace
 
+size_t mx4_split_ws_bytes(int64_t M, int64_t N, int64_t K) {
+  const int z = splits_of(M, N, K);
+  return z > 1 ? static_cast<size_t>(z) * small_tiles(M, N) * 128 * 128 * sizeof(float) : 0;
+}
+
 hipError_t launch_mx4_matmul(const Mx4View &X, const Mx4View &W, const uint16_t *T, const uint16_t *B, int r, uint16_t *Y,
-                             hipStream_t s) {
+                             void *ws, hipStream_t s) {
   Mx4Args a{};
   a.xc = X.codes;
   a.xs = X.scales;
@@ -417,9 +510,14 @@ hipError_t launch_mx4_matmul(const Mx4View &X, const Mx4View &W, const uint16_t 
   a.N = static_cast<int>(W.rows);
   a.r = r;
   a.KT = static_cast<int>(mx4_slabs(X.cols));
-  // The small tile where the large one leaves compute units without work.
-  const int64_t large = ((X.rows + 255) / 256) * ((W.rows + 255) / 256);
-  return large >= kCUs ? launch_tiles<4, 2>(a, 1, s) : launch_tiles<2, 1>(a, 2, s);
+  a.part = static_cast<float *>(ws);
+  a.splits = ws ? splits_of(X.rows, W.rows, X.cols) : 1;
+  // Small tiles while all of them run at once, two a compute unit (2048 x 4096
+  // x 4096: 23.7 us, large 30.1); beyond, the large ones, which read half as
+  // much (2048 x 5120 x 11008: 71.6 us, small 78.8; 8192 x 11008 x 4096: 206,
+  // small 243).  A single small tile row would be half a large one (100 x 131072
+  // x 4096: 64.9 us, large 72.7).
+  return X.rows > 128 && small_tiles(X.rows, W.rows) > 2 * kCUs ? launch_tiles<4, 2>(a, 1, s) : launch_tiles<2, 1>(a, 2, s);
 }
 
 }  // namespace qlora

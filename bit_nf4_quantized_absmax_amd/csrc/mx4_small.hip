@@ -29,6 +29,13 @@ typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
 
 constexpr int kPrepWaves = 16;
+// Columns of a slice of the partial sums: 32 a step, two steps a wave.  A
+// compute unit fetches some 30 KB/us, so many small workgroups make them: at 32
+// to 64 tokens of 4096 columns 4.4 us, with four steps a wave 6.0.  The main
+// kernel then sums twice the slices, which costs it as much only at 64 tokens
+// of 11008 columns (25.7 us in all against 25.2).
+constexpr int kSteps = 2;
+constexpr int kSlice = kPrepWaves * 32 * kSteps;
 constexpr int kMainRows = 16;         // weight rows of a workgroup
 constexpr int kFusedTokens = 16;      // see fused_ok
 constexpr int kFusedGrid = 256;
@@ -79,9 +86,8 @@ __device__ __forceinline__ uint32_t round_block(const uint32_t (&x)[16], i32x4_t
 
 }  // namespace
 
-// kSteps: 32-column steps of a wave, all loaded before the first product.
-// Workgroups from `downs` on round X.
-template <int kSteps>
+// A wave's steps are all loaded before the first product.  Workgroups from
+// `downs` on round X.
 __global__ __launch_bounds__(kPrepWaves * 64) void k_mx4_prep(const SmallArgs a, int downs, uint8_t *xc, uint8_t *xs) {
   __shared__ float red[kPrepWaves][256];
   const int lane = threadIdx.x & 63;
@@ -212,6 +218,17 @@ __device__ __forceinline__ void put_T(const SmallArgs &a, uint16_t (*sT)[136]) {
 
 }  // namespace
 
+// T from the partials, where a tiled product follows.
+__global__ __launch_bounds__(256) void k_mx4_sum(const float *__restrict__ P, int S, int64_t n, float scale,
+                                                 uint16_t *__restrict__ T) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= n) return;
+  float t = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < S; ++s) t += P[s * n + i];
+  T[i] = f32_to_bf16(scale * t);
+}
+
 // kMB: tiles of 16 tokens.  kFused: X is bf16 and rounded here (kMB == 1).
 // kWaves waves take the slabs in turn.
 template <int kMB, bool kFused, int kWaves>
@@ -319,16 +336,12 @@ __global__ __launch_bounds__(kWaves * 64, 4) void k_mx4_small(const SmallArgs a)
 
 namespace {
 
-// Columns of a slice of the LoRA partial sums.  A compute unit fetches some 30
-// KB/us, so many small workgroups make them; but every workgroup of the main
-// kernel sums the slices of all of T, so more tokens take longer slices.
-int steps_of(int64_t M) { return M <= 16 ? 2 : 4; }
-int slice_of(int64_t M) { return kPrepWaves * 32 * steps_of(M); }
-
 template <int kMB>
 hipError_t launch_waves(const SmallArgs &a, hipStream_t s) {
   const int grid = (a.N + kMainRows - 1) / kMainRows;
-  // up to two workgroups a CU: 16 waves; more: 8, of which more share a CU
+  // Up to two workgroups a CU: 16 waves (64 x 4096 x 11008: 18.9 us, with 8
+  // waves 21.0).  More: 8, of which more share a CU (1 x 11008 x 4096: 6.5 us,
+  // with 16 waves 9.8).
   if (grid <= 512)
     hipLaunchKernelGGL((k_mx4_small<kMB, false, 16>), dim3(grid), dim3(1024), 0, s, a);
   else
@@ -355,12 +368,21 @@ hipError_t launch_main(const SmallArgs &a, hipStream_t s) {
   return launch_waves<4>(a, s);
 }
 
+// The partial sums of X A^T (r > 0) and Q(X), one launch.
+hipError_t launch_prep(const SmallArgs &a, const Mx4View &Xq, hipStream_t s) {
+  const int64_t downs = a.r > 0 ? static_cast<int64_t>(a.S) * ((a.r + 15) / 16) * ((a.M + 15) / 16) : 0;
+  const int64_t blocks = static_cast<int64_t>(a.M) * mx4_slabs(a.K) * 8;
+  const dim3 grid(static_cast<uint32_t>(downs + (blocks + kPrepWaves * 64 - 1) / (kPrepWaves * 64))), block(kPrepWaves * 64);
+  hipLaunchKernelGGL(k_mx4_prep, grid, block, 0, s, a, static_cast<int>(downs), Xq.codes, Xq.scales);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 bool mx4_small_ok(int64_t M) { return M <= kMx4SmallMax; }
 
 size_t mx4_small_ws_bytes(int64_t M, int64_t K, int r) {
-  return static_cast<size_t>((K + slice_of(M) - 1) / slice_of(M)) * M * r * sizeof(float);
+  return static_cast<size_t>((K + kSlice - 1) / kSlice) * M * r * sizeof(float);
 }
 
 hipError_t launch_mx4_small_matmul(const Mx4View &X, const Mx4View &W, const uint16_t *T, const uint16_t *B, int r,
@@ -380,6 +402,26 @@ hipError_t launch_mx4_small_matmul(const Mx4View &X, const Mx4View &W, const uin
   return launch_main<false>(a, s);
 }
 
+hipError_t launch_mx4_prep(const uint16_t *X, const Mx4View &Xq, const uint16_t *A, int r, float scale, uint16_t *T,
+                           float *P, hipStream_t s) {
+  SmallArgs a{};
+  a.X = X;
+  a.A = A;
+  a.P = P;
+  a.Tout = T;
+  a.M = static_cast<int>(Xq.rows);
+  a.K = static_cast<int>(Xq.cols);
+  a.r = r;
+  a.slice = kSlice;
+  a.S = (a.K + a.slice - 1) / a.slice;
+  a.scale = scale;
+  const hipError_t e = launch_prep(a, Xq, s);
+  if (e != hipSuccess) return e;
+  const int64_t n = static_cast<int64_t>(a.M) * r;
+  hipLaunchKernelGGL(k_mx4_sum, dim3(static_cast<uint32_t>((n + 255) / 256)), dim3(256), 0, s, P, a.S, n, scale, T);
+  return hipGetLastError();
+}
+
 hipError_t launch_mx4_small_linear(const uint16_t *X, const Mx4View &W, const uint16_t *A, const uint16_t *B, int r,
                                    float scale, uint16_t *Y, uint16_t *Tout, float *P, const Mx4View &Xq, hipStream_t s) {
   SmallArgs a{};
@@ -397,20 +439,12 @@ hipError_t launch_mx4_small_linear(const uint16_t *X, const Mx4View &W, const ui
   a.N = static_cast<int>(W.rows);
   a.K = static_cast<int>(W.cols);
   a.r = r;
-  a.slice = slice_of(a.M);
+  a.slice = kSlice;
   a.S = (a.K + a.slice - 1) / a.slice;
   a.scale = scale;
   const bool fused = fused_ok(a);
-  const int downs = r > 0 ? a.S * ((r + 15) / 16) * ((a.M + 15) / 16) : 0;
-  const int64_t blocks = fused ? 0 : static_cast<int64_t>(a.M) * mx4_slabs(a.K) * 8;
-  const int64_t rounds = (blocks + kPrepWaves * 64 - 1) / (kPrepWaves * 64);
-  const dim3 grid(static_cast<uint32_t>(downs + rounds)), block(kPrepWaves * 64);
-  if (grid.x > 0) {
-    if (steps_of(a.M) == 2)
-      hipLaunchKernelGGL(k_mx4_prep<2>, grid, block, 0, s, a, downs, Xq.codes, Xq.scales);
-    else
-      hipLaunchKernelGGL(k_mx4_prep<4>, grid, block, 0, s, a, downs, Xq.codes, Xq.scales);
-    const hipError_t e = hipGetLastError();
+  if (!fused) {
+    const hipError_t e = launch_prep(a, Xq, s);
     if (e != hipSuccess) return e;
   }
   return fused ? launch_main<true>(a, s) : launch_main<false>(a, s);

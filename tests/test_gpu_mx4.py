@@ -198,6 +198,48 @@ def test_linear_forward(M, N, K, r):
     assert gy.intact()
 
 
+@pytest.mark.parametrize("M,N,K,r", [(75, 552, 8224, 64), (129, 203, 6656, 0), (70, 1001, 11008, 8), (200, 264, 5632, 100),
+                                     (300, 330, 8192, 33), (65, 1, 16384, 1), (128, 136, 22016, 64)])
+@pytest.mark.parametrize("keep", [False, True])
+def test_linear_forward_of_few_tiles(M, N, K, r, keep):
+    """Long contractions of few output tiles, T kept by the caller or not."""
+    X, W, A, B, _ = _linear_case(M, N, K, max(r, 1), M + N + K)
+    w = q.MX4Tensor.quantize(W.to(DEV))
+    wv, xv = mx4.quantized(_host64(W)), mx4.quantized(_host64(X))
+    gy, Y = guarded_like((M, N), BF16, 8)
+    want, size = xv @ wv.T, np.abs(xv) @ np.abs(wv).T
+    if r:
+        T = torch.empty(M, r, dtype=BF16, device=DEV) if keep else None
+        _, T = q.mx4_linear_fwd(X.to(DEV), w, A.to(DEV), B.to(DEV), 0.5, T_out=T, out=Y)
+        assert_close(as_f64(T), 0.5 * _host64(X) @ _host64(A).T, "T")
+        want, size = want + as_f64(T) @ _host64(B).T, size + np.abs(as_f64(T)) @ np.abs(_host64(B)).T
+    else:
+        q.mx4_linear_fwd(X.to(DEV), w, out=Y)
+    assert (np.abs(as_f64(Y) - want) <= _bound(want, size, K + r)).all()
+    assert gy.intact()
+    first = Y.clone()
+    q.mx4_linear_fwd(X.to(DEV), w, *((A.to(DEV), B.to(DEV), 0.5) if r else ()), out=Y)
+    assert torch.equal(first, Y)
+
+
+@pytest.mark.parametrize("M,N,K,r", [(2047, 72, 1056, 64), (2048, 136, 288, 64), (2050, 64, 1056, 5), (2081, 128, 320, 33),
+                                     (100, 264, 512, 100), (2100, 24, 96, 128), (65, 4104, 96, 0), (130, 33000, 64, 0),
+                                     (100, 66000, 32, 8)])
+def test_linear_forward_of_many_tokens(M, N, K, r):
+    """X rounded and multiplied by the adapter in one pass or by parts; large and small tiles."""
+    X, W, A, B, _ = _linear_case(M, N, K, max(r, 1), M + N + K)
+    w = q.MX4Tensor.quantize(W.to(DEV))
+    wv, xv = mx4.quantized(_host64(W)), mx4.quantized(_host64(X))
+    want, size = xv @ wv.T, np.abs(xv) @ np.abs(wv).T
+    if r:
+        Y, T = q.mx4_linear_fwd(X.to(DEV), w, A.to(DEV), B.to(DEV), 0.25)
+        assert_close(as_f64(T), 0.25 * _host64(X) @ _host64(A).T, "T")
+        want, size = want + as_f64(T) @ _host64(B).T, size + np.abs(as_f64(T)) @ np.abs(_host64(B)).T
+    else:
+        Y, _ = q.mx4_linear_fwd(X.to(DEV), w)
+    assert (np.abs(as_f64(Y) - want) <= _bound(want, size, K + r)).all()
+
+
 @pytest.mark.parametrize("M,N,K,r", [(1, 64, 64, 8), (40, 128, 320, 16), (300, 512, 768, 64), (129, 192, 4096, 33)])
 def test_linear_backward(M, N, K, r):
     X, W, A, B, dY = _linear_case(M, N, K, r, M + N)
