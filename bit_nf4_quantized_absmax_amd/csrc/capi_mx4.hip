@@ -48,13 +48,19 @@ int check_shape(int64_t M, int64_t N, int64_t K, int32_t r, bool bwd) {
   return QLORA_OK;
 }
 
-// How X's rounding and T are made, by measurement (r = 64): one pass over X
-// with 32 tokens a workgroup from kMx4RowsMin tokens on; below, where those
-// are too few to fetch X fast, partial sums from many workgroups (75 x 8224: 9.4
-// us and 41 in one pass; 1024 x 4096: 15 and 26; 2048 x 4096: 23 and 26; 4096 x
-// 4096: 42 and 27).  More adapter rows than the one pass holds: the LoRA
-// kernels' product and the codec.
-bool by_partials(int64_t M, int32_t r) { return r > 0 && (mx4_small_ok(M) || (r <= kMx4RowsMax && M < kMx4RowsMin)); }
+// How T and X's rounding are made above the decode sizes, by measurement (us,
+// both):              partial sums   LoRA product and codec   one pass
+//   75 x 8224, r 64         8.9               26.4               40.4
+//   512 x 4096, r 64       12.3               14.3               26.0
+//   1024 x 4096, r 64      15.7               14.7               26.2
+//   1536 x 4096, r 64      19.9               15.1               26.7
+//   1536 x 4096, r 8       12.2               14.8               14.7
+//   8192 x 4096, r 8                          31.2               23.2
+// Partial sums fetch X once per 16 adapter rows, and win while tokens times
+// such tiles are 4096 at most; from 2048 tokens on, one pass for a single tile.
+bool by_partials(int64_t M, int32_t r) {
+  return r > 0 && (mx4_small_ok(M) || (M < 2048 && M * ((r + 15) / 16) <= 4096));
+}
 
 // Workspace of the forward pass: T (when the caller keeps none) | partial sums
 // of T | X's codes | X's scales | the product's split tiles.

