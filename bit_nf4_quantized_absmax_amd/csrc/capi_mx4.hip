@@ -77,6 +77,16 @@ FwdWs fwd_ws(int64_t M, int64_t N, int64_t K, int32_t r) {
   return w;
 }
 
+// Workspace of a dX of few tiles, after the others: A^T | partial tiles.
+struct DxWs {
+  size_t at, total;
+};
+DxWs dx_ws(int64_t M, int64_t N, int64_t K, int32_t r) {
+  if (N % 64 != 0 || !mx4_dx_small_ok(M, N, K)) return DxWs{0, 0};
+  const size_t at = bf16_bytes(K * r);
+  return DxWs{at, at + mx4_dx_small_ws_bytes(M, N, K)};
+}
+
 }  // namespace
 
 extern "C" {
@@ -123,7 +133,7 @@ int qlora_mx4_matmul(const qlora_mx4_array *X, const qlora_mx4_array *W, const u
 size_t qlora_mx4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t r, int is_bwd) {
   if (M == 0 || check_shape(M, N, K, r, is_bwd != 0)) return 0;
   if (!is_bwd) return fwd_ws(M, N, K, r).total;
-  return bf16_bytes(N * K) + bwd_ws(M, N, K, r).total;
+  return bf16_bytes(N * K) + bwd_ws(M, N, K, r).total + dx_ws(M, N, K, r).total;
 }
 
 int qlora_mx4_linear_fwd(const uint16_t *X, int64_t M, const qlora_mx4_array *W, const uint16_t *A, const uint16_t *B,
@@ -170,7 +180,8 @@ int qlora_mx4_linear_bwd(const uint16_t *dY, const uint16_t *X, const uint16_t *
   const int64_t N = W->rows, K = W->cols;
   const BwdWs L = bwd_ws(M, N, K, r);
   const size_t wd_bytes = bf16_bytes(N * K);
-  if (!ws || !aligned(ws, 16) || ws_bytes < wd_bytes + L.total) return QLORA_ERR_WORKSPACE;
+  const DxWs D = dx_ws(M, N, K, r);
+  if (!ws || !aligned(ws, 16) || ws_bytes < wd_bytes + L.total + D.total) return QLORA_ERR_WORKSPACE;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int m = static_cast<int>(M), n = static_cast<int>(N), k = static_cast<int>(K);
   uint16_t *Wd = static_cast<uint16_t *>(ws);
@@ -181,7 +192,11 @@ int qlora_mx4_linear_bwd(const uint16_t *dY, const uint16_t *X, const uint16_t *
   void *pa = base + L.t + L.g + L.bt;
   void *pb = base + L.t + L.g + L.bt + L.pa;
   if ((dX || dA) && launch_lora_grad_in(dY, m, n, B, r, scale, G, bt, s) != hipSuccess) return QLORA_ERR_HIP;
-  if (dX) {
+  if (dX && D.total > 0) {
+    uint16_t *At = reinterpret_cast<uint16_t *>(base + L.total);
+    if (launch_mx4_transpose(view_of(W), A, r, Wd, At, s) != hipSuccess) return QLORA_ERR_HIP;
+    if (launch_mx4_dx_small(dY, Wd, G, At, m, n, k, r, dX, base + L.total + D.at, s) != hipSuccess) return QLORA_ERR_HIP;
+  } else if (dX) {
     if (launch_mx4_dequantize(view_of(W), Wd, s) != hipSuccess) return QLORA_ERR_HIP;
     const NF4View shape{nullptr, nullptr, nullptr, nullptr, n, k, 0};
     if (launch_pre_matmul_dx(MatmulJob{dY, G, A, nullptr, dX, shape, m, r, Wd}, s) != hipSuccess) return QLORA_ERR_HIP;

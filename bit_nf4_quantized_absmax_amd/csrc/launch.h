@@ -244,6 +244,15 @@ hipError_t launch_mx4_rows(const uint16_t *X, const Mx4View &Xq, const uint16_t 
 // 256 x 256 or 128 x 128 tiles, any M and N.
 // ws (nullable): mx4_split_ws_bytes, for few tiles of a long contraction.
 size_t mx4_split_ws_bytes(int64_t M, int64_t N, int64_t K);
+// dX [M, K] = dY W + G A of few output tiles, from Wt [K, N] = W^T and At [K, r] =
+// A^T in bf16, N % 64 == 0; ws: mx4_dx_small_ws_bytes.
+bool mx4_dx_small_ok(int64_t M, int64_t N, int64_t K);
+size_t mx4_dx_small_ws_bytes(int64_t M, int64_t N, int64_t K);
+hipError_t launch_mx4_dx_small(const uint16_t *dY, const uint16_t *Wt, const uint16_t *G, const uint16_t *At, int M, int N,
+                               int K, int r, uint16_t *dX, void *ws, hipStream_t s);
+// The values of W [N, K] transposed, Wt [K, N], and At = A^T of A [r, K]; N and K
+// multiples of 64.
+hipError_t launch_mx4_transpose(const Mx4View &W, const uint16_t *A, int r, uint16_t *Wt, uint16_t *At, hipStream_t s);
 hipError_t launch_mx4_matmul(const Mx4View &X, const Mx4View &W, const uint16_t *T, const uint16_t *B, int r,
                              uint16_t *Y, void *ws, hipStream_t s);
 

@@ -127,6 +127,52 @@ __global__ __launch_bounds__(kMxThreads) void k_mx4_dequantize(const uint8_t *__
   }
 }
 
+// 64 x 64 values of W transposed by way of LDS, or (workgroups from `tiles` on) up
+// to 64 rows by 64 columns of A.  4096 x 4096: 14.6 us (2.9 TB/s), in rows 8.1: whole
+// cache lines are stored, but a quarter of one is read at a time.
+__global__ __launch_bounds__(kMxThreads) void k_mx4_transpose(const uint8_t *__restrict__ codes,
+                                                              const uint8_t *__restrict__ scales, int64_t N, int64_t K,
+                                                              const uint16_t *__restrict__ A, int r, int64_t tiles,
+                                                              uint16_t *__restrict__ Wt, uint16_t *__restrict__ At) {
+  __shared__ __attribute__((aligned(16))) uint16_t sh[64][72];   // [column][row] and a skew
+  const int row = threadIdx.x >> 2, part = threadIdx.x & 3;
+  const int64_t cols = K / 64, slabs = (K + 255) / 256;
+  if (blockIdx.x < tiles) {
+    const int64_t n = blockIdx.x / cols * 64, k = blockIdx.x % cols * 64;
+    const uint2 c = *reinterpret_cast<const uint2 *>(codes + (n + row) * (slabs * 128) + k / 2 + 8 * part);
+    const int64_t block = k / 32 + (part >> 1);
+    const uint32_t byte = scales[(block / 8 * N + n + row) * 8 + block % 8];
+    const float f = mx4_scale(byte);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t code = h ? c.y : c.x;
+      uint32_t v[4];
+      v[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(code, f, 0));
+      v[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(code, f, 1));
+      v[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(code, f, 2));
+      v[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(code, f, 3));
+      if (byte == 255u) v[0] = v[1] = v[2] = v[3] = 0x7FC07FC0u;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sh[16 * part + 8 * h + e][row] = static_cast<uint16_t>(v[e >> 1] >> (16 * (e & 1)));
+    }
+    __syncthreads();
+    uint4 *out = reinterpret_cast<uint4 *>(Wt + (k + row) * N + n + 16 * part);
+    out[0] = *reinterpret_cast<const uint4 *>(&sh[row][16 * part]);
+    out[1] = *reinterpret_cast<const uint4 *>(&sh[row][16 * part + 8]);
+    return;
+  }
+  const int64_t at = blockIdx.x - tiles, k = at % cols * 64;
+  const int j0 = static_cast<int>(at / cols) * 64;
+  if (j0 + row < r) {
+    const uint16_t *a = A + static_cast<int64_t>(j0 + row) * K + k + 16 * part;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) sh[16 * part + e][row] = a[e];
+  }
+  __syncthreads();
+  for (int e = 0; e < 16; ++e)
+    if (j0 + 16 * part + e < r) At[(k + row) * r + j0 + 16 * part + e] = sh[row][16 * part + e];
+}
+
 namespace {
 
 // Workgroups of `each` rows of a slab.
@@ -152,6 +198,13 @@ hipError_t launch_mx4_quantize(const void *X, int in_type, const Mx4View &a, hip
 hipError_t launch_mx4_dequantize(const Mx4View &a, uint16_t *out, hipStream_t s) {
   hipLaunchKernelGGL(k_mx4_dequantize, mx4_grid(a, kMxGroups * kDeRows), dim3(kMxThreads), 0, s, a.codes, a.scales, a.rows,
                      a.cols, mx4_slabs(a.cols), out);
+  return hipGetLastError();
+}
+
+hipError_t launch_mx4_transpose(const Mx4View &W, const uint16_t *A, int r, uint16_t *Wt, uint16_t *At, hipStream_t s) {
+  const int64_t tiles = W.rows / 64 * (W.cols / 64);
+  hipLaunchKernelGGL(k_mx4_transpose, dim3(static_cast<uint32_t>(tiles + W.cols / 64 * ((r + 63) / 64))), dim3(kMxThreads), 0, s,
+                     W.codes, W.scales, W.rows, W.cols, A, r, tiles, Wt, At);
   return hipGetLastError();
 }
 

@@ -181,8 +181,9 @@ typedef uint4 __attribute__((aligned(2))) uint4_any;   // rows of an odd N start
 
 // kPiped: r == 64, the LoRA step runs in the pipeline.  kSplit: a workgroup has
 // one tile and a part of the contraction, and leaves its fp32 sums (the last
-// part's with the LoRA term) for k_mx4_join.
-template <int kFM, int kFN, bool kPiped, bool kSplit>
+// part's with the LoRA term) for k_mx4_join.  kBf16 (with kSplit): X and W are
+// bf16, every step is one of 64 columns on bf16 MFMA and there are no scales.
+template <int kFM, int kFN, bool kPiped, bool kSplit, bool kBf16 = false>
 __global__ __launch_bounds__(kMxMmThreads) void k_mx4_matmul(const Mx4Args args) {
   constexpr int kBM = 64 * kFM, kBN = 128 * kFN;
   constexpr int kHold = kFM / 2;                 // row fragments whose last products run after the barrier
@@ -218,7 +219,7 @@ __global__ __launch_bounds__(kMxMmThreads) void k_mx4_matmul(const Mx4Args args)
     const uint32_t pitch = static_cast<uint32_t>(KT) * 128;
     if (part & 1) dma_rows<kBM>(x, args.xc + static_cast<int64_t>(m0) * pitch + kt * 128, pitch, lastm, wave, lane);
     if (part & 2) dma_rows<kBN>(w, args.wc + static_cast<int64_t>(n0) * pitch + kt * 128, pitch, lastn, wave, lane);
-    if (part & 1)
+    if (!kBf16 && (part & 1))
 #pragma unroll
     for (int u = wave; u < (kBM + kBN) / 32; u += 8) {
       if (u < kBM / 32)
@@ -283,7 +284,7 @@ __global__ __launch_bounds__(kMxMmThreads) void k_mx4_matmul(const Mx4Args args)
 #pragma unroll
       for (int j = 0; j < kFN; ++j) {
         f32x16_t &c = acc[kFM - kHold + i][j];
-        c = mul1<false>(fb.a[kFM - kHold + i], fb.b[j], ha[i], hb[j], 3, c);
+        c = mul1<kBf16>(fb.a[kFM - kHold + i], fb.b[j], ha[i], hb[j], 3, c);
       }
     fetch(1);
     __builtin_amdgcn_sched_barrier(0);
@@ -331,12 +332,12 @@ __global__ __launch_bounds__(kMxMmThreads) void k_mx4_matmul(const Mx4Args args)
       else if (more)
         dma(st, m1, n1, k0, part);
     };
-    for (int kt = k0; kt < k1; ++kt) step(std::false_type(), [&](int part) __attribute__((always_inline)) { fetch(kt, part); });
+    for (int kt = k0; kt < k1; ++kt) step(std::bool_constant<kBf16>(), [&](int part) __attribute__((always_inline)) { fetch(kt, part); });
     if (kPiped && last) {
       step(std::true_type(), [&](int part) __attribute__((always_inline)) { fetch(KT, part); });
       mul<kFM - kHold, kFM, true>(fb, sc, 3, acc);
     } else {
-      mul<kFM - kHold, kFM, false>(fb, sc, 3, acc);
+      mul<kFM - kHold, kFM, kBf16>(fb, sc, 3, acc);
       // The stage just consumed takes T and B; the other one is being filled.
       for (int j0 = 0; !kPiped && last && j0 < r; j0 += 64) {
         stage_narrow<kBM>(smem + (st ? 0 : kStX), args.T, r, m0, M, j0);
@@ -494,7 +495,57 @@ hipError_t launch_tiles(Mx4Args a, int per_cu, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Parts of the contraction of dX, in steps of 64 columns.
+int dx_splits_of(int64_t M, int64_t N, int64_t K) {
+  const int64_t KT = N / 64;
+  return static_cast<int>(std::max<int64_t>(1, std::min(KT / 4, 384 / small_tiles(M, K))));
+}
+
 }  // namespace
+
+// While the small tiles all run at once: k_matmul_pre gives a large tile a whole
+// contraction, some 1.4 us a step of 64 columns however few there are.  Both with
+// the weight's decoding (and transposition here), us:
+//   128 x 4096 from 11008   57   233        1024 x 4096 from 4096   71   95
+//   707 x 256 from 3264     18    75        2048 x 4096 from 4096   91  105
+//   1470 x 960 from 1408    22    40        2048 x 4096 from 1024   39   37
+// Under 4 steps there is nothing to win (300 x 4096 from 192: 17.5 and 17.4).
+// Offsets of a tile's rows are 32-bit.
+bool mx4_dx_small_ok(int64_t M, int64_t N, int64_t K) {
+  return N >= 256 && N <= (int64_t{1} << 20) && small_tiles(M, K) <= 2 * kCUs;
+}
+
+size_t mx4_dx_small_ws_bytes(int64_t M, int64_t N, int64_t K) {
+  return mx4_dx_small_ok(M, N, K) ? static_cast<size_t>(dx_splits_of(M, N, K)) * small_tiles(M, K) * 128 * 128 * sizeof(float) : 0;
+}
+
+hipError_t launch_mx4_dx_small(const uint16_t *dY, const uint16_t *Wt, const uint16_t *G, const uint16_t *At, int M, int N,
+                               int K, int r, uint16_t *dX, void *ws, hipStream_t s) {
+  Mx4Args a{};
+  a.xc = reinterpret_cast<const uint8_t *>(dY);
+  a.wc = reinterpret_cast<const uint8_t *>(Wt);
+  a.T = G;
+  a.B = At;
+  a.Y = dX;
+  a.M = M;
+  a.N = K;
+  a.r = r;
+  a.KT = N / 64;
+  a.part = static_cast<float *>(ws);
+  a.splits = dx_splits_of(M, N, K);
+  a.trows = (M + 127) / 128;
+  a.tcols = (K + 127) / 128;
+  const int tiles = a.trows * a.tcols;
+  const dim3 grid(static_cast<uint32_t>(tiles * a.splits)), block(kMxMmThreads);
+  if (r == 64)
+    hipLaunchKernelGGL((k_mx4_matmul<2, 1, true, true, true>), grid, block, 0, s, a);
+  else
+    hipLaunchKernelGGL((k_mx4_matmul<2, 1, false, true, true>), grid, block, 0, s, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((k_mx4_join<2, 1>), dim3(static_cast<uint32_t>(tiles * 8)), dim3(512), 0, s, a);
+  return hipGetLastError();
+}
 
 size_t mx4_split_ws_bytes(int64_t M, int64_t N, int64_t K) {
   const int z = splits_of(M, N, K);

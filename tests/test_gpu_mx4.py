@@ -261,6 +261,26 @@ def test_linear_backward(M, N, K, r):
     assert_close(as_f64(only[1]), want[1], "dA alone")
 
 
+@pytest.mark.parametrize("M,N,K,r", [(69, 2240, 2560, 64), (75, 576, 1344, 33), (200, 1024, 192, 100), (1, 4096, 64, 8),
+                                     (513, 1344, 704, 64), (33, 22016, 128, 1), (128, 512, 320, 128), (65, 8192, 64, 64),
+                                     (1100, 256, 4096, 64), (700, 320, 2048, 16)])
+def test_linear_backward_of_few_tiles(M, N, K, r):
+    X, W, A, B, dY = _linear_case(M, N, K, r, M + N)
+    w = q.MX4Tensor.quantize(W.to(DEV))
+    scale = 8.0 / r
+    Xd, Ad, Bd, dYd = (t.to(DEV) for t in (X, A, B, dY))
+    want = olin.linear_bwd(*(t.contiguous().view(torch.int16).numpy().view(np.uint16) for t in (dY, X)),
+                           mx4.quantized(_host64(W)), *(t.contiguous().view(torch.int16).numpy().view(np.uint16) for t in (A, B)),
+                           scale)
+    gx, dX = guarded_like((M, K), BF16, 9)
+    got = q.mx4_linear_bwd(dYd, Xd, None, w, Ad, Bd, scale, dX_out=dX)
+    for name, a, b in zip(("dX", "dA", "dB"), got, want):
+        assert_close(as_f64(a), b, name)
+    assert gx.intact()
+    only = q.mx4_linear_bwd(dYd, Xd, None, w, Ad, Bd, scale, need_dA=False, need_dB=False)
+    assert torch.equal(only[0], got[0])
+
+
 def test_pair_gradients_against_differences():
     """Y is linear in A and in B, the codes of X fixed: central differences of
     sum(dY * Y), in float64 on the oracle's values, are exact up to rounding."""
