@@ -47,10 +47,6 @@ __device__ __forceinline__ float decode_absmax(float t8_level, float c2, float m
   return prod + mean;
 }
 
-// The scale 2^(byte - 127) of an MX4 block as the fp32 operand of the E2M1
-// conversions (byte 0 is the subnormal 2^-127).
-__device__ __forceinline__ float mx4_scale(uint32_t byte) { return u2f(byte == 0u ? 0x00400000u : byte << 23); }
-
 // Wave-wide (64-lane) reductions.
 __device__ __forceinline__ float wave_max(float v) {
 #pragma unroll

@@ -20,12 +20,4 @@ __device__ __forceinline__ void dma16(const void *src, uint32_t dst) {
   asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "{m0}"(dst) : "memory");
 }
 
-// The same from a uniform base and a 32-bit byte offset a lane; 4 bytes a lane.
-__device__ __forceinline__ void dma16(const void *base, uint32_t off, uint32_t dst) {
-  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(dst) : "memory");
-}
-__device__ __forceinline__ void dma4(const void *base, uint32_t off, uint32_t dst) {
-  asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(off), "s"(base), "{m0}"(dst) : "memory");
-}
-
 }  // namespace qlora

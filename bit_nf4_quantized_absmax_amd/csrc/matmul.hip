@@ -48,7 +48,6 @@
 #include "common.h"
 #include "launch.h"
 #include "lds_dma.h"
-#include "tile.h"
 
 namespace qlora {
 
@@ -85,10 +84,32 @@ constexpr int kBK = 64;                   // contraction step
 constexpr int kThreadsMM = 512;
 constexpr int kStageBytes = 256 * 64 * 2; // every stage holds 256 x 64 bf16
 
+// s_waitcnt immediate (gfx9 encoding: vmcnt bits 3:0 and 15:14, expcnt 6:4,
+// lgkmcnt 11:8); vm = 63 / lgkm = 15 do not wait.
+constexpr int wait_imm(int vm, int lgkm) { return (vm & 15) | ((vm >> 4) << 14) | 0x70 | ((lgkm & 15) << 8); }
+
+// 128-byte rows (64 bf16): chunk c of row r at 16-byte position c ^ f(r).
+__device__ __forceinline__ int swz128(int row, int chunk) {
+  return row * 128 + 16 * (chunk ^ ((row & 7) ^ ((row >> 3) & 1)));
+}
 // 512-byte rows (256 bf16): chunk c (0..31) of row r at c ^ g(r),
 // g(r) = 4 (r % 4) + (r / 4) % 4 (within the chunk's half row).
 __device__ __forceinline__ int swz512(int row, int chunk) {
   return row * 512 + 16 * (chunk ^ (((row & 3) << 2) | ((row >> 2) & 3)));
+}
+
+// Workgroup barrier without a memory-model fence (a fence would also wait for
+// every outstanding DMA and prefetch): waits per kWait, then s_barrier.  The
+// signal fences stop the compiler from moving memory accesses across it and
+// the scheduling barriers keep each side its own scheduling region.
+template <int kWait>
+__device__ __forceinline__ void raw_barrier() {
+  __builtin_amdgcn_sched_barrier(0);
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __builtin_amdgcn_s_waitcnt(kWait);
+  __builtin_amdgcn_s_barrier();
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __builtin_amdgcn_sched_barrier(0);
 }
 
 // Left operand tile: rows m0 .. m0+255 (clamped to rows - 1: never stored)

@@ -22,6 +22,7 @@
 // goes over them in two DPP steps.
 #include "common.h"
 #include "launch.h"
+#include "tile.h"
 
 namespace qlora {
 

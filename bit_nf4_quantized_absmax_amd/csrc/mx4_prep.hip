@@ -19,6 +19,7 @@
 // 27 against 19 for 4096 tokens, so they are not made here.
 #include "common.h"
 #include "launch.h"
+#include "tile.h"
 
 namespace qlora {
 

@@ -22,6 +22,7 @@
 
 #include "common.h"
 #include "launch.h"
+#include "tile.h"
 
 namespace qlora {
 

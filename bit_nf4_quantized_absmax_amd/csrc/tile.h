@@ -1,5 +1,6 @@
-// Helpers of the LDS-tiled MFMA kernels: wait counts, the operand tiles'
-// swizzle and the workgroup barrier.
+// Helpers of the MX4 kernels: wait counts, the operand tiles' swizzle and the
+// workgroup barrier (matmul.hip, whose sources a recorded profile covers, has its
+// own), block scales, DMA from a uniform base.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -27,6 +28,20 @@ __device__ __forceinline__ void raw_barrier() {
   __builtin_amdgcn_s_barrier();
   __atomic_signal_fence(__ATOMIC_SEQ_CST);
   __builtin_amdgcn_sched_barrier(0);
+}
+
+// The scale 2^(byte - 127) of an MX4 block as the fp32 operand of the E2M1
+// conversions (byte 0 is the subnormal 2^-127).
+__device__ __forceinline__ float mx4_scale(uint32_t byte) {
+  return __uint_as_float(byte == 0u ? 0x00400000u : byte << 23);
+}
+
+// dma16 of lds_dma.h from a uniform base and a 32-bit byte offset a lane; 4 bytes a lane.
+__device__ __forceinline__ void dma16(const void *base, uint32_t off, uint32_t dst) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(dst) : "memory");
+}
+__device__ __forceinline__ void dma4(const void *base, uint32_t off, uint32_t dst) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(off), "s"(base), "{m0}"(dst) : "memory");
 }
 
 }  // namespace qlora
