@@ -257,7 +257,7 @@ hipError_t launch_mx4_matmul(const Mx4View &X, const Mx4View &W, const uint16_t 
                              uint16_t *Y, void *ws, hipStream_t s);
 
 // M <= kMx4SmallMax.  P: mx4_small_ws_bytes(M, K, r), the LoRA partial sums;
-// Xq: storage for X in MX4 (written from 17 tokens on).
+// Xq: storage for X in MX4 (unused where the product's lanes round X).
 constexpr int64_t kMx4SmallMax = 64;
 bool mx4_small_ok(int64_t M);
 // Xq = Q(X) and T = bf16(scale X A^T) for any M by way of P, mx4_small_ws_bytes:

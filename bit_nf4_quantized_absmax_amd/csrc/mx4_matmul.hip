@@ -504,7 +504,7 @@ int dx_splits_of(int64_t M, int64_t N, int64_t K) {
 }  // namespace
 
 // While the small tiles all run at once: k_matmul_pre gives a large tile a whole
-// contraction, some 1.4 us a step of 64 columns however few there are.  Both with
+// contraction, 1.3 to 1.45 us a step of 64 columns however few tiles there are.  Both with
 // the weight's decoding (and transposition here), us:
 //   128 x 4096 from 11008   57   233        1024 x 4096 from 4096   71   95
 //   707 x 256 from 3264     18    75        2048 x 4096 from 4096   91  105

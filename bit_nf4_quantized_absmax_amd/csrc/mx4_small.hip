@@ -7,7 +7,7 @@
 // k_mx4_prep: partial sums P of X A^T, one workgroup per (slice of the
 //   columns, 16 adapter rows, 16 tokens); its 16 waves split the slice and are
 //   summed in LDS in wave order.  Further workgroups of the same launch round
-//   X to MX4.
+//   X to MX4.  With k_mx4_sum it also serves more tokens, ahead of the tiles.
 // k_mx4_small: one workgroup per 16 weight rows, its waves take slabs of 256
 //   columns in turn: v_mfma_scale_f32_16x16x128 with W as the left operand
 //   (lane l: row l % 16, block l / 16 of 128 columns) and 16 tokens a product
