@@ -259,14 +259,19 @@ struct Held {
 };
 
 // 2^t of the words, t = (z - a) c.  One fused multiply-add by r = fl(a c);
-// dr = a c - r is what that rounding changed, the same for every word.  Where
-// a c leaves fp32 (a = the lowest value of a type) the difference comes first.
+// dr = a c - r is what that rounding changed, the same for every word, and the
+// sums are relative to 2^dr (see corrected).  Up to |r| = kNear |dr| is 2^-9 at
+// most, so nothing leaves fp32's range and the correction costs no digits.
+// Beyond (masks by a finite value of any size, small temperatures) the
+// difference comes first, which is as exact and one operation more; the choice
+// is the same for a whole workgroup.
+constexpr float kNear = 65536.f;
 struct Exps {
   float a, c, r, dr;
   bool far;
   __device__ __forceinline__ Exps(float zmax, float scale) : a(zmax == -INFINITY ? 0.f : zmax), c(scale) {
     r = a * c;
-    far = !(fabsf(r) < 1e38f);
+    far = !(fabsf(r) < kNear);
     dr = far ? 0.f : __builtin_fmaf(a, c, -r);
   }
   template <bool kFar>
