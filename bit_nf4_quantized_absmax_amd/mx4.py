@@ -126,7 +126,8 @@ def mx4_linear_bwd(dY, X, T, w, A, B, scale, need_dX=True, need_dA=True, need_dB
                    dX_out=None, dA_out=None, dB_out=None):
     """(dX, dA, dB) of mx4_linear_fwd with a LoRA pair (None where not
     requested); T as returned by it, or None (recomputed).  The rounding of X
-    passes its gradient straight through."""
+    passes its gradient straight through.  Without tokens dA and dB are zero,
+    also where the caller gave their storage."""
     if A is None or B is None:
         raise ValueError("the backward pass needs a LoRA pair")
     M, N, K, r = _checks(X, w, A, B)
@@ -142,6 +143,10 @@ def mx4_linear_bwd(dY, X, T, w, A, B, scale, need_dX=True, need_dA=True, need_dB
     check(lib().qlora_mx4_linear_bwd(_ptr(dY), _ptr(X), _ptr(T), M, ctypes.byref(st), _ptr(A), _ptr(B), r,
                                      float(scale), _ptr(dX), _ptr(dA), _ptr(dB), _ptr(ws), ws_bytes, _stream(X)),
           "qlora_mx4_linear_bwd")
+    if M == 0:   # the call above writes nothing then
+        for d in (dA, dB):
+            if d is not None:
+                d.zero_()
     return dX, dA, dB
 
 

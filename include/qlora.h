@@ -567,7 +567,8 @@ int qlora_mx4_linear_fwd(const uint16_t *X, int64_t M, const qlora_mx4_array *W,
  * and dA reads the unrounded X, which the LoRA branch read.  dX multiplies
  * W's bf16 values (expanded into the workspace).  r >= 1, K % 64 == 0,
  * N % 8 == 0 and, for dX, N % 64 == 0; outputs and T nullable as there (a
- * recomputed T may round differently from the forward's). */
+ * recomputed T may round differently from the forward's).  M = 0 writes
+ * nothing: dA and dB, then zero, are left as they were. */
 int qlora_mx4_linear_bwd(const uint16_t *dY, const uint16_t *X, const uint16_t *T, int64_t M, const qlora_mx4_array *W,
                          const uint16_t *A, const uint16_t *B, int32_t r, float scale, uint16_t *dX, uint16_t *dA,
                          uint16_t *dB, void *ws, size_t ws_bytes, void *stream);

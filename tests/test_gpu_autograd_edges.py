@@ -1,0 +1,47 @@
+"""The MX4 and vocabulary operators where a training loop goes beyond one plain
+step: a batch without tokens."""
+
+import pytest
+import torch
+
+import bit_nf4_quantized_absmax_amd as q
+from tests.gpu_util import DEV
+
+pytestmark = pytest.mark.gpu
+
+BF16 = torch.bfloat16
+
+
+def _dirty(*shapes):
+    """Leaves freed memory of these shapes behind that holds no zeros."""
+    held = [torch.full(s, float("nan"), dtype=BF16, device=DEV) for s in shapes]
+    del held
+
+
+def _pair(N, K, r):
+    g = torch.Generator().manual_seed(N + K)
+    W, A, B = torch.randn(N, K, generator=g), torch.randn(r, K, generator=g), torch.randn(N, r, generator=g)
+    return q.MX4Linear(W.to(DEV), r, 8.0, A.to(BF16).to(DEV), B.to(BF16).to(DEV))
+
+
+@pytest.mark.parametrize("N,K,r", [(128, 320, 8), (4096, 4096, 64)])
+def test_no_tokens_have_zero_gradients(N, K, r):
+    """A batch (an expert, a micro-batch) without tokens adds nothing to the adapter's gradients."""
+    lin = _pair(N, K, r)
+    x = torch.empty(0, K, dtype=BF16, device=DEV, requires_grad=True)
+    _dirty((r, K), (N, r))
+    lin(x).sum().backward()
+    assert x.grad.shape == (0, K)
+    assert lin.lora_A.grad.shape == (r, K) and not lin.lora_A.grad.any()
+    assert lin.lora_B.grad.shape == (N, r) and not lin.lora_B.grad.any()
+
+
+def test_no_tokens_into_given_gradients():
+    lin = _pair(128, 320, 8)
+    A, B = lin.lora_A.detach(), lin.lora_B.detach()
+    x, dy = (torch.empty(0, n, dtype=BF16, device=DEV) for n in (320, 128))
+    dA, dB = torch.ones_like(A), torch.ones_like(B)
+    got = q.mx4_linear_bwd(dy, x, None, lin.w, A, B, 1.0, dA_out=dA, dB_out=dB)
+    assert got[1] is dA and got[2] is dB and not dA.any() and not dB.any()
+    got = q.mx4_linear_bwd(dy, x, None, lin.w, A, B, 1.0, need_dX=False, need_dB=False)
+    assert got[0] is None and got[2] is None and not got[1].any()
