@@ -159,9 +159,11 @@ __device__ __forceinline__ float block_max(float v, float *sh) {
   for (int w = 1; w < static_cast<int>(blockDim.x >> 6); ++w) m = fmaxf(m, sh[w]);
   return m;
 }
-// Order-preserving integer of a float (-0 as +0; a NaN above or below all).
+// Order-preserving integer of a float (-0 as +0).  A NaN counts as -inf, as in
+// the maxima, which pass over it: every word can be an alternative, and a row
+// always has enough of them.
 __device__ __forceinline__ uint32_t ordered(float v) {
-  const uint32_t b = __float_as_uint(v + 0.f);
+  const uint32_t b = __float_as_uint(v == v ? v + 0.f : -INFINITY);
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 // A word as a key: larger for a larger logit, then for a lower index.

@@ -581,8 +581,8 @@ int qlora_mx4_linear_bwd(const uint16_t *dY, const uint16_t *X, const uint16_t *
  *
  * A row of logits z has p = softmax(z).  A word that is masked out is -inf.
  * In a row that is all -inf: log probabilities -inf, entropy 0, gradients 0.
- * A NaN or +inf makes its row's numbers NaN (the alternatives' indices stay
- * inside the row).  Sums are fp32 over at most 16384 words, joined in 64
+ * A NaN or +inf makes its row's numbers NaN (its alternatives are still `top`
+ * different words of the row, a NaN ranked as -inf).  Sums are fp32 over at most 16384 words, joined in 64
  * bits; gradients are rounded once to the logits' type. */
 
 /* Logits [rows, words] of `type` (0: fp32, else QLORA_IN_BF16 or
