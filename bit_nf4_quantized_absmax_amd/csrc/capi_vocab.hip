@@ -10,10 +10,15 @@ namespace {
 
 int elem_bytes(int32_t type) { return type == 0 ? 4 : 2; }
 
+// A kernel's offsets within a row: bytes in 32 bits, words in 31, up to a
+// gradient workgroup's part (less than 2^23 bytes) past its end.
+constexpr int64_t kMaxRowBytes = (int64_t{1} << 32) - (int64_t{1} << 24);
+
 int check_rows(int32_t type, int64_t M, int64_t V) {
   if (type < 0 || type > QLORA_IN_FP16 || M < 0 || V < 1) return QLORA_ERR_INVALID_ARG;
+  if (V > kMaxRowBytes / elem_bytes(type)) return QLORA_ERR_UNSUPPORTED_SHAPE;
   // the grids: slices of at least 2048 words, gradient chunks of at least 4096
-  if (V > kMaxElems - 64 || (M > 0 && (V + 8) / 2048 + 1 > kMaxElems / M)) return QLORA_ERR_UNSUPPORTED_SHAPE;
+  if (M > 0 && (V + 8) / 2048 + 1 > kMaxElems / M) return QLORA_ERR_UNSUPPORTED_SHAPE;
   return QLORA_OK;
 }
 

@@ -588,7 +588,8 @@ int qlora_mx4_linear_bwd(const uint16_t *dY, const uint16_t *X, const uint16_t *
 /* Logits [rows, words] of `type` (0: fp32, else QLORA_IN_BF16 or
  * QLORA_IN_FP16), row m at z + m * pitch elements (pitch >= words: padded
  * vocabularies, columns of a larger matrix).  z needs only its element's
- * alignment; rows that start on 16 bytes are fastest. */
+ * alignment; rows that start on 16 bytes are fastest.  A row of more than
+ * 2^32 - 2^24 bytes is an UNSUPPORTED_SHAPE. */
 typedef struct {
   const void *z;
   int32_t type;
