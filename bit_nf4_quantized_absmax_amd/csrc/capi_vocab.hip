@@ -14,13 +14,21 @@ int elem_bytes(int32_t type) { return type == 0 ? 4 : 2; }
 // gradient workgroup's part (less than 2^23 bytes) past its end.
 constexpr int64_t kMaxRowBytes = (int64_t{1} << 32) - (int64_t{1} << 24);
 
+// HIP counts the threads of a launch in 32 bits.
+constexpr int64_t kMaxThreads = (int64_t{1} << 32) - 1;
+
 int check_rows(int32_t type, int64_t M, int64_t V) {
   if (type < 0 || type > QLORA_IN_FP16 || M < 0 || V < 1) return QLORA_ERR_INVALID_ARG;
-  if (V > kMaxRowBytes / elem_bytes(type)) return QLORA_ERR_UNSUPPORTED_SHAPE;
-  // the grids: slices of at least 2048 words, gradient chunks of at least 4096
-  if (M > 0 && (V + 8) / 2048 + 1 > kMaxElems / M) return QLORA_ERR_UNSUPPORTED_SHAPE;
+  if (V > kMaxRowBytes / elem_bytes(type) || M > kMaxThreads) return QLORA_ERR_UNSUPPORTED_SHAPE;
   return QLORA_OK;
 }
+
+// Whether the launch of M rows of so many threads can be counted.
+bool launch_ok(int64_t M, int64_t row_threads) { return M <= kMaxThreads / row_threads; }
+
+bool sums_ok(int32_t type, int64_t M, int64_t V, int32_t top) { return M == 0 || launch_ok(M, vocab_row_threads(M, V, type, top)); }
+
+bool distill_bwd_ok(int32_t type, int64_t M, int64_t V) { return M == 0 || launch_ok(M, distill_bwd_row_threads(M, V, type)); }
 
 // Logits (or their gradient): pitch, presence and the element's alignment.
 int check_matrix(const void *p, int32_t type, int64_t M, int64_t V, int64_t ld) {
@@ -58,6 +66,7 @@ extern "C" {
 
 size_t qlora_vocab_workspace_bytes(int32_t type, int64_t rows, int64_t words, int32_t top) {
   if (check_rows(type, rows, words) || rows == 0 || top < 0 || top > kTopMax || top > words) return 0;
+  if (!sums_ok(type, rows, words, top)) return 0;
   return vocab_ws_bytes(rows, words, type, top);
 }
 
@@ -66,7 +75,7 @@ int qlora_token_logprobs(const qlora_logits *l, const int64_t *target, int32_t t
   const int st = check_logits(l);
   if (st) return st;
   const int64_t M = l->rows;
-  if (top < 0 || top > kTopMax || top > l->words) return QLORA_ERR_UNSUPPORTED_SHAPE;
+  if (top < 0 || top > kTopMax || top > l->words || !sums_ok(l->type, M, l->words, top)) return QLORA_ERR_UNSUPPORTED_SHAPE;
   if (!present(target, M, 8) || !present(logprob, M, 4) || !present(entropy, M, 4) || !present(lse, M, 4))
     return QLORA_ERR_INVALID_ARG;
   if (top > 0 && (!present(top_logprob, M, 4) || !present(top_index, M, 8))) return QLORA_ERR_INVALID_ARG;
@@ -82,6 +91,7 @@ int qlora_token_logprobs_bwd(const qlora_logits *l, const int64_t *target, const
   if (!st) st = check_matrix(dz, l->type, l->rows, l->words, dz_pitch);
   if (st) return st;
   const int64_t M = l->rows;
+  if (!launch_ok(M, logprobs_bwd_row_threads(l->words, l->type))) return QLORA_ERR_UNSUPPORTED_SHAPE;
   if (!present(target, M, 8) || !present(lse, M, 4) || !present(entropy, M, 4) || !aligned(g_logprob, 4) ||
       !aligned(g_entropy, 4))
     return QLORA_ERR_INVALID_ARG;
@@ -96,6 +106,7 @@ int qlora_distill_fwd(const qlora_logits *l, const qlora_teacher *t, float *loss
   if (!st) st = check_teacher(t, l->rows);
   if (st) return st;
   const int64_t M = l->rows;
+  if (!sums_ok(l->type, M, l->words, 0)) return QLORA_ERR_UNSUPPORTED_SHAPE;
   if (!present(loss, M, 4) || !present(lse, M, 4)) return QLORA_ERR_INVALID_ARG;
   if (M == 0) return QLORA_OK;
   if (!ws_ok(ws, ws_bytes, vocab_ws_bytes(M, l->words, l->type, 0))) return QLORA_ERR_WORKSPACE;
@@ -108,6 +119,7 @@ int qlora_distill_bwd(const qlora_logits *l, const qlora_teacher *t, const float
   if (!st) st = check_teacher(t, l->rows);
   if (!st) st = check_matrix(dz, l->type, l->rows, l->words, dz_pitch);
   if (st) return st;
+  if (!distill_bwd_ok(l->type, l->rows, l->words)) return QLORA_ERR_UNSUPPORTED_SHAPE;
   if (!present(lse, l->rows, 4) || !aligned(weight, 4)) return QLORA_ERR_INVALID_ARG;
   if (l->rows == 0) return QLORA_OK;
   return from_hip(
@@ -121,6 +133,7 @@ int qlora_distill(const qlora_logits *l, const qlora_teacher *t, const float *we
   if (!st) st = check_matrix(dz, l->type, l->rows, l->words, dz_pitch);
   if (st) return st;
   const int64_t M = l->rows;
+  if (!sums_ok(l->type, M, l->words, 0) || !distill_bwd_ok(l->type, M, l->words)) return QLORA_ERR_UNSUPPORTED_SHAPE;
   if (!present(loss, M, 4) || !present(lse, M, 4) || !aligned(weight, 4)) return QLORA_ERR_INVALID_ARG;
   if (M == 0) return QLORA_OK;
   if (!ws_ok(ws, ws_bytes, vocab_ws_bytes(M, l->words, l->type, 0))) return QLORA_ERR_WORKSPACE;

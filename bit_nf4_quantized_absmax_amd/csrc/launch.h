@@ -282,6 +282,11 @@ struct Logits {
 constexpr int kTopMax = 64;        // alternatives of a token
 constexpr int kDistillMax = 256;   // teacher logits of a token
 size_t vocab_ws_bytes(int64_t M, int64_t V, int type, int top);
+// Threads that a row (M >= 1 of them) takes of the largest launch of the
+// operators that sum rows, and of each gradient's.
+int64_t vocab_row_threads(int64_t M, int64_t V, int type, int top);
+int64_t logprobs_bwd_row_threads(int64_t V, int type);
+int64_t distill_bwd_row_threads(int64_t M, int64_t V, int type);
 hipError_t launch_token_logprobs(const Logits &l, const int64_t *target, int top, float *logprob, float *entropy,
                                  float *lse, float *top_logprob, int64_t *top_index, void *ws, hipStream_t s);
 hipError_t launch_token_logprobs_bwd(const Logits &l, const int64_t *target, const float *lse, const float *entropy,

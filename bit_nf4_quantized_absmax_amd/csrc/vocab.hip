@@ -1140,15 +1140,19 @@ hipError_t distill_fwd_as(const Logits &l, const Teacher &t, float *loss, float 
   return hipGetLastError();
 }
 
-// The teacher's list is worked out once a workgroup: the whole row in one,
-// down to kGradVecs vectors where there are few rows.
+// Steps of kGradVecs vectors of a workgroup: the teacher's list is worked out
+// once in each, so the whole row, down to one step where there are few rows.
+template <typename T>
+int distill_steps(int64_t M, int64_t V) {
+  const int most = grad_chunks<T>(V);
+  const int64_t want = std::min<int64_t>(most, std::max<int64_t>(1, 2048 / M));
+  return static_cast<int>((most + want - 1) / want);
+}
+
 template <typename T>
 hipError_t distill_bwd_as(const Logits &l, const Teacher &t, const float *lse, const float *weight, void *dz,
                           int64_t ldd, hipStream_t s) {
-  const int most = grad_chunks<T>(l.V);
-  const int64_t want = std::max<int64_t>(1, 2048 / l.M);
-  const int steps = static_cast<int>((most + std::min<int64_t>(most, want) - 1) / std::min<int64_t>(most, want));
-  const int chunks = (most + steps - 1) / steps;
+  const int steps = distill_steps<T>(l.M, l.V), chunks = (grad_chunks<T>(l.V) + steps - 1) / steps;
   hipLaunchKernelGGL(k_distill_bwd<T>, dim3(static_cast<uint32_t>(l.M * chunks)), dim3(kVThreads), 0, s,
                      static_cast<const T *>(l.z), static_cast<int>(l.V), l.ld, chunks, steps * kGradVecs,
                      scaled_log2e(t.temperature), t, lse, weight, static_cast<T *>(dz), ldd);
@@ -1198,6 +1202,19 @@ hipError_t launch_distill_bwd(const Logits &l, const Teacher &t, const float *ls
 hipError_t launch_distill(const Logits &l, const Teacher &t, const float *weight, float *loss, float *lse, void *dz,
                           int64_t ldd, void *ws, hipStream_t s) {
   QLORA_BY_TYPE(l.type, distill_as<T>(l, t, weight, loss, lse, dz, ldd, ws, s))
+}
+
+int64_t vocab_row_threads(int64_t M, int64_t V, int type, int top) {
+  const Slices a = slices_of(M, V, type, top, true), b = slices_of(M, V, type, top, false);
+  return std::max(int64_t{a.S} * a.threads, int64_t{b.S} * b.threads);
+}
+
+int64_t logprobs_bwd_row_threads(int64_t V, int type) {
+  QLORA_BY_TYPE(type, int64_t{grad_chunks<T>(V)} * kVThreads)
+}
+
+int64_t distill_bwd_row_threads(int64_t M, int64_t V, int type) {
+  QLORA_BY_TYPE(type, int64_t{(grad_chunks<T>(V) + distill_steps<T>(M, V) - 1) / distill_steps<T>(M, V)} * kVThreads)
 }
 
 #undef QLORA_BY_TYPE

@@ -589,7 +589,8 @@ int qlora_mx4_linear_bwd(const uint16_t *dY, const uint16_t *X, const uint16_t *
  * QLORA_IN_FP16), row m at z + m * pitch elements (pitch >= words: padded
  * vocabularies, columns of a larger matrix).  z needs only its element's
  * alignment; rows that start on 16 bytes are fastest.  A row of more than
- * 2^32 - 2^24 bytes is an UNSUPPORTED_SHAPE. */
+ * 2^32 - 2^24 bytes is an UNSUPPORTED_SHAPE, and so are 2^24 rows and more
+ * (fewer where a row takes over 256 threads: a launch holds 2^32 - 1). */
 typedef struct {
   const void *z;
   int32_t type;

@@ -38,3 +38,25 @@ def test_rows_past_32_bit_offsets(type, size):
         if words > most:
             assert set(_calls(type, 1, words).values()) == {SHAPE}, words
             assert q.lib().qlora_vocab_workspace_bytes(type, 1, words, 0) == 0
+
+
+@pytest.mark.parametrize("type", [FP32, BF16, FP16])
+def test_rows_past_a_launch(type):
+    """A launch holds 2^32 - 1 threads, 256 a row at least."""
+    query = q.lib().qlora_vocab_workspace_bytes
+    assert set(_calls(type, (1 << 24) - 1, 1000).values()) == {INVALID}
+    assert set(_calls(type, 1 << 24, 1000).values()) == {SHAPE}
+    assert set(_calls(type, 1 << 40, 1000).values()) == {SHAPE}
+    assert set(_calls(type, (1 << 63) - 1, 1).values()) == {SHAPE}
+    # rows in slices: as many workgroups of 256 threads as their 2048 vectors fill
+    n = 4 if type == FP32 else 8
+    slices = -(-(200000 // n) // 2048)
+    most = ((1 << 32) - 1) // (256 * slices)
+    assert query(type, most // 2, 200000, 64) > 0
+    assert query(type, most + 1, 200000, 64) == 0 and query(type, 1 << 30, 200000, 0) == 0
+    assert _calls(type, most + 1, 200000, 64)["logprobs"] == SHAPE
+    # a gradient workgroup takes 1024 vectors; the distillation's takes a whole row where there are many
+    chunks = -(-200000 // n // 1024)
+    most = ((1 << 32) - 1) // (256 * chunks)
+    got = _calls(type, most + 1, 200000)
+    assert got["logprobs_bwd"] == SHAPE and got["distill_bwd"] == INVALID
