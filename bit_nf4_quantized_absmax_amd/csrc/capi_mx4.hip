@@ -17,7 +17,6 @@ constexpr int64_t kMaxCols = int64_t{1} << 24;   // 256 rows of codes stay withi
 int check_mx4_shape(int64_t rows, int64_t cols, bool empty_ok) {
   if (rows < (empty_ok ? 0 : 1) || cols < 1) return QLORA_ERR_INVALID_ARG;
   if (cols % 32 != 0 || rows > kMaxElems || cols > kMaxCols) return QLORA_ERR_UNSUPPORTED_SHAPE;
-  if ((rows + 7) / 8 > kMaxElems / mx4_slabs(cols)) return QLORA_ERR_UNSUPPORTED_SHAPE;   // the codec's grid
   return QLORA_OK;
 }
 
@@ -34,8 +33,8 @@ Mx4View view_of(const qlora_mx4_array *a) { return Mx4View{a->codes, a->scales, 
 size_t code_bytes(int64_t rows, int64_t cols) { return static_cast<size_t>(rows) * mx4_slabs(cols) * 128; }
 size_t scale_bytes(int64_t rows, int64_t cols) { return static_cast<size_t>(rows) * mx4_slabs(cols) * 8; }
 
-// Shape rules of the linear layer: the codec's for X and W, an optional LoRA
-// pair of rank r (0: none) and the LoRA kernels' size limit with it.
+// Shape rules of a product and of the linear layer: the arrays' for X and W, an
+// optional LoRA pair of rank r (0: none) and the LoRA kernels' size limit with it.
 int check_shape(int64_t M, int64_t N, int64_t K, int32_t r, bool bwd) {
   if (M < 0) return QLORA_ERR_INVALID_ARG;
   int st = check_mx4_shape(N, K, false);
@@ -43,9 +42,16 @@ int check_shape(int64_t M, int64_t N, int64_t K, int32_t r, bool bwd) {
   if (st) return st;
   if (r < 0 || r > 128 || (bwd && r < 1)) return QLORA_ERR_UNSUPPORTED_SHAPE;
   if (bwd && (K % 64 != 0 || N % 8 != 0 || N > kMaxElems / K)) return QLORA_ERR_UNSUPPORTED_SHAPE;
-  if ((M + 127) / 128 * ((N + 127) / 128) > kMaxElems) return QLORA_ERR_UNSUPPORTED_SHAPE;   // the product's grid
+  if ((M + 127) / 128 * ((N + 127) / 128) > kMaxElems) return QLORA_ERR_UNSUPPORTED_SHAPE;   // the product's tiles
+  if (mx4_small_ok(M) && !mx4_small_launch_ok(N)) return QLORA_ERR_UNSUPPORTED_SHAPE;
   if (r > 0 && M > 0 && M > kMaxElems / std::max(N, K)) return QLORA_ERR_UNSUPPORTED_SHAPE;
   return QLORA_OK;
+}
+
+// The linear layer's: X is rounded here.
+int check_linear(int64_t M, int64_t N, int64_t K, int32_t r, bool bwd) {
+  const int st = check_shape(M, N, K, r, bwd);
+  return st || mx4_quantize_ok(M, K) ? st : QLORA_ERR_UNSUPPORTED_SHAPE;
 }
 
 // How T and X's rounding are made above the decode sizes, by measurement (us,
@@ -102,6 +108,7 @@ int qlora_mx4_sizes(int64_t rows, int64_t cols, int64_t *codes, int64_t *scales)
 int qlora_mx4_quantize(const void *X, int32_t in_type, const qlora_mx4_array *out, void *stream) {
   const int st = check_mx4(out, true);
   if (st) return st;
+  if (!mx4_quantize_ok(out->rows, out->cols)) return QLORA_ERR_UNSUPPORTED_SHAPE;
   if (in_type < 0 || in_type > QLORA_IN_FP16 || !rows_ok(X, out->rows)) return QLORA_ERR_INVALID_ARG;
   if (out->rows == 0) return QLORA_OK;
   return from_hip(launch_mx4_quantize(X, in_type, view_of(out), static_cast<hipStream_t>(stream)));
@@ -110,6 +117,7 @@ int qlora_mx4_quantize(const void *X, int32_t in_type, const qlora_mx4_array *ou
 int qlora_mx4_dequantize(const qlora_mx4_array *a, uint16_t *out_bf16, void *stream) {
   const int st = check_mx4(a, true);
   if (st) return st;
+  if (!mx4_dequantize_ok(a->rows, a->cols)) return QLORA_ERR_UNSUPPORTED_SHAPE;
   if (!rows_ok(out_bf16, a->rows)) return QLORA_ERR_INVALID_ARG;
   if (a->rows == 0) return QLORA_OK;
   return from_hip(launch_mx4_dequantize(view_of(a), out_bf16, static_cast<hipStream_t>(stream)));
@@ -131,7 +139,7 @@ int qlora_mx4_matmul(const qlora_mx4_array *X, const qlora_mx4_array *W, const u
 }
 
 size_t qlora_mx4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t r, int is_bwd) {
-  if (M == 0 || check_shape(M, N, K, r, is_bwd != 0)) return 0;
+  if (M == 0 || check_linear(M, N, K, r, is_bwd != 0)) return 0;
   if (!is_bwd) return fwd_ws(M, N, K, r).total;
   return bf16_bytes(N * K) + bwd_ws(M, N, K, r).total + dx_ws(M, N, K, r).total;
 }
@@ -139,7 +147,7 @@ size_t qlora_mx4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t
 int qlora_mx4_linear_fwd(const uint16_t *X, int64_t M, const qlora_mx4_array *W, const uint16_t *A, const uint16_t *B,
                          int32_t r, float scale, uint16_t *Y, uint16_t *T_out, void *ws, size_t ws_bytes, void *stream) {
   int st = check_mx4(W, false);
-  if (!st) st = check_shape(M, W->rows, W->cols, r, false);
+  if (!st) st = check_linear(M, W->rows, W->cols, r, false);
   if (st) return st;
   if (!rows_ok(X, M) || !rows_ok(Y, M)) return QLORA_ERR_INVALID_ARG;
   if (r > 0 && (!bf16_ok(A) || !bf16_ok(B) || !bf16_opt(T_out) || !isfinite(scale))) return QLORA_ERR_INVALID_ARG;
@@ -171,7 +179,7 @@ int qlora_mx4_linear_bwd(const uint16_t *dY, const uint16_t *X, const uint16_t *
                          const uint16_t *A, const uint16_t *B, int32_t r, float scale, uint16_t *dX, uint16_t *dA,
                          uint16_t *dB, void *ws, size_t ws_bytes, void *stream) {
   int st = check_mx4(W, false);
-  if (!st) st = check_shape(M, W->rows, W->cols, r, true);
+  if (!st) st = check_linear(M, W->rows, W->cols, r, true);
   if (st) return st;
   if (dX && W->rows % 64 != 0) return QLORA_ERR_UNSUPPORTED_SHAPE;
   if (!rows_ok(dY, M) || !rows_ok(X, M) || !bf16_ok(A) || !bf16_ok(B) || !isfinite(scale)) return QLORA_ERR_INVALID_ARG;

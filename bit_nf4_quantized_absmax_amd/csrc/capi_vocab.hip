@@ -14,9 +14,6 @@ int elem_bytes(int32_t type) { return type == 0 ? 4 : 2; }
 // gradient workgroup's part (less than 2^23 bytes) past its end.
 constexpr int64_t kMaxRowBytes = (int64_t{1} << 32) - (int64_t{1} << 24);
 
-// HIP counts the threads of a launch in 32 bits.
-constexpr int64_t kMaxThreads = (int64_t{1} << 32) - 1;
-
 int check_rows(int32_t type, int64_t M, int64_t V) {
   if (type < 0 || type > QLORA_IN_FP16 || M < 0 || V < 1) return QLORA_ERR_INVALID_ARG;
   if (V > kMaxRowBytes / elem_bytes(type) || M > kMaxThreads) return QLORA_ERR_UNSUPPORTED_SHAPE;

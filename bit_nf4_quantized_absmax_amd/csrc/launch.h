@@ -221,6 +221,9 @@ size_t lora_grad_pair_ws_bytes(int M, int D, int K, int N, int r);
 hipError_t launch_lora_grad_w(const uint16_t *P, const uint16_t *Q, int M, int D, int r, bool out_r_major,
                               uint16_t *out, void *ws, hipStream_t s);
 
+// HIP counts the threads of a launch in 32 bits.
+constexpr int64_t kMaxThreads = (int64_t{1} << 32) - 1;
+
 // ---- MX4 arrays: codec -----------------------------------------------------------
 // codes [rows][Kp / 2], scales [Kp / 256][rows][8], Kp = cols filled up to a
 // multiple of 256; cols % 32 == 0.
@@ -231,6 +234,8 @@ struct Mx4View {
   int64_t cols;
 };
 inline int64_t mx4_slabs(int64_t cols) { return (cols + 255) / 256; }
+bool mx4_quantize_ok(int64_t rows, int64_t cols);     // whether the launch can be counted
+bool mx4_dequantize_ok(int64_t rows, int64_t cols);
 hipError_t launch_mx4_quantize(const void *X, int in_type, const Mx4View &a, hipStream_t s);
 hipError_t launch_mx4_dequantize(const Mx4View &a, uint16_t *out, hipStream_t s);
 
@@ -260,6 +265,7 @@ hipError_t launch_mx4_matmul(const Mx4View &X, const Mx4View &W, const uint16_t 
 // Xq: storage for X in MX4 (unused where the product's lanes round X).
 constexpr int64_t kMx4SmallMax = 64;
 bool mx4_small_ok(int64_t M);
+bool mx4_small_launch_ok(int64_t N);   // whether the launch can be counted
 // Xq = Q(X) and T = bf16(scale X A^T) for any M by way of P, mx4_small_ws_bytes:
 // for few tokens, where launch_mx4_rows has too few workgroups.
 hipError_t launch_mx4_prep(const uint16_t *X, const Mx4View &Xq, const uint16_t *A, int r, float scale, uint16_t *T,

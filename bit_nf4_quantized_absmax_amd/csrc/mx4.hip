@@ -177,9 +177,9 @@ __global__ __launch_bounds__(kMxThreads) void k_mx4_transpose(const uint8_t *__r
 namespace {
 
 // Workgroups of `each` rows of a slab.
-dim3 mx4_grid(const Mx4View &a, int each) {
-  return dim3(static_cast<uint32_t>((a.rows + each - 1) / each * mx4_slabs(a.cols)));
-}
+int64_t mx4_groups(int64_t rows, int64_t cols, int each) { return (rows + each - 1) / each * mx4_slabs(cols); }
+
+dim3 mx4_grid(const Mx4View &a, int each) { return dim3(static_cast<uint32_t>(mx4_groups(a.rows, a.cols, each))); }
 
 template <typename T>
 hipError_t quantize_as(const T *X, const Mx4View &a, hipStream_t s) {
@@ -189,6 +189,12 @@ hipError_t quantize_as(const T *X, const Mx4View &a, hipStream_t s) {
 }
 
 }  // namespace
+
+bool mx4_quantize_ok(int64_t rows, int64_t cols) { return mx4_groups(rows, cols, kMxGroups) <= kMaxThreads / kMxThreads; }
+
+bool mx4_dequantize_ok(int64_t rows, int64_t cols) {
+  return mx4_groups(rows, cols, kMxGroups * kDeRows) <= kMaxThreads / kMxThreads;
+}
 
 hipError_t launch_mx4_quantize(const void *X, int in_type, const Mx4View &a, hipStream_t s) {
   if (in_type == 0) return quantize_as(static_cast<const float *>(X), a, s);

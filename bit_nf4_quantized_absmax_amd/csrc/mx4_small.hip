@@ -385,6 +385,8 @@ hipError_t launch_prep(const SmallArgs &a, const Mx4View &Xq, hipStream_t s) {
 
 bool mx4_small_ok(int64_t M) { return M <= kMx4SmallMax; }
 
+bool mx4_small_launch_ok(int64_t N) { return (N + kMainRows - 1) / kMainRows <= kMaxThreads / 512; }   // 8 waves (launch_waves)
+
 size_t mx4_small_ws_bytes(int64_t M, int64_t K, int r) {
   return static_cast<size_t>((K + kSlice - 1) / kSlice) * M * r * sizeof(float);
 }

@@ -523,8 +523,10 @@ int qlora_linear_bwd_dropout(const uint16_t *dY, const uint16_t *X, const uint16
  * next multiple of 256, with zero codes and zero scale bytes:
  *   codes   [rows][Kp / 2]       element 2j in the low half of byte j, 2j + 1 in the high half
  *   scales  [Kp / 256][rows][8]  the scale bytes of the 8 blocks of a 256-wide slab of a row
- * both 16-byte aligned.  rows may be 0 (no tokens) except for a weight.  A
- * user who fills an array by other means writes the fill too: the product
+ * both 16-byte aligned.  rows may be 0 (no tokens) except for a weight;
+ * rows <= 2^31 - 1, and a launch's thread count limits the codec to ceil(rows /
+ * 8) * (Kp / 256) < 2^24 (decoding: rows / 16; a product of up to 64 rows with
+ * W: W's rows / 16 < 2^23), else UNSUPPORTED_SHAPE.  A user who fills an array by other means writes the fill too: the product
  * reads it. */
 typedef struct {
   uint8_t *codes;
