@@ -77,7 +77,8 @@ def token_logprobs(logits, target, top=0, workspace=None):
     M, V, st = _logits(logits)
     _need(target, torch.int64, "target", (M,))
     dev = logits.device
-    logprob, entropy = torch.empty(2, M, dtype=torch.float32, device=dev).unbind(0)
+    logprob = torch.empty(M, dtype=torch.float32, device=dev)     # their own storage: a view's base keeps it from being
+    entropy = torch.empty(M, dtype=torch.float32, device=dev)     # changed in place under autograd
     lse = torch.empty(M, 2, dtype=torch.float32, device=dev)
     top_logprob = top_index = None
     if top:

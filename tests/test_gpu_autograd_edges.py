@@ -1,5 +1,5 @@
 """The MX4 and vocabulary operators where a training loop goes beyond one plain
-step: a batch without tokens."""
+step: a batch without tokens, results changed in place."""
 
 import pytest
 import torch
@@ -45,3 +45,23 @@ def test_no_tokens_into_given_gradients():
     assert got[1] is dA and got[2] is dB and not dA.any() and not dB.any()
     got = q.mx4_linear_bwd(dy, x, None, lin.w, A, B, 1.0, need_dX=False, need_dB=False)
     assert got[0] is None and got[2] is None and not got[1].any()
+
+
+def test_results_may_be_changed_in_place():
+    """A loss mask applied to the log probabilities where they lie, with and without autograd."""
+    g = torch.Generator().manual_seed(3)
+    z = torch.randn(6, 500, generator=g).to(DEV)
+    t = torch.arange(6, device=DEV)
+    mask = torch.tensor([1.0, 0.0, 1.0, 1.0, 0.0, 1.0], device=DEV)
+    za, zb = z.clone().requires_grad_(), z.clone().requires_grad_()
+    lp, h = q.TokenLogprobsFn.apply(za, t)
+    lp *= mask
+    (lp.sum() + h.sum()).backward()
+    lp, h = q.TokenLogprobsFn.apply(zb, t)
+    ((lp * mask).sum() + h.sum()).backward()
+    assert torch.equal(za.grad, zb.grad) and za.grad.any()
+    r = q.token_logprobs(z, t)
+    entropy = r.entropy.clone()
+    coef = torch.ones(6, device=DEV, requires_grad=True)
+    r.logprob.mul_(coef).sum().backward()
+    assert coef.grad.any() and torch.equal(r.entropy, entropy)
