@@ -6,6 +6,7 @@ import ctypes
 from dataclasses import dataclass
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from ._capi import MX4ArrayStruct, check, lib
 from .ops import _mat, _need, _out, _ptr, _stream, _workspace
@@ -161,6 +162,7 @@ class MX4LinearFn(torch.autograd.Function):
         return Y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dY):
         X, A, B, T = ctx.saved_tensors
         dX, dA, dB = mx4_linear_bwd(dY.contiguous(), X, T, ctx.w, A, B, ctx.scale,

@@ -10,6 +10,7 @@ import ctypes
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from ._capi import LogitsStruct, TeacherStruct, check, lib
 from .ops import _need, _ptr, _stream, _workspace
@@ -173,6 +174,7 @@ class TokenLogprobsFn(torch.autograd.Function):
         return r.logprob, r.entropy
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g_logprob, g_entropy):
         logits, target, lse, entropy = ctx.saved_tensors
         return token_logprobs_bwd(logits, target, lse, entropy, g_logprob.contiguous(), g_entropy.contiguous()), None
@@ -189,6 +191,7 @@ class DistillTopKFn(torch.autograd.Function):
         return loss
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g):
         logits, index, logit, lse = ctx.saved_tensors
         return distill_topk_bwd(logits, index, logit, ctx.temperature, lse, g.contiguous()), None, None, None

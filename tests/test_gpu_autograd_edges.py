@@ -1,5 +1,6 @@
 """The MX4 and vocabulary operators where a training loop goes beyond one plain
-step: a batch without tokens, results changed in place."""
+step: a batch without tokens, results changed in place, a gradient of a
+gradient."""
 
 import pytest
 import torch
@@ -65,3 +66,19 @@ def test_results_may_be_changed_in_place():
     coef = torch.ones(6, device=DEV, requires_grad=True)
     r.logprob.mul_(coef).sum().backward()
     assert coef.grad.any() and torch.equal(r.entropy, entropy)
+
+
+def test_second_derivatives_are_refused():
+    """Gradients are computed outside autograd: a gradient of one raises, it is not taken as constant."""
+    g = torch.Generator().manual_seed(4)
+    z = torch.randn(3, 40, generator=g).to(DEV).requires_grad_()
+    lin = _pair(64, 64, 8)
+    x = torch.randn(5, 64, generator=g).to(BF16).to(DEV).requires_grad_()
+    idx = torch.arange(4, device=DEV).repeat(3, 1)
+    val = torch.zeros(3, 4, device=DEV)
+    for leaf, out in ((z, lambda: q.TokenLogprobsFn.apply(z, torch.arange(3, device=DEV))[0]),
+                      (z, lambda: q.DistillTopKFn.apply(z, idx, val, 1.0)), (x, lambda: lin(x))):
+        first, = torch.autograd.grad((out().float() ** 2).sum() + (leaf.float() ** 2).sum(), leaf, create_graph=True)
+        assert first.any()
+        with pytest.raises(RuntimeError):
+            (first.float() ** 2).sum().backward()
