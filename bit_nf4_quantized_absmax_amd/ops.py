@@ -21,7 +21,10 @@ from ._capi import DeqMatmulFwdDescStruct, LoraGradsDescStruct, MatmulFwdDescStr
 
 def _stream(t):
     # the handle of torch.cuda.current_stream(t.device), without the Stream object (0.2 us a call instead of 2.2)
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
+    device = t.get_device()
+    if device < 0:   # in host memory; the call below would take it for the current device
+        raise ValueError("expected a tensor on a GPU device, got one on %s" % t.device)
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 def _ptr(t):
