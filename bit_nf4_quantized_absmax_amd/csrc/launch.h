@@ -308,7 +308,8 @@ struct Teacher {
 hipError_t launch_distill_fwd(const Logits &l, const Teacher &t, float *loss, float *lse, void *ws, hipStream_t s);
 hipError_t launch_distill_bwd(const Logits &l, const Teacher &t, const float *lse, const float *weight, void *dz,
                               int64_t ldd, hipStream_t s);
-// Loss and gradient at once; rows up to distill_fused_max(type) words are read once.
+// Loss and gradient at once; rows that one workgroup holds (32768 fp32 words,
+// 65536 of 16 bits) are read once.
 hipError_t launch_distill(const Logits &l, const Teacher &t, const float *weight, float *loss, float *lse, void *dz,
                           int64_t ldd, void *ws, hipStream_t s);
 

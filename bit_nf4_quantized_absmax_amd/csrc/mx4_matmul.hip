@@ -27,10 +27,13 @@
 //    accumulators run along a row of Y: two half-wave swaps make 16 bytes of
 //    them, which cross the wave's own part of a free stage.
 //
-// 8192 x 11008 x 4096 with r = 64: 209 to 217 us, 3.4 to 3.5 PFLOP/s, 0.67 of four
-// times what a large bf16 product reaches here.  What bounds it is the way from
-// the L2 to the LDS: 64 KB a step and compute unit at 55 to 60 bytes a clock (128-
-// byte rows; rows of 64 bytes reach 29).
+// 8192 x 11008 x 4096 with r = 64: 205 to 230 us, 3.2 to 3.6 PFLOP/s, 0.62 to 0.70
+// of four times what a large bf16 product reaches here, the matrix pipes busy 45 %
+// of the clocks.  No part of it is the bound by itself: of 227 us, 163 remain
+// without the fetch, 167 without the products and 72 without both (operand reads,
+// barriers, stores): fetch and products overlap by a third, since a step's barrier
+// waits for the fetch that the step itself issued.  The 1376 tiles are six
+// rounds of the 256 compute units, the last of 96 tiles.
 #include <algorithm>
 #include <type_traits>
 

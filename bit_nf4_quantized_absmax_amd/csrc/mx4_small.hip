@@ -16,8 +16,9 @@
 //   workgroups a lane rounds the block of X that it supplies itself, 32 bf16
 //   of one token: the block's maximum needs no other lane.
 //
-// r = 64: 1 x 11008 x 4096 takes 4.5 + 6.7 us (W's 24 MB at 3.6 TB/s), 64 x 4096 x
-// 11008 4.7 + 21 us.
+// r = 64: 1 x 11008 x 4096 takes 4.2 + 7.7 us in a kernel trace (W's 24 MB at 3.1
+// TB/s; 4.3 + 6.7 by torch's profiler, whose figures stand beside the rules
+// below), 64 x 4096 x 11008 5 + 21 us.
 #include <algorithm>
 
 #include "common.h"
@@ -343,9 +344,9 @@ namespace {
 template <int kMB>
 hipError_t launch_waves(const SmallArgs &a, hipStream_t s) {
   const int grid = (a.N + kMainRows - 1) / kMainRows;
-  // Up to two workgroups a CU: 16 waves (64 x 4096 x 11008: 18.9 us, with 8
-  // waves 21.0).  More: 8, of which more share a CU (1 x 11008 x 4096: 6.5 us,
-  // with 16 waves 9.8).
+  // Up to two workgroups a CU: 16 waves (64 x 4096 x 11008: 20.7 us, with 8
+  // waves 21.1; 1 x 4096 x 4096: 3.7 and 3.5).  More: 8, of which more share a CU
+  // (1 x 11008 x 4096: 6.7 us, with 16 waves 9.1; 16 x 11008 x 4096: 11.5 and 12.6).
   if (grid <= 512)
     hipLaunchKernelGGL((k_mx4_small<kMB, false, 16>), dim3(grid), dim3(1024), 0, s, a);
   else

@@ -523,10 +523,11 @@ int qlora_linear_bwd_dropout(const uint16_t *dY, const uint16_t *X, const uint16
  * next multiple of 256, with zero codes and zero scale bytes:
  *   codes   [rows][Kp / 2]       element 2j in the low half of byte j, 2j + 1 in the high half
  *   scales  [Kp / 256][rows][8]  the scale bytes of the 8 blocks of a 256-wide slab of a row
- * both 16-byte aligned.  rows may be 0 (no tokens) except for a weight;
- * rows <= 2^31 - 1, and a launch's thread count limits the codec to ceil(rows /
- * 8) * (Kp / 256) < 2^24 (decoding: rows / 16; a product of up to 64 rows with
- * W: W's rows / 16 < 2^23), else UNSUPPORTED_SHAPE.  A user who fills an array by other means writes the fill too: the product
+ * both 16-byte aligned.  rows may be 0 (no tokens) except for a weight, and at
+ * most 2^31 - 1.  A launch's thread count limits the codec to ceil(rows / 8) *
+ * (Kp / 256) < 2^24 (decoding: ceil(rows / 16)) and W's rows in a product of up
+ * to 64 rows of X to ceil(rows / 16) < 2^23; more is an UNSUPPORTED_SHAPE.  A
+ * user who fills an array by other means writes the fill too: the product
  * reads it. */
 typedef struct {
   uint8_t *codes;
@@ -558,19 +559,20 @@ size_t qlora_mx4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t
 /* qlora_linear_fwd on an MX4 weight W [N, K]:
  *   Y [M, N] = Q(X) W^T + T B^T,   T = scale X A^T
  * X [M, K] bf16 is rounded to MX4 (Q) for the frozen product; the LoRA branch
- * reads it as it is.  r = 0: no LoRA pair (A, B and T_out unused).  T_out
- * (nullable) receives T.  K % 32 == 0, any N; M * max(N, K) < 2^31 with a
- * LoRA pair. */
+ * reads it as it is, and T is rounded to bf16 before its product with B.
+ * r = 0: no LoRA pair (A, B and T_out unused).  T_out (nullable) receives T.
+ * K % 32 == 0, any N; M * max(N, K) < 2^31 with a LoRA pair. */
 int qlora_mx4_linear_fwd(const uint16_t *X, int64_t M, const qlora_mx4_array *W, const uint16_t *A, const uint16_t *B,
                          int32_t r, float scale, uint16_t *Y, uint16_t *T_out, void *ws, size_t ws_bytes, void *stream);
 
 /* qlora_linear_bwd on an MX4 weight: dX = dY W + G A, dA = G^T X, dB = dY^T T,
  * G = scale dY B.  The rounding of X passes its gradient straight through,
- * and dA reads the unrounded X, which the LoRA branch read.  dX multiplies
- * W's bf16 values (expanded into the workspace).  r >= 1, K % 64 == 0,
- * N % 8 == 0 and, for dX, N % 64 == 0; outputs and T nullable as there (a
- * recomputed T may round differently from the forward's).  M = 0 writes
- * nothing: dA and dB, then zero, are left as they were. */
+ * and dA reads the unrounded X, which the LoRA branch read; G and T are rounded
+ * to bf16 between their products.  dX multiplies W's bf16 values (expanded
+ * into the workspace).  r >= 1, K % 64 == 0, N % 8 == 0 and, for dX, N % 64 == 0;
+ * outputs and T nullable as there (a recomputed T may round differently from
+ * the forward's).  M = 0 writes nothing: dA and dB, whose value is then zero,
+ * are left as they were. */
 int qlora_mx4_linear_bwd(const uint16_t *dY, const uint16_t *X, const uint16_t *T, int64_t M, const qlora_mx4_array *W,
                          const uint16_t *A, const uint16_t *B, int32_t r, float scale, uint16_t *dX, uint16_t *dA,
                          uint16_t *dB, void *ws, size_t ws_bytes, void *stream);
@@ -583,9 +585,11 @@ int qlora_mx4_linear_bwd(const uint16_t *dY, const uint16_t *X, const uint16_t *
  *
  * A row of logits z has p = softmax(z).  A word that is masked out is -inf.
  * In a row that is all -inf: log probabilities -inf, entropy 0, gradients 0.
- * A NaN or +inf makes its row's numbers NaN (its alternatives are still `top`
- * different words of the row, a NaN ranked as -inf).  Sums are fp32 over at most 16384 words, joined in 64
- * bits; gradients are rounded once to the logits' type. */
+ * Finite logits of any size, masks among them, give no NaN.  A NaN or +inf makes
+ * its row's numbers NaN (its alternatives are still `top` different words of
+ * the row, a NaN ranked as -inf).  Sums are fp32 within a workgroup, over at
+ * most 65536 words (16384 where a row is cut), and joined in 64 bits; gradients
+ * are rounded once to the logits' type. */
 
 /* Logits [rows, words] of `type` (0: fp32, else QLORA_IN_BF16 or
  * QLORA_IN_FP16), row m at z + m * pitch elements (pitch >= words: padded
