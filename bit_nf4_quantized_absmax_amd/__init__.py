@@ -13,6 +13,7 @@ from .ops import (Q4_TYPES, NF4Weight, QLoRALinear, QLoRALinearFn, linear_bwd, l
                   linear_fwd_dropout, linear_bwd_dropout, quantize_group, dequantize_group,
                   lora_grads_group, nf4_matmul_fwd_group, deq_matmul_fwd, deq_matmul_fwd_group, deq_matmul_dx)
 from .mx4 import MX4Linear, MX4LinearFn, MX4Tensor, mx4_linear_bwd, mx4_linear_fwd, mx4_matmul  # noqa: F401
+from .adapters import AdapterLinear, AdapterLinearFn, adapter_linear_bwd, adapter_linear_fwd  # noqa: F401
 from .vocab import (DistillTopKFn, TokenLogprobs, TokenLogprobsFn, distill_topk, distill_topk_bwd,  # noqa: F401
                     distill_topk_fwd, token_logprobs, token_logprobs_bwd)
 
@@ -23,6 +24,7 @@ __all__ = [
     "linear_fwd_dropout", "linear_bwd_dropout", "quantize_group", "dequantize_group", "lora_grads_group", "nf4_matmul_fwd_group",
     "deq_matmul_fwd", "deq_matmul_fwd_group", "deq_matmul_dx",
     "MX4Tensor", "MX4Linear", "MX4LinearFn", "mx4_matmul", "mx4_linear_fwd", "mx4_linear_bwd",
+    "AdapterLinear", "AdapterLinearFn", "adapter_linear_fwd", "adapter_linear_bwd",
     "token_logprobs", "token_logprobs_bwd", "TokenLogprobs", "TokenLogprobsFn",
     "distill_topk", "distill_topk_fwd", "distill_topk_bwd", "DistillTopKFn", "QLoRAError", "status_string",
 ]

@@ -33,6 +33,7 @@ EXPORTED = (
     "qlora_mx4_linear_workspace_bytes", "qlora_mx4_linear_fwd", "qlora_mx4_linear_bwd",
     "qlora_vocab_workspace_bytes", "qlora_token_logprobs", "qlora_token_logprobs_bwd",
     "qlora_distill_fwd", "qlora_distill_bwd", "qlora_distill",
+    "qlora_adapter_linear_workspace_bytes", "qlora_adapter_linear_fwd", "qlora_adapter_linear_bwd",
     "qlora_dropout_mask", "qlora_dropout_apply", "qlora_nf4_matmul_dx_dropout",
     "qlora_linear_dropout_workspace_bytes", "qlora_linear_fwd_dropout", "qlora_linear_bwd_dropout",
 )
@@ -138,11 +139,23 @@ class TeacherStruct(ctypes.Structure):
     ]
 
 
+class AdaptersStruct(ctypes.Structure):
+    _fields_ = [
+        ("A", ctypes.c_void_p),
+        ("B", ctypes.c_void_p),
+        ("scale", ctypes.c_void_p),
+        ("index", ctypes.c_void_p),
+        ("count", ctypes.c_int32),
+        ("r", ctypes.c_int32),
+    ]
+
+
 _lib = None
 
 _vp, _i64, _i32, _sz, _f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t, ctypes.c_float
 _wp = ctypes.POINTER(NF4WeightStruct)
 _mp, _lp, _tp = ctypes.POINTER(MX4ArrayStruct), ctypes.POINTER(LogitsStruct), ctypes.POINTER(TeacherStruct)
+_ap = ctypes.POINTER(AdaptersStruct)
 
 _SIGS = {
     "qlora_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -195,6 +208,9 @@ _SIGS = {
     "qlora_distill_fwd": (ctypes.c_int, [_lp, _tp, _vp, _vp, _vp, _sz, _vp]),
     "qlora_distill_bwd": (ctypes.c_int, [_lp, _tp, _vp, _vp, _vp, _i64, _vp]),
     "qlora_distill": (ctypes.c_int, [_lp, _tp, _vp, _vp, _vp, _vp, _i64, _vp, _sz, _vp]),
+    "qlora_adapter_linear_workspace_bytes": (_sz, [_i64, _i64, _i64, _i32, _i32, ctypes.c_int]),
+    "qlora_adapter_linear_fwd": (ctypes.c_int, [_vp, _i64, _wp, _ap, _vp, _vp, _vp, _sz, _vp]),
+    "qlora_adapter_linear_bwd": (ctypes.c_int, [_vp, _vp, _vp, _i64, _wp, _ap, _vp, _vp, _vp, _vp, _sz, _vp]),
     "qlora_dropout_mask": (ctypes.c_int, [_vp, _i64, _i64, _f32, ctypes.c_uint64, _vp, _vp, _vp]),
     "qlora_dropout_apply": (ctypes.c_int, [_vp, _i64, _i64, _vp, _vp, _vp]),
     "qlora_nf4_matmul_dx_dropout": (ctypes.c_int, [_vp, _i64, _wp, _vp, _vp, _i32, _vp, _vp, _vp]),

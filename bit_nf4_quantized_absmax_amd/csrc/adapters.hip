@@ -1,0 +1,806 @@
+// Many LoRA adapters beside one frozen projection (gfx950): every token names
+// the adapter of its request.
+//     T_m  = s_a X_m A_a^T              Y_m  = X_m deq(W)^T + T_m B_a^T
+//     G_m  = s_a dY_m B_a               dX_m = dY_m deq(W) + G_m A_a
+//     dA_a = sum_m G_m^T X_m            dB_a = sum_m dY_m^T T_m   (m of adapter a)
+// with a = index[m], A [n, r, K], B [n, N, r].  A token whose index is outside
+// [0, n) has no adapter.
+//
+// Up to kAdSmall tokens (decoding) two kernels do it: k_ad_down forms T, one
+// workgroup per adapter in use and 16 of its rows; k_ad_small multiplies the
+// packed weight and adds each token's own T B^T.  A wave finds the tokens of
+// an adapter by a ballot over the indices: nothing is sorted.
+//
+// Above that the tokens are sorted by adapter once (k_ad_sort, by rank and so
+// in a fixed order); T and G are products over 32-token tiles of one adapter
+// (k_ad_down_tiles); the wide products run on 256 x 256 tiles of sorted tokens,
+// gathered by the DMA, whose epilogue adds the adapters' term 32 tokens at a
+// time (k_ad_matmul); dA and dB are products over an adapter's run of tokens
+// (k_ad_grads).  An adapter's numbers meet only its own tokens: a product with
+// another's is dropped, not multiplied by zero, so a NaN in one adapter stays there.
+#include <algorithm>
+
+#include "common.h"
+#include "gemm16.h"
+#include "launch.h"
+
+namespace qlora {
+
+__constant__ uint32_t cAdQ4Level[3 * 16] = {QLORA_Q4_LEVEL_BITS};
+__constant__ uint32_t cAdT8Level[256] = {QLORA_T8_LEVEL_BITS};
+
+namespace {
+
+constexpr int kAdWaves = 16;
+constexpr int kAdThreads = kAdWaves * 64;
+constexpr int kAdRows = 16;        // weight rows of a workgroup of k_ad_small
+
+__device__ __forceinline__ int adapter_of(const int64_t *index, int m, int n) {
+  const int64_t a = index[m];
+  return a >= 0 && a < n ? static_cast<int>(a) : -1;
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------------------
+// Decoding, T [M, r]: workgroup (token m, 16 adapter rows).  The first token of
+// an adapter does the work of all of them, 16 tokens an MFMA tile; the 16
+// waves split K and are summed in LDS in wave order.
+template <int kMB>
+__global__ __launch_bounds__(kAdThreads) void k_ad_down(const uint16_t *__restrict__ X, int M, int K, const uint16_t *__restrict__ A,
+                                                        int r, const float *__restrict__ scale, const int64_t *__restrict__ index,
+                                                        int n, uint16_t *__restrict__ T) {
+  __shared__ float red[kAdWaves][16][17];
+  __shared__ int tok[64];
+  const int jt = blockIdx.x, m0 = blockIdx.y;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int nl = lane & 15, g = lane >> 4;
+  const int mine = lane < M ? adapter_of(index, lane, n) : -1;
+  const int a = __shfl(mine, m0, 64);
+  if (a < 0) {
+    if (threadIdx.x < 16 && 16 * jt + threadIdx.x < r) T[static_cast<int64_t>(m0) * r + 16 * jt + threadIdx.x] = 0;
+    return;
+  }
+  const uint64_t mask = __ballot(mine == a);
+  if (__builtin_ctzll(mask) != m0) return;
+  const int cnt = __popcll(mask);
+  if (wave == 0 && mine == a) tok[__popcll(mask & ((uint64_t{1} << lane) - 1))] = lane;
+  __syncthreads();
+  const int j = 16 * jt + nl;
+  const uint16_t *arow = A + (static_cast<int64_t>(a) * r + min(j, r - 1)) * K;
+  const float s = scale[a];
+  const int steps = K >> 5;                       // K % 64 == 0
+#pragma unroll 1
+  for (int t0 = 0; t0 < cnt; t0 += 16 * kMB) {
+    const uint16_t *xrow[kMB];
+#pragma unroll
+    for (int mb = 0; mb < kMB; ++mb) xrow[mb] = X + static_cast<int64_t>(tok[min(t0 + 16 * mb + nl, cnt - 1)]) * K;
+    f32x4_t acc[kMB];
+#pragma unroll
+    for (int mb = 0; mb < kMB; ++mb) acc[mb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    constexpr int kBatch = 8;
+    for (int b = wave; b < steps; b += kAdWaves * kBatch) {
+      bf16x8_t av[kBatch], xv[kBatch][kMB];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int k = 32 * min(b + u * kAdWaves, steps - 1) + 8 * g;
+        av[u] = *reinterpret_cast<const bf16x8_t *>(arow + k);
+#pragma unroll
+        for (int mb = 0; mb < kMB; ++mb) xv[u][mb] = *reinterpret_cast<const bf16x8_t *>(xrow[mb] + k);
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        if (b + u * kAdWaves >= steps) break;     // uniform
+#pragma unroll
+        for (int mb = 0; mb < kMB; ++mb) acc[mb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[u][mb], av[u], acc[mb], 0, 0, 0);
+      }
+    }
+    // lane: column (adapter row) nl, tokens 4 g + e
+#pragma unroll
+    for (int mb = 0; mb < kMB; ++mb) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) red[wave][4 * g + e][nl] = acc[mb][e];
+      __syncthreads();
+      if (threadIdx.x < 256) {
+        const int row = threadIdx.x >> 4, c = threadIdx.x & 15, at = t0 + 16 * mb + row;
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kAdWaves; ++w) v += red[w][row][c];
+        if (at < cnt && 16 * jt + c < r) T[static_cast<int64_t>(tok[at]) * r + 16 * jt + c] = f32_to_bf16(s * v);
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Decoding, Y: workgroup = 16 weight rows x the whole K.  Wave w takes the
+// blocks w, w + 16, ...; lane (row n = l % 16, g = l / 16) expands codes 16 g ..
+// +15 of its row's block through a byte -> bf16x2 table and each block's partial
+// product is scaled by its constant in fp32, so the weight is bf16(level) times
+// the constant, as in the framework's other decoding kernels.  The adapters in
+// use go to the waves in turn; a token takes the product with its own adapter
+// only.  The 16 waves' sums are added in LDS in wave order and rounded once.
+template <int kMB>
+__global__ __launch_bounds__(kAdThreads) void k_ad_small(const uint16_t *__restrict__ X, int M, NF4View w,
+                                                         const uint16_t *__restrict__ T, const uint16_t *__restrict__ B, int r,
+                                                         const int64_t *__restrict__ index, int nad, uint16_t *__restrict__ Y) {
+  constexpr int kBlk = kMB == 1 ? 6 : (kMB == 2 ? 3 : (kMB == 3 ? 2 : 1));
+  __shared__ uint32_t sLut[256 * 64];
+  __shared__ float sT8[256];
+  __shared__ float red[kAdWaves][kMB * 16][kAdRows + 1];
+  const int N = w.N, K = w.K;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int nl = lane & 15, g = lane >> 4;
+  const int n0 = blockIdx.x * kAdRows;
+  const int n = min(n0 + nl, N - 1);
+  const int KB = K >> 6;
+  const float mean = w.mean[0];
+  const float t8v = u2f(cAdT8Level[threadIdx.x & 255]);
+  const int mine = lane < M ? adapter_of(index, lane, nad) : -1;
+
+  uint2 pk[kBlk];
+  uint32_t code[kBlk];
+  float c2v[kBlk];
+  bf16x8_t xb[kBlk][kMB][2];
+  const uint8_t *prow = w.packed + static_cast<int64_t>(n) * (K >> 1);
+  const int64_t rowblk = static_cast<int64_t>(n) * KB;
+  auto load_batch = [&](int b0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < kBlk; ++u) {
+      const int b = min(b0 + u * kAdWaves, KB - 1);
+      pk[u] = *reinterpret_cast<const uint2 *>(prow + 32 * b + 8 * g);
+      code[u] = w.code8[rowblk + b];
+      c2v[u] = w.c2[(rowblk + b) >> 8];
+    }
+#pragma unroll
+    for (int u = 0; u < kBlk; ++u) {
+      const int k = 64 * min(b0 + u * kAdWaves, KB - 1) + 16 * g;
+#pragma unroll
+      for (int mb = 0; mb < kMB; ++mb)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          xb[u][mb][t] = *reinterpret_cast<const bf16x8_t *>(X + static_cast<int64_t>(min(16 * mb + nl, M - 1)) * K + k + 8 * t);
+    }
+  };
+  load_batch(min(wave, KB - 1));
+  {
+    const uint32_t *lvt = cAdQ4Level + 16 * w.qtype;
+    const float lo = u2f(lvt[wave]);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) sLut[64 * (wave + 16 * j) + lane] = pack_bf16x2(lo, u2f(lvt[j]));
+  }
+  sT8[threadIdx.x & 255] = t8v;                 // four threads write each entry, same value
+  raw_barrier<wait_imm(63, 0)>();
+
+  f32x4_t acc[kMB];
+#pragma unroll
+  for (int mb = 0; mb < kMB; ++mb) acc[mb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int b0 = wave; b0 < KB; b0 += kAdWaves * kBlk) {
+    if (b0 != wave) load_batch(b0);
+#pragma unroll
+    for (int u = 0; u < kBlk; ++u) {
+      if (b0 + u * kAdWaves >= KB) break;       // uniform
+      const float chat = decode_absmax(sT8[code[u]], c2v[u], mean);
+      const uint32_t words[2] = {pk[u].x, pk[u].y};
+      bf16x8_t wop[2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = sLut[64 * ((words[t] >> (8 * i)) & 0xffu) + lane];
+        wop[t] = __builtin_bit_cast(bf16x8_t, o);
+      }
+#pragma unroll
+      for (int mb = 0; mb < kMB; ++mb) {
+        f32x4_t part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb[u][mb][0], wop[0], f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+        part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb[u][mb][1], wop[1], part, 0, 0, 0);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[mb][e] = __builtin_fmaf(chat, part[e], acc[mb][e]);
+      }
+    }
+  }
+
+  // The adapters in use, this wave's share of them.
+  uint64_t left = __ballot(mine >= 0);
+  for (int d = 0; left; ++d) {
+    const int a = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
+    const uint64_t mask = __ballot(mine == a);
+    left &= ~mask;
+    if ((d & (kAdWaves - 1)) != wave) continue;
+    const uint16_t *brow = B + (static_cast<int64_t>(a) * N + n) * r;
+    f32x4_t part[kMB];
+#pragma unroll
+    for (int mb = 0; mb < kMB; ++mb) part[mb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int j0 = 0; j0 < r; j0 += 32) {
+      const int j = j0 + 8 * g;
+      const bool ok = j < r;                    // r % 8 == 0
+      bf16x8_t bop = *reinterpret_cast<const bf16x8_t *>(brow + (ok ? j : 0));
+      if (!ok) bop = bf16x8_t{};
+#pragma unroll
+      for (int mb = 0; mb < kMB; ++mb) {
+        bf16x8_t top = *reinterpret_cast<const bf16x8_t *>(T + static_cast<int64_t>(min(16 * mb + nl, M - 1)) * r + (ok ? j : 0));
+        if (!ok) top = bf16x8_t{};
+        part[mb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(top, bop, part[mb], 0, 0, 0);
+      }
+    }
+#pragma unroll
+    for (int mb = 0; mb < kMB; ++mb)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if ((mask >> (16 * mb + 4 * g + e)) & 1) acc[mb][e] += part[mb][e];
+  }
+
+#pragma unroll
+  for (int mb = 0; mb < kMB; ++mb)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) red[wave][16 * mb + 4 * g + e][nl] = acc[mb][e];
+  __syncthreads();
+  for (int idx = threadIdx.x; idx < kMB * 16 * kAdRows; idx += kAdThreads) {
+    const int m = idx / kAdRows, c = idx % kAdRows;
+    if (m < M && n0 + c < N) {
+      float v = red[0][m][c];
+#pragma unroll
+      for (int q = 1; q < kAdWaves; ++q) v += red[q][m][c];
+      Y[static_cast<int64_t>(m) * N + n0 + c] = f32_to_bf16(v);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Tokens sorted by adapter, in order of their number within one; tokens without
+// an adapter come last.  One workgroup; wave w has the w-th part of the tokens.
+//   perm [M]     token at a sorted place
+//   who  [M]     its adapter, -1: none
+//   seg  [n + 1] first place of every adapter's run
+//   tile [ntiles] (adapter, first place, tokens <= 32, 0), ntile [1]
+//   zero [64]    a row of zeros for the DMA of places past a run
+namespace {
+constexpr int kSortWaves = 16;
+constexpr int kSortThreads = kSortWaves * 64;
+}  // namespace
+
+__global__ __launch_bounds__(kSortThreads) void k_ad_sort(const int64_t *__restrict__ index, int M, int n, AdPlan p) {
+  __shared__ int hist[kSortWaves][kAdMax + 1];
+  __shared__ int wsum[2][kSortWaves];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  for (int i = lane; i <= n; i += 64) hist[wave][i] = 0;
+  __syncthreads();
+  const int per = ((M + kSortWaves - 1) / kSortWaves + 63) / 64 * 64;
+  const int lo = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(wave) * per, M));
+  const int hi = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(wave + 1) * per, M));
+  for (int m = lo + lane; m < hi; m += 64) {
+    const int a = adapter_of(index, m, n);
+    atomicAdd(&hist[wave][a < 0 ? n : a], 1);     // counts: order does not matter
+  }
+  if (tid < 64) p.zero[tid] = 0;
+  __syncthreads();
+  // Column a of the table: this adapter's tokens before each wave's part.
+  int total = 0, tiles = 0;
+  if (tid <= n) {
+    for (int w = 0; w < kSortWaves; ++w) {
+      const int c = hist[w][tid];
+      hist[w][tid] = total;
+      total += c;
+    }
+    if (tid < n) tiles = (total + 31) / 32;
+  }
+  int pos = total, tpos = tiles;                 // inclusive sums over the workgroup
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int u = __shfl_up(pos, o, 64), v = __shfl_up(tpos, o, 64);
+    if (lane >= o) {
+      pos += u;
+      tpos += v;
+    }
+  }
+  if (lane == 63) {
+    wsum[0][wave] = pos;
+    wsum[1][wave] = tpos;
+  }
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) {
+    pos += wsum[0][w];
+    tpos += wsum[1][w];
+  }
+  const int start = pos - total;
+  if (tid <= n) {
+    for (int w = 0; w < kSortWaves; ++w) hist[w][tid] += start;
+    p.seg[tid] = start;
+    if (tid < n) {
+      const int t0 = tpos - tiles;
+      for (int i = 0; i < tiles; ++i) p.tile[t0 + i] = make_int4(tid, start + 32 * i, min(32, total - 32 * i), 0);
+      if (tid == n - 1) p.ntile[0] = tpos;
+    }
+  }
+  __syncthreads();
+  for (int m0 = lo; m0 < hi; m0 += 64) {          // wave-uniform; this wave's row of the table only
+    const int m = m0 + lane;
+    const int a = m < hi ? adapter_of(index, m, n) : -2;
+    uint64_t left = __ballot(a != -2);
+    while (left) {
+      const int a0 = __builtin_amdgcn_readlane(a, __builtin_ctzll(left));
+      const uint64_t mask = __ballot(a == a0);
+      left &= ~mask;
+      const int col = a0 < 0 ? n : a0;
+      int base = 0;
+      if (lane == 0) base = atomicAdd(&hist[wave][col], static_cast<int>(__popcll(mask)));
+      base = __builtin_amdgcn_readfirstlane(base);
+      if (a == a0) {
+        const int at = base + static_cast<int>(__popcll(mask & ((uint64_t{1} << lane) - 1)));
+        p.perm[at] = m;
+        p.who[at] = a0;
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// out [tokens, r] = scale_a P_m Q_a^T over 32-token tiles of one adapter: P
+// [M, D] (X or dY), Q [n, r, D] (A, or B transposed).  Workgroup (tile, 64
+// adapter rows), 4 waves; wave w takes the 64-column steps w, w + 4, ... from a
+// private ring in LDS, so there is no barrier in the loop, and the waves are
+// summed in wave order.  Bound by the stream of P.
+namespace {
+constexpr int kDtWaves = 4;
+constexpr int kDtThreads = kDtWaves * 64;
+constexpr int kDtSlots = 3;
+
+template <int kJB>
+constexpr int dt_slot() { return (1 + kJB) * 4096; }   // 32 rows of P, 32 kJB rows of Q, 128 bytes each
+}  // namespace
+
+template <int kJB>
+__global__ __launch_bounds__(kDtThreads) void k_ad_down_tiles(const uint16_t *__restrict__ P, int D, const uint16_t *__restrict__ Q,
+                                                              int r, const float *__restrict__ scale, AdPlan p,
+                                                              uint16_t *__restrict__ out) {
+  __shared__ __attribute__((aligned(16))) uint8_t smem[kDtWaves][kDtSlots][dt_slot<kJB>()];
+  if (static_cast<int>(blockIdx.x) >= p.ntile[0]) return;
+  const int4 tl = p.tile[blockIdx.x];
+  const int a = tl.x, p0 = tl.y, cnt = tl.z;
+  const int j0 = blockIdx.y * 32 * kJB;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lr = lane & 31, lh = lane >> 5;
+  const uint16_t *Qa = Q + static_cast<int64_t>(a) * r * D;
+  const int steps = D >> 6;
+  const int n_i = wave < steps ? (steps - wave + kDtWaves - 1) / kDtWaves : 0;
+
+  // 8 rows of 128 bytes a DMA instruction; the chunk that belongs at a lane's position.
+  uint32_t po[4], qo[4 * kJB];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int row = 8 * u + (lane >> 3);
+    const int chunk = (lane & 7) ^ ((row & 7) ^ ((row >> 3) & 1));
+    po[u] = static_cast<uint32_t>(p.perm[p0 + min(row, cnt - 1)]) * D * 2 + 16 * chunk;
+  }
+#pragma unroll
+  for (int u = 0; u < 4 * kJB; ++u) {
+    const int row = 8 * u + (lane >> 3);
+    const int chunk = (lane & 7) ^ ((row & 7) ^ ((row >> 3) & 1));
+    qo[u] = static_cast<uint32_t>(min(j0 + row, r - 1)) * D * 2 + 16 * chunk;   // rows past r: columns never stored
+  }
+  const uint32_t ring = lds_addr(smem[wave][0]);
+  auto issue = [&](int i, int slot) __attribute__((always_inline)) {
+    const int64_t k = 64 * (wave + static_cast<int64_t>(kDtWaves) * i);
+    const uint32_t dst = __builtin_amdgcn_readfirstlane(ring + slot * dt_slot<kJB>());
+#pragma unroll
+    for (int u = 0; u < 4; ++u) dma16(P + k, po[u], dst + u * 1024);
+#pragma unroll
+    for (int u = 0; u < 4 * kJB; ++u) dma16(Qa + k, qo[u], dst + 4096 + u * 1024);
+  };
+  constexpr int kDma = 4 + 4 * kJB;
+  f32x16_t acc[kJB];
+#pragma unroll
+  for (int jb = 0; jb < kJB; ++jb)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[jb][e] = 0.f;
+  // Only DMAs count here: in issue order, so the two younger steps may be in flight.
+  __builtin_amdgcn_s_waitcnt(wait_imm(0, 0));
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  if (n_i > 0) issue(0, 0);
+  if (n_i > 1) issue(1, 1);
+  for (int i = 0; i < n_i; ++i) {
+    const int slot = i % kDtSlots;
+    if (i + 2 < n_i) issue(i + 2, (i + 2) % kDtSlots);
+    __builtin_amdgcn_sched_barrier(0);
+    if (i + 2 < n_i)
+      __builtin_amdgcn_s_waitcnt(wait_imm(2 * kDma, 15));
+    else if (i + 1 < n_i)
+      __builtin_amdgcn_s_waitcnt(wait_imm(kDma, 15));
+    else
+      __builtin_amdgcn_s_waitcnt(wait_imm(0, 15));
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_sched_barrier(0);
+    const uint8_t *ps = smem[wave][slot], *qs = ps + 4096;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const bf16x8_t x = *reinterpret_cast<const bf16x8_t *>(ps + swz128(lr, 2 * s + lh));
+#pragma unroll
+      for (int jb = 0; jb < kJB; ++jb) {
+        const bf16x8_t y = *reinterpret_cast<const bf16x8_t *>(qs + swz128(32 * jb + lr, 2 * s + lh));
+        acc[jb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, y, acc[jb], 0, 0, 0);
+      }
+    }
+    // The operand reads are done before the next step's DMA into this slot is issued.
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(wait_imm(63, 0));
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  // lane: column (adapter row) lr of block jb, token 8 (e / 4) + 4 lh + e % 4.
+  float *red = reinterpret_cast<float *>(smem[wave][0]);
+#pragma unroll
+  for (int jb = 0; jb < kJB; ++jb)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) red[(8 * (e >> 2) + 4 * lh + (e & 3)) * 32 * kJB + 32 * jb + lr] = acc[jb][e];
+  __syncthreads();
+  const float s = scale[a];
+  for (int idx = threadIdx.x; idx < 32 * 4 * kJB; idx += kDtThreads) {
+    const int row = idx / (4 * kJB), c = idx % (4 * kJB), j = j0 + 8 * c;
+    if (row >= cnt || j >= r) continue;          // r % 8 == 0
+    float v[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      v[q] = 0.f;
+#pragma unroll
+      for (int w = 0; w < kDtWaves; ++w) v[q] += reinterpret_cast<const float *>(smem[w][0])[row * 32 * kJB + 8 * c + q];
+      v[q] *= s;
+    }
+    *reinterpret_cast<uint4 *>(out + static_cast<int64_t>(p.perm[p0 + row]) * r + j) =
+        make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+  }
+}
+
+// Zeros in the T of tokens without an adapter (they are the last of the order).
+__global__ __launch_bounds__(256) void k_ad_bare(AdPlan p, int M, int n, int r, uint16_t *__restrict__ out) {
+  const int first = p.seg[n];
+  const int per = r >> 3;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < static_cast<int64_t>(M - first) * per;
+       i += static_cast<int64_t>(gridDim.x) * 256)
+    *reinterpret_cast<uint4 *>(out + static_cast<int64_t>(p.perm[first + i / per]) * r + 8 * (i % per)) = make_uint4(0, 0, 0, 0);
+}
+
+// ---------------------------------------------------------------------------
+// C [M, cols] = L Wd^T (or L Wd) + T_m U_a^T: L = X, U = B (NT), or L = dY, U
+// = A transposed (NN); U [n, cols, r].  The adapters' term is added to a
+// wave's accumulators 32 tokens at a time, from T and U as they lie in memory (16
+// bytes a lane are an operand of the matrix instruction).  Sorted tokens: most
+// blocks have one adapter and accumulate in place; in the others the product is
+// formed apart and added in the lanes whose token has this adapter.
+// Kc, L's row pitch: a multiple of 64; NN: columns N .. Kc - 1 of L are zero.
+template <bool kNN>
+__global__ __launch_bounds__(gemm16::kThreads) void k_ad_matmul(const uint16_t *__restrict__ L, int Kc,
+                                                                const uint16_t *__restrict__ Wd, int M, int N, int K,
+                                                                const uint16_t *__restrict__ T, const uint16_t *__restrict__ U, int r,
+                                                                AdPlan p, uint16_t *__restrict__ out) {
+  using namespace gemm16;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[kLds];
+  const int cols = kNN ? K : N;
+  int tr, tc;
+  if (!place(blockIdx.x, (M + kBM - 1) / kBM, (cols + kBN - 1) / kBN, tr, tc)) return;
+  const int m0 = tr * kBM, c0 = tc * kBN;
+  f32x16_t acc[4][2];
+  tile<kNN>(smem, L, Kc, [&](int row) { return p.perm[min(m0 + row, M - 1)]; }, Wd, K, c0, cols - 1, N - 1, Kc / kBK, acc);
+
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 2, wn = wave & 3, lr = lane & 31, lh = lane >> 5;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int at = min(m0 + 128 * wm + 32 * i + lr, M - 1);
+    const int a = p.who[at];
+    const uint16_t *trow = T + static_cast<int64_t>(p.perm[at]) * r;
+    uint64_t left = __ballot(a >= 0);
+    while (left) {
+      const int a0 = __builtin_amdgcn_readlane(a, __builtin_ctzll(left));
+      const uint64_t mask = __ballot(a == a0);
+      left &= ~mask;
+      const uint16_t *u0 = U + (static_cast<int64_t>(a0) * cols + min(c0 + 64 * wn + lr, cols - 1)) * r;
+      const uint16_t *u1 = U + (static_cast<int64_t>(a0) * cols + min(c0 + 64 * wn + 32 + lr, cols - 1)) * r;
+      const bool whole = mask == ~uint64_t{0};
+      f32x16_t part[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) part[j][e] = whole ? acc[i][j][e] : 0.f;
+      for (int j0 = 0; j0 < r; j0 += 16) {
+        const int j = j0 + 8 * lh;
+        const bool ok = j < r;                    // r % 8 == 0
+        bf16x8_t tv = *reinterpret_cast<const bf16x8_t *>(trow + (ok ? j : 0));
+        bf16x8_t v0 = *reinterpret_cast<const bf16x8_t *>(u0 + (ok ? j : 0));
+        bf16x8_t v1 = *reinterpret_cast<const bf16x8_t *>(u1 + (ok ? j : 0));
+        if (!ok) tv = v0 = v1 = bf16x8_t{};
+        part[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v0, tv, part[0], 0, 0, 0);
+        part[1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v1, tv, part[1], 0, 0, 0);
+      }
+      const bool mine = a == a0;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][j][e] = whole ? part[j][e] : acc[i][j][e] + (mine ? part[j][e] : 0.f);
+    }
+  }
+  store_bf16(acc, smem, [&](int row, int col, uint4 v) {
+    if (m0 + row < M && c0 + col < cols)          // cols % 8 == 0
+      *reinterpret_cast<uint4 *>(out + static_cast<int64_t>(p.perm[m0 + row]) * cols + c0 + col) = v;
+  });
+}
+
+// ---------------------------------------------------------------------------
+// n matrices [rows, cols] -> [cols, pitch], zeros in the columns rows .. pitch - 1:
+// A [n, r, K] -> [n, K, r] and B [n, N, r] -> [n, r, N filled up to 64]: the
+// backward products then read their adapter operand along its rows.
+__global__ __launch_bounds__(256) void k_ad_transpose(const uint16_t *__restrict__ src, int rows, int cols, int pitch,
+                                                      uint16_t *__restrict__ dst) {
+  __shared__ uint16_t t[32][33];
+  src += static_cast<int64_t>(blockIdx.z) * rows * cols;
+  dst += static_cast<int64_t>(blockIdx.z) * cols * pitch;
+  const int r0 = blockIdx.x * 32, c0 = blockIdx.y * 32;
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+    t[y + i][x] = r0 + y + i < rows && c0 + x < cols ? src[static_cast<int64_t>(r0 + y + i) * cols + c0 + x] : 0;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+    if (c0 + y + i < cols && r0 + x < pitch) dst[static_cast<int64_t>(c0 + y + i) * pitch + r0 + x] = t[x][y + i];
+}
+
+// dst [M, pitch] = src [M, cols] and zeros; multiples of 8.
+__global__ __launch_bounds__(256) void k_ad_pad(const uint16_t *__restrict__ src, int M, int cols, int pitch, uint16_t *__restrict__ dst) {
+  const int per = pitch >> 3;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < static_cast<int64_t>(M) * per;
+       i += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t m = i / per;
+    const int c = 8 * static_cast<int>(i % per);
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (c < cols) v = *reinterpret_cast<const uint4 *>(src + m * cols + c);
+    *reinterpret_cast<uint4 *>(dst + m * pitch + c) = v;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// dA_a [r, K] = sum G_m^T X_m and dB_a [N, r] = sum dY_m^T T_m over an adapter's
+// run: acc[j][d] = sum_m Q[m][j] P[m][d] for 64 columns d of the wide operand
+// and 32 kJB columns j of the narrow one.  Workgroup (64-column chunk of X or
+// dY, adapter, chunk of r); wave w takes 32-token stages w, w + 4, ... of the run
+// in a private ring; both operands are read with the transposing LDS load.
+// Places past the run are read from a row of zeros.  Empty runs give zeros.
+namespace {
+constexpr int kGdWaves = 4;
+constexpr int kGdThreads = kGdWaves * 64;
+constexpr int kGdSlots = 3;
+constexpr int kGdTile = 32 * 128;
+constexpr int kGdSlot = 2 * kGdTile;   // P then Q
+
+// Byte offset in a [32 tokens][64 columns] swizzled tile of this lane's
+// source for the transposed read that hands lanes 16 G .. +15 columns
+// 32 cb + 16 (G % 2) .. +15 of tokens 8 (G / 2) + 4 h .. +3 (+ 16 s).
+__device__ __forceinline__ uint32_t gd_offset(int lane, int cb, int h) {
+  const int t = lane & 15, g = lane >> 4;
+  const int row = 8 * (g >> 1) + 4 * h + (t >> 2);
+  const int chunk = 4 * cb + 2 * (g & 1) + ((t & 3) >> 1);
+  return static_cast<uint32_t>(swz128(row, chunk) + 8 * (t & 1));
+}
+}  // namespace
+
+struct AdGradArgs {
+  const uint16_t *P[2], *Q[2];
+  uint16_t *out[2];
+  int D[2], chunks[2];   // columns of P; 64-column chunks (0: not wanted)
+  int r;
+};
+
+__global__ __launch_bounds__(kGdThreads) void k_ad_grads(AdGradArgs g, AdPlan p) {
+  __shared__ __attribute__((aligned(16))) uint8_t smem[kGdWaves][kGdSlots][kGdSlot];
+  const int which = static_cast<int>(blockIdx.x) < g.chunks[0] ? 0 : 1;
+  const int d0 = 64 * (static_cast<int>(blockIdx.x) - (which ? g.chunks[0] : 0));
+  const int a = blockIdx.y, j0 = 64 * blockIdx.z;
+  const uint16_t *P = g.P[which], *Q = g.Q[which];
+  const int D = g.D[which], r = g.r;
+  const int s0 = p.seg[a], s1 = p.seg[a + 1];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lr = lane & 31, lh = lane >> 5;
+  const int stages = (s1 - s0 + 31) >> 5;
+  const int n_i = wave < stages ? (stages - wave + kGdWaves - 1) / kGdWaves : 0;
+  const uint32_t ring = lds_addr(smem[wave][0]);
+  const bool two = r - j0 > 32;
+
+  // Token numbers of the stage to be issued next are loaded a step ahead; the
+  // DMA counter is not relied on for these register loads (the compiler waits).
+  int tokn[4];
+  auto tokens = [&](int i) __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int at = s0 + 32 * (wave + kGdWaves * i) + 8 * u + (lane >> 3);
+      tokn[u] = at < s1 ? p.perm[at] : -1;
+    }
+  };
+  auto issue = [&](int slot) __attribute__((always_inline)) {
+    const uint32_t dst = __builtin_amdgcn_readfirstlane(ring + slot * kGdSlot);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int row = 8 * u + (lane >> 3);
+      const int chunk = (lane & 7) ^ ((row & 7) ^ ((row >> 3) & 1));
+      const int m = tokn[u];
+      const int dc = min(d0 + 8 * chunk, D - 8);      // D % 8 == 0: columns past it are never stored
+      const int jc = min(j0 + 8 * chunk, r - 8);
+      const uint16_t *ps = m >= 0 ? P + static_cast<int64_t>(m) * D + dc : p.zero;
+      const uint16_t *qs = m >= 0 ? Q + static_cast<int64_t>(m) * r + jc : p.zero;
+      dma16(ps, dst + u * 1024);
+      dma16(qs, dst + kGdTile + u * 1024);
+    }
+  };
+  f32x16_t acc[2][2];   // [j block][d block]
+#pragma unroll
+  for (int jb = 0; jb < 2; ++jb)
+#pragma unroll
+    for (int db = 0; db < 2; ++db)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[jb][db][e] = 0.f;
+  uint32_t off[2][2];
+#pragma unroll
+  for (int cb = 0; cb < 2; ++cb)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) off[cb][h] = gd_offset(lane, cb, h);
+  auto operand = [&](const uint8_t *t, int cb, int s) __attribute__((always_inline)) {
+    const gemm16::bf16x4_t lo = gemm16::ds_tr16(t + off[cb][0] + 2048 * s);
+    const gemm16::bf16x4_t hi = gemm16::ds_tr16(t + off[cb][1] + 2048 * s);
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  };
+  if (n_i > 0) {
+    tokens(0);
+    issue(0);
+  }
+  if (n_i > 1) tokens(1);
+  for (int i = 0; i < n_i; ++i) {
+    const int slot = i & 1;
+    // The stage after next's token numbers come with the wait of this stage.
+    if (i + 1 < n_i) issue(slot ^ 1);
+    __builtin_amdgcn_sched_barrier(0);
+    if (i + 1 < n_i)
+      __builtin_amdgcn_s_waitcnt(wait_imm(8, 15));
+    else
+      __builtin_amdgcn_s_waitcnt(wait_imm(0, 15));
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_sched_barrier(0);
+    if (i + 2 < n_i) tokens(i + 2);
+    const uint8_t *ps = smem[wave][slot], *qs = ps + kGdTile;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const bf16x8_t x0 = operand(ps, 0, s), x1 = operand(ps, 1, s);
+      const bf16x8_t q0 = operand(qs, 0, s);
+      acc[0][0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(q0, x0, acc[0][0], 0, 0, 0);
+      acc[0][1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(q0, x1, acc[0][1], 0, 0, 0);
+      if (two) {
+        const bf16x8_t q1 = operand(qs, 1, s);
+        acc[1][0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(q1, x0, acc[1][0], 0, 0, 0);
+        acc[1][1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(q1, x1, acc[1][1], 0, 0, 0);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(wait_imm(63, 0));   // operand reads done before the slot is filled again
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  // lane: column d = lr of block db, row j = 8 (e / 4) + 4 lh + e % 4 of block jb.
+  // Sums over the waves in LDS, one j block (32 x 64 fp32) at a time.
+  __syncthreads();
+  for (int jb = 0; jb < (two ? 2 : 1); ++jb) {
+    float *red = reinterpret_cast<float *>(smem[wave][0]);
+#pragma unroll
+    for (int db = 0; db < 2; ++db)
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        red[(8 * (e >> 2) + 4 * lh + (e & 3)) * 64 + 32 * db + lr] = jb ? acc[1][db][e] : acc[0][db][e];
+    __syncthreads();
+    auto sum = [&](int j, int d) {
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < kGdWaves; ++w) v += reinterpret_cast<const float *>(smem[w][0])[j * 64 + d];
+      return v;
+    };
+    const int jr = min(32, r - j0 - 32 * jb);     // rows of this block, a multiple of 8
+    if (which == 0) {                             // [r][D]
+      for (int idx = threadIdx.x; idx < jr * 8; idx += kGdThreads) {
+        const int j = idx >> 3, d = 8 * (idx & 7);
+        if (d0 + d >= D) continue;
+        float v[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = sum(j, d + q);
+        *reinterpret_cast<uint4 *>(g.out[0] + (static_cast<int64_t>(a) * r + j0 + 32 * jb + j) * D + d0 + d) =
+            make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+      }
+    } else {                                      // [D][r]
+      for (int idx = threadIdx.x; idx < 64 * (jr >> 3); idx += kGdThreads) {
+        const int d = idx / (jr >> 3), j = 8 * (idx % (jr >> 3));
+        if (d0 + d >= D) continue;
+        float v[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = sum(j + q, d);
+        *reinterpret_cast<uint4 *>(g.out[1] + (static_cast<int64_t>(a) * D + d0 + d) * r + j0 + 32 * jb + j) =
+            make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------------------
+hipError_t launch_ad_small(const uint16_t *X, int M, const NF4View &w, const AdapterSet &ad, uint16_t *T, uint16_t *Y, hipStream_t s) {
+  const dim3 down((ad.r + 15) / 16, M), main((w.N + kAdRows - 1) / kAdRows), th(kAdThreads);
+  const int mb = (M + 15) / 16;
+  if (mb == 1)
+    hipLaunchKernelGGL(k_ad_down<1>, down, th, 0, s, X, M, w.K, ad.A, ad.r, ad.scale, ad.index, ad.n, T);
+  else
+    hipLaunchKernelGGL(k_ad_down<2>, down, th, 0, s, X, M, w.K, ad.A, ad.r, ad.scale, ad.index, ad.n, T);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  switch (mb) {
+    case 1: hipLaunchKernelGGL(k_ad_small<1>, main, th, 0, s, X, M, w, T, ad.B, ad.r, ad.index, ad.n, Y); break;
+    case 2: hipLaunchKernelGGL(k_ad_small<2>, main, th, 0, s, X, M, w, T, ad.B, ad.r, ad.index, ad.n, Y); break;
+    case 3: hipLaunchKernelGGL(k_ad_small<3>, main, th, 0, s, X, M, w, T, ad.B, ad.r, ad.index, ad.n, Y); break;
+    default: hipLaunchKernelGGL(k_ad_small<4>, main, th, 0, s, X, M, w, T, ad.B, ad.r, ad.index, ad.n, Y); break;
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_ad_sort(const AdapterSet &ad, int M, const AdPlan &p, hipStream_t s) {
+  hipLaunchKernelGGL(k_ad_sort, dim3(1), dim3(kSortThreads), 0, s, ad.index, M, ad.n, p);
+  return hipGetLastError();
+}
+
+hipError_t launch_ad_down(const uint16_t *P, int M, int D, const uint16_t *Q, const AdapterSet &ad, const AdPlan &p, uint16_t *out,
+                          hipStream_t s) {
+  const int tiles = static_cast<int>(ad_tiles_max(M, ad.n));
+  if (ad.r <= 32)
+    hipLaunchKernelGGL(k_ad_down_tiles<1>, dim3(tiles, 1), dim3(kDtThreads), 0, s, P, D, Q, ad.r, ad.scale, p, out);
+  else
+    hipLaunchKernelGGL(k_ad_down_tiles<2>, dim3(tiles, (ad.r + 63) / 64), dim3(kDtThreads), 0, s, P, D, Q, ad.r, ad.scale, p, out);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(k_ad_bare, dim3(std::min<int64_t>(256, (static_cast<int64_t>(M) * ad.r / 8 + 255) / 256)), dim3(256), 0, s, p, M,
+                     ad.n, ad.r, out);
+  return hipGetLastError();
+}
+
+template <bool kNN>
+static hipError_t launch_ad_matmul(const uint16_t *L, int Kc, int M, int N, int K, const uint16_t *Wd, const uint16_t *T,
+                                   const uint16_t *U, int r, const AdPlan &p, uint16_t *out, hipStream_t s) {
+  const int cols = kNN ? K : N;
+  const int tiles = ((M + gemm16::kBM - 1) / gemm16::kBM) * ((cols + gemm16::kBN - 1) / gemm16::kBN);
+  hipLaunchKernelGGL(k_ad_matmul<kNN>, dim3(tiles), dim3(gemm16::kThreads), 0, s, L, Kc, Wd, M, N, K, T, U, r, p, out);
+  return hipGetLastError();
+}
+hipError_t launch_ad_matmul_fwd(const uint16_t *X, int M, int N, int K, const uint16_t *Wd, const uint16_t *T, const uint16_t *B, int r,
+                                const AdPlan &p, uint16_t *Y, hipStream_t s) {
+  return launch_ad_matmul<false>(X, K, M, N, K, Wd, T, B, r, p, Y, s);
+}
+hipError_t launch_ad_matmul_dx(const uint16_t *dY, int Np, int M, int N, int K, const uint16_t *Wd, const uint16_t *G,
+                               const uint16_t *At, int r, const AdPlan &p, uint16_t *dX, hipStream_t s) {
+  return launch_ad_matmul<true>(dY, Np, M, N, K, Wd, G, At, r, p, dX, s);
+}
+
+hipError_t launch_ad_transpose(const uint16_t *src, int n, int rows, int cols, int pitch, uint16_t *dst, hipStream_t s) {
+  hipLaunchKernelGGL(k_ad_transpose, dim3((pitch + 31) / 32, (cols + 31) / 32, n), dim3(256), 0, s, src, rows, cols, pitch, dst);
+  return hipGetLastError();
+}
+
+hipError_t launch_ad_pad(const uint16_t *src, int M, int cols, int pitch, uint16_t *dst, hipStream_t s) {
+  const int64_t n = static_cast<int64_t>(M) * pitch / 8;
+  hipLaunchKernelGGL(k_ad_pad, dim3(static_cast<int>(std::min<int64_t>(4096, (n + 255) / 256))), dim3(256), 0, s, src, M, cols, pitch, dst);
+  return hipGetLastError();
+}
+
+hipError_t launch_ad_grads(const uint16_t *X, const uint16_t *dY, const uint16_t *G, const uint16_t *T, int N, int K, const AdapterSet &ad,
+                           const AdPlan &p, uint16_t *dA, uint16_t *dB, hipStream_t s) {
+  AdGradArgs g{{X, dY}, {G, T}, {dA, dB}, {K, N}, {dA ? (K + 63) / 64 : 0, dB ? (N + 63) / 64 : 0}, ad.r};
+  hipLaunchKernelGGL(k_ad_grads, dim3(g.chunks[0] + g.chunks[1], ad.n, (ad.r + 63) / 64), dim3(kGdThreads), 0, s, g, p);
+  return hipGetLastError();
+}
+
+}  // namespace qlora

@@ -313,4 +313,47 @@ hipError_t launch_distill_bwd(const Logits &l, const Teacher &t, const float *ls
 hipError_t launch_distill(const Logits &l, const Teacher &t, const float *weight, float *loss, float *lse, void *dz,
                           int64_t ldd, void *ws, hipStream_t s);
 
+// ---- many adapters beside one projection ------------------------------------------------
+constexpr int kAdSmall = 64;     // tokens up to which the decoding kernels run
+constexpr int kAdMax = 1023;     // adapters of a set (with the tokens that have none: a thread each of the sort)
+// A [n, r, K], B [n, N, r] bf16, scale [n]; index [M]: the adapter of a token.
+struct AdapterSet {
+  const uint16_t *A;
+  const uint16_t *B;
+  const float *scale;
+  const int64_t *index;
+  int n;
+  int r;
+};
+// The sorted order of the tokens (see k_ad_sort).
+struct AdPlan {
+  int *perm;
+  int *who;
+  int *seg;
+  int4 *tile;
+  int *ntile;
+  uint16_t *zero;
+};
+// 32-token tiles of one adapter each that M tokens of n adapters can make.
+inline int64_t ad_tiles_max(int64_t M, int64_t n) { return (M + 31) / 32 + (M < n ? M : n); }
+// M <= kAdSmall.  T [M, r] is written too.
+hipError_t launch_ad_small(const uint16_t *X, int M, const NF4View &w, const AdapterSet &ad, uint16_t *T, uint16_t *Y, hipStream_t s);
+hipError_t launch_ad_sort(const AdapterSet &ad, int M, const AdPlan &p, hipStream_t s);
+// out [M, r] = scale_a P Q_a^T, P [M, D], Q [n, r, D], D % 64 == 0; zeros for tokens without an adapter.
+hipError_t launch_ad_down(const uint16_t *P, int M, int D, const uint16_t *Q, const AdapterSet &ad, const AdPlan &p, uint16_t *out,
+                          hipStream_t s);
+// Y [M, N] = X Wd^T + T B_a^T; dX [M, K] = dY Wd + G A_a with At [n, K, r] and dY's
+// rows filled up to Np, a multiple of 64, with zeros.
+hipError_t launch_ad_matmul_fwd(const uint16_t *X, int M, int N, int K, const uint16_t *Wd, const uint16_t *T, const uint16_t *B, int r,
+                                const AdPlan &p, uint16_t *Y, hipStream_t s);
+hipError_t launch_ad_matmul_dx(const uint16_t *dY, int Np, int M, int N, int K, const uint16_t *Wd, const uint16_t *G,
+                               const uint16_t *At, int r, const AdPlan &p, uint16_t *dX, hipStream_t s);
+// n matrices [rows, cols] -> [cols, pitch], pitch >= rows, zeros behind.
+hipError_t launch_ad_transpose(const uint16_t *src, int n, int rows, int cols, int pitch, uint16_t *dst, hipStream_t s);
+// dst [M, pitch] = src [M, cols], zeros behind; multiples of 8.
+hipError_t launch_ad_pad(const uint16_t *src, int M, int cols, int pitch, uint16_t *dst, hipStream_t s);
+// dA [n, r, K] and dB [n, N, r], either nullable.
+hipError_t launch_ad_grads(const uint16_t *X, const uint16_t *dY, const uint16_t *G, const uint16_t *T, int N, int K, const AdapterSet &ad,
+                           const AdPlan &p, uint16_t *dA, uint16_t *dB, hipStream_t s);
+
 }  // namespace qlora

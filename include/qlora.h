@@ -659,6 +659,47 @@ int qlora_distill_bwd(const qlora_logits *l, const qlora_teacher *t, const float
 int qlora_distill(const qlora_logits *l, const qlora_teacher *t, const float *weight, float *loss, float *lse, void *dz,
                   int64_t dz_pitch, void *ws, size_t ws_bytes, void *stream);
 
+/* ---- Many adapters beside one frozen projection ----------------------------------
+ * The linear layer of a server whose requests come with adapters of their own, or of
+ * a run that tunes several over one base (the pages' point that adapters are
+ * small beside the base that they share: automatone.win, "QLoRA paper explained",
+ * The problem).  Token m's adapter is a = index[m]; an index outside [0, count) is a token on
+ * the bare base.
+ *   T_m  = scale_a X_m A_a^T          Y_m  = X_m deq(W)^T + T_m B_a^T
+ *   G_m  = scale_a dY_m B_a           dX_m = dY_m deq(W) + G_m A_a
+ *   dA_a = sum of G_m^T X_m,  dB_a = sum of dY_m^T T_m  over the adapter's tokens m
+ * T and G are rounded to bf16 between their products, as in qlora_linear_fwd; those of a
+ * token without an adapter are 0.  Tokens need no order.  What one adapter or token holds,
+ * NaN and infinities included, reaches no other token's outputs and no other
+ * adapter's gradients.  Sums are fp32 and in a fixed order. */
+
+/* count adapters of one rank r: A [count][r][K], B [count][N][r] in bf16, scale
+ * [count], index [M] (8-byte aligned).  Adapters of smaller rank are filled up with
+ * zeros (rows of A, columns of B).  1 <= count <= 1023, r % 8 == 0, 8 <= r <= 128. */
+typedef struct {
+  const uint16_t *A;
+  const uint16_t *B;
+  const float *scale;
+  const int64_t *index;
+  int32_t count;
+  int32_t r;
+} qlora_adapters;
+
+/* Workspace bytes of the two passes below (0 at M = 0 or for an unsupported shape). */
+size_t qlora_adapter_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t count, int32_t r, int is_bwd);
+
+/* Y [M, N]; T_out [M, r] (nullable) receives T.  Shapes as in qlora_linear_fwd
+ * (K % 64 == 0, N % 8 == 0; M times K, and M times N filled up to 64, below 2^31). */
+int qlora_adapter_linear_fwd(const uint16_t *X, int64_t M, const qlora_nf4_weight *W, const qlora_adapters *ad, uint16_t *Y,
+                             uint16_t *T_out, void *ws, size_t ws_bytes, void *stream);
+
+/* dX [M, K], dA [count][r][K] and dB [count][N][r], each nullable; T as the forward
+ * returned it, or NULL (recomputed).  An adapter without tokens has zero
+ * gradients.  M = 0 writes nothing. */
+int qlora_adapter_linear_bwd(const uint16_t *dY, const uint16_t *X, const uint16_t *T, int64_t M, const qlora_nf4_weight *W,
+                             const qlora_adapters *ad, uint16_t *dX, uint16_t *dA, uint16_t *dB, void *ws, size_t ws_bytes,
+                             void *stream);
+
 #ifdef __cplusplus
 }
 #endif
