@@ -14,6 +14,7 @@ from .ops import (Q4_TYPES, NF4Weight, QLoRALinear, QLoRALinearFn, linear_bwd, l
                   lora_grads_group, nf4_matmul_fwd_group, deq_matmul_fwd, deq_matmul_fwd_group, deq_matmul_dx)
 from .mx4 import MX4Linear, MX4LinearFn, MX4Tensor, mx4_linear_bwd, mx4_linear_fwd, mx4_matmul  # noqa: F401
 from .adapters import AdapterLinear, AdapterLinearFn, adapter_linear_bwd, adapter_linear_fwd  # noqa: F401
+from .head import HeadCrossEntropyFn, head_cross_entropy, head_cross_entropy_dW, head_cross_entropy_fwd  # noqa: F401
 from .vocab import (DistillTopKFn, TokenLogprobs, TokenLogprobsFn, distill_topk, distill_topk_bwd,  # noqa: F401
                     distill_topk_fwd, token_logprobs, token_logprobs_bwd)
 
@@ -25,6 +26,7 @@ __all__ = [
     "deq_matmul_fwd", "deq_matmul_fwd_group", "deq_matmul_dx",
     "MX4Tensor", "MX4Linear", "MX4LinearFn", "mx4_matmul", "mx4_linear_fwd", "mx4_linear_bwd",
     "AdapterLinear", "AdapterLinearFn", "adapter_linear_fwd", "adapter_linear_bwd",
+    "head_cross_entropy", "head_cross_entropy_fwd", "head_cross_entropy_dW", "HeadCrossEntropyFn",
     "token_logprobs", "token_logprobs_bwd", "TokenLogprobs", "TokenLogprobsFn",
     "distill_topk", "distill_topk_fwd", "distill_topk_bwd", "DistillTopKFn", "QLoRAError", "status_string",
 ]

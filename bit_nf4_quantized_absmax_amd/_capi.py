@@ -34,6 +34,7 @@ EXPORTED = (
     "qlora_vocab_workspace_bytes", "qlora_token_logprobs", "qlora_token_logprobs_bwd",
     "qlora_distill_fwd", "qlora_distill_bwd", "qlora_distill",
     "qlora_adapter_linear_workspace_bytes", "qlora_adapter_linear_fwd", "qlora_adapter_linear_bwd",
+    "qlora_head_workspace_bytes", "qlora_head_cross_entropy", "qlora_head_scale", "qlora_head_cross_entropy_dW",
     "qlora_dropout_mask", "qlora_dropout_apply", "qlora_nf4_matmul_dx_dropout",
     "qlora_linear_dropout_workspace_bytes", "qlora_linear_fwd_dropout", "qlora_linear_bwd_dropout",
 )
@@ -211,6 +212,10 @@ _SIGS = {
     "qlora_adapter_linear_workspace_bytes": (_sz, [_i64, _i64, _i64, _i32, _i32, ctypes.c_int]),
     "qlora_adapter_linear_fwd": (ctypes.c_int, [_vp, _i64, _wp, _ap, _vp, _vp, _vp, _sz, _vp]),
     "qlora_adapter_linear_bwd": (ctypes.c_int, [_vp, _vp, _vp, _i64, _wp, _ap, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "qlora_head_workspace_bytes": (_sz, [_i64, _i64, _i64, _i32]),
+    "qlora_head_cross_entropy": (ctypes.c_int, [_vp, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _sz, _vp]),
+    "qlora_head_scale": (ctypes.c_int, [_vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp]),
+    "qlora_head_cross_entropy_dW": (ctypes.c_int, [_vp, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "qlora_dropout_mask": (ctypes.c_int, [_vp, _i64, _i64, _f32, ctypes.c_uint64, _vp, _vp, _vp]),
     "qlora_dropout_apply": (ctypes.c_int, [_vp, _i64, _i64, _vp, _vp, _vp]),
     "qlora_nf4_matmul_dx_dropout": (ctypes.c_int, [_vp, _i64, _wp, _vp, _vp, _i32, _vp, _vp, _vp]),

@@ -30,19 +30,6 @@ NF4View view_of(const qlora_nf4_weight *w) {
 
 AdapterSet set_of(const qlora_adapters *a) { return AdapterSet{a->A, a->B, a->scale, a->index, a->count, a->r}; }
 
-// The parts of a workspace, in order, each on 256 bytes.
-struct Carve {
-  char *base;
-  size_t used = 0;
-  explicit Carve(void *p) : base(static_cast<char *>(p)) {}
-  template <class T>
-  T *take(size_t n) {
-    T *p = reinterpret_cast<T *>(base + used);
-    used += round_up(n * sizeof(T), 256);
-    return p;
-  }
-};
-
 AdPlan take_plan(Carve &c, int64_t M, int64_t n) {
   AdPlan p;
   p.perm = c.take<int>(M);

@@ -43,4 +43,17 @@ inline BwdWs bwd_ws(int64_t M, int64_t N, int64_t K, int32_t r) {
   return w;
 }
 
+// The parts of a workspace, in order, each on 256 bytes.
+struct Carve {
+  char *base;
+  size_t used = 0;
+  explicit Carve(void *p) : base(static_cast<char *>(p)) {}
+  template <class T>
+  T *take(size_t n) {
+    T *p = reinterpret_cast<T *>(base + used);
+    used += round_up(n * sizeof(T), 256);
+    return p;
+  }
+};
+
 }  // namespace qlora

@@ -122,6 +122,15 @@ __device__ __forceinline__ void mfma_rows(const Frag &f, f32x16_t (&acc)[4][2]) 
     for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.b[j], f.a[i], acc[i][j], 0, 0, 0);
 }
 
+__device__ __forceinline__ void clear(f32x16_t (&acc)[4][2]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+}
+
 // This thread's place in the four 1 KB DMA instructions of a stage with
 // 128-byte rows: row(j) of the tile, and the chunk that lands at its position.
 struct RowDma {
@@ -183,12 +192,7 @@ __device__ __forceinline__ void tile(uint8_t *smem, const uint16_t *L, uint32_t 
     }
   };
   const Offsets ops = offsets();
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+  clear(acc);
   dma_l(0, 0);
   dma_r(0, 0);
   raw_barrier<wait_imm(0, 0)>();

@@ -356,4 +356,36 @@ hipError_t launch_ad_pad(const uint16_t *src, int M, int cols, int pitch, uint16
 hipError_t launch_ad_grads(const uint16_t *X, const uint16_t *dY, const uint16_t *G, const uint16_t *T, int N, int K, const AdapterSet &ad,
                            const AdPlan &p, uint16_t *dA, uint16_t *dB, hipStream_t s);
 
+// ---- cross entropy through the output head ------------------------------------------------
+// The rows that have a target, and what is known of each (see head.hip).
+struct HeadRows {
+  int *place;      // [M]
+  int *list;       // [M], count[0] of them in use
+  int *tgt;
+  int *count;      // [1]
+  float *zt;       // logit of the target
+  float *ref;
+  double *sum;
+  float *factor;
+};
+struct HeadPiece {
+  float2 *part;    // [64-word group][rows]
+  uint16_t *E;     // [rows][pitch], nullptr without a gradient
+  int rows;        // M
+  int pitch;       // the piece's words filled up to 64
+};
+hipError_t launch_head_rows(const int64_t *target, int M, int V, const HeadRows &h, hipStream_t s);
+// Xc [M filled up to 64, K]
+hipError_t launch_head_gather(const uint16_t *X, int M, int K, const HeadRows &h, uint16_t *Xc, hipStream_t s);
+// Words v0 .. v0 + words - 1; C [splits][M][K] fp32, or nullptr without a gradient.
+hipError_t launch_head_piece(const uint16_t *Xc, int M, const uint16_t *W, int V, int K, int v0, int words, bool first, const HeadRows &h,
+                             const HeadPiece &pc, int splits, float *C, hipStream_t s);
+// grad 0: none, 1: dX in bf16, 2: in fp32.
+hipError_t launch_head_finish(const uint16_t *W, int64_t M, int K, const float *weight, const HeadRows &h, int splits, const float *C,
+                              float *loss, float *lse, void *dX, int grad, hipStream_t s);
+hipError_t launch_head_scale(const float *D, int64_t M, int K, const int64_t *target, int V, const float *g, uint16_t *dX, hipStream_t s);
+// Rows v0 .. v0 + words - 1 of dW; Zt [words, M filled up to 64].
+hipError_t launch_head_dw(const uint16_t *Xc, int M, const uint16_t *W, int K, int v0, int words, const HeadRows &h, const float *lse,
+                          const float *weight, uint16_t *Zt, uint16_t *dW, hipStream_t s);
+
 }  // namespace qlora

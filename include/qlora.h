@@ -700,6 +700,39 @@ int qlora_adapter_linear_bwd(const uint16_t *dY, const uint16_t *X, const uint16
                              const qlora_adapters *ad, uint16_t *dX, uint16_t *dA, uint16_t *dB, void *ws, size_t ws_bytes,
                              void *stream);
 
+/* ---- Cross entropy through a frozen output head --------------------------------------
+ * The loss of a tuned model's next words from its last hidden states, without the
+ * matrix of logits (z [M, V] is the largest array of a step: at 8192 tokens and 128 000
+ * words 2 GB in bf16, and again for its gradient).  X [M, K] and W [V, K] in bf16,
+ * z = X W^T in fp32, target [M] int64:
+ *   loss_m = log sum_j e^z_mj - z_m,t,   t = target[m]
+ *   dz_mj  = weight_m (p_mj - [j = t]),  p = softmax(z);   dX = dz W,   dW = dz^T X
+ * A target outside [0, V) (prompt, padding) is no target: loss 0 and gradient 0,
+ * whatever X and weight hold there; such rows cost nothing.  The vocabulary is taken in
+ * pieces; e^z (dW: dz) is rounded to bf16 between the two products, except the
+ * target's own term; sums are fp32, over words 64 bits.  A NaN or an infinity of a row of X
+ * makes that row's loss and dX NaN.  K % 64 == 0, M <= 2^22, M K < 2^31, K <= 2^18, V < 2^31. */
+
+typedef enum { QLORA_HEAD_LOSS = 0, QLORA_HEAD_DX = 1, QLORA_HEAD_DW = 2 } qlora_head_pass;
+
+/* Workspace bytes of a pass (qlora_head_cross_entropy without or with dX, its _dW). */
+size_t qlora_head_workspace_bytes(int64_t M, int64_t V, int64_t K, int32_t pass);
+
+/* loss [M], and lse [M][2], a pair (reference, rest) whose sum is log sum_j e^z_mj
+ * (0, 0 without a target).  dX (nullable): [M, K], of bf16 (dx_fp32 0) or fp32 (1), for
+ * gradients weight [M] (NULL: 1) of the losses: two products where loss and gradient
+ * come from one call, as with a step's weights known beforehand. */
+int qlora_head_cross_entropy(const uint16_t *X, int64_t M, const uint16_t *W, int64_t V, int64_t K, const int64_t *target,
+                             const float *weight, float *loss, float *lse, void *dX, int32_t dx_fp32, void *ws, size_t ws_bytes,
+                             void *stream);
+
+/* dX [M, K] bf16 = g_m D_m from that call's fp32 gradient D at weight 1. */
+int qlora_head_scale(const float *D, int64_t M, int64_t V, int64_t K, const int64_t *target, const float *g, uint16_t *dX, void *stream);
+
+/* dW [V, K] bf16, for a head that is tuned too, from that call's lse (the logits are made again).  M = 0 writes nothing. */
+int qlora_head_cross_entropy_dW(const uint16_t *X, int64_t M, const uint16_t *W, int64_t V, int64_t K, const int64_t *target,
+                                const float *lse, const float *weight, uint16_t *dW, void *ws, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
