@@ -15,6 +15,7 @@ from .ops import (Q4_TYPES, NF4Weight, QLoRALinear, QLoRALinearFn, linear_bwd, l
 from .mx4 import MX4Linear, MX4LinearFn, MX4Tensor, mx4_linear_bwd, mx4_linear_fwd, mx4_matmul  # noqa: F401
 from .adapters import AdapterLinear, AdapterLinearFn, adapter_linear_bwd, adapter_linear_fwd  # noqa: F401
 from .head import HeadCrossEntropyFn, head_cross_entropy, head_cross_entropy_dW, head_cross_entropy_fwd  # noqa: F401
+from .gradnorm import clip_grad_norm, grad_norm  # noqa: F401
 from .vocab import (DistillTopKFn, TokenLogprobs, TokenLogprobsFn, distill_topk, distill_topk_bwd,  # noqa: F401
                     distill_topk_fwd, token_logprobs, token_logprobs_bwd)
 
@@ -27,6 +28,7 @@ __all__ = [
     "MX4Tensor", "MX4Linear", "MX4LinearFn", "mx4_matmul", "mx4_linear_fwd", "mx4_linear_bwd",
     "AdapterLinear", "AdapterLinearFn", "adapter_linear_fwd", "adapter_linear_bwd",
     "head_cross_entropy", "head_cross_entropy_fwd", "head_cross_entropy_dW", "HeadCrossEntropyFn",
+    "grad_norm", "clip_grad_norm",
     "token_logprobs", "token_logprobs_bwd", "TokenLogprobs", "TokenLogprobsFn",
     "distill_topk", "distill_topk_fwd", "distill_topk_bwd", "DistillTopKFn", "QLoRAError", "status_string",
 ]

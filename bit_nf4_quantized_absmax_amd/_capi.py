@@ -35,6 +35,7 @@ EXPORTED = (
     "qlora_distill_fwd", "qlora_distill_bwd", "qlora_distill",
     "qlora_adapter_linear_workspace_bytes", "qlora_adapter_linear_fwd", "qlora_adapter_linear_bwd",
     "qlora_head_workspace_bytes", "qlora_head_cross_entropy", "qlora_head_scale", "qlora_head_cross_entropy_dW",
+    "qlora_grad_norm_workspace_bytes", "qlora_grad_norm", "qlora_clip_grad_norm",
     "qlora_dropout_mask", "qlora_dropout_apply", "qlora_nf4_matmul_dx_dropout",
     "qlora_linear_dropout_workspace_bytes", "qlora_linear_fwd_dropout", "qlora_linear_bwd_dropout",
 )
@@ -216,6 +217,9 @@ _SIGS = {
     "qlora_head_cross_entropy": (ctypes.c_int, [_vp, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _sz, _vp]),
     "qlora_head_scale": (ctypes.c_int, [_vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp]),
     "qlora_head_cross_entropy_dW": (ctypes.c_int, [_vp, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "qlora_grad_norm_workspace_bytes": (_sz, [_i32, _vp, _i32]),
+    "qlora_grad_norm": (ctypes.c_int, [_i32, _vp, _i32, _vp, _vp, _sz, _vp]),
+    "qlora_clip_grad_norm": (ctypes.c_int, [_i32, _vp, _i32, _f32, _vp, _vp, _sz, _vp]),
     "qlora_dropout_mask": (ctypes.c_int, [_vp, _i64, _i64, _f32, ctypes.c_uint64, _vp, _vp, _vp]),
     "qlora_dropout_apply": (ctypes.c_int, [_vp, _i64, _i64, _vp, _vp, _vp]),
     "qlora_nf4_matmul_dx_dropout": (ctypes.c_int, [_vp, _i64, _wp, _vp, _vp, _i32, _vp, _vp, _vp]),

@@ -388,4 +388,36 @@ hipError_t launch_head_scale(const float *D, int64_t M, int K, const int64_t *ta
 hipError_t launch_head_dw(const uint16_t *Xc, int M, const uint16_t *W, int K, int v0, int words, const HeadRows &h, const float *lse,
                           const float *weight, uint16_t *Zt, uint16_t *dW, hipStream_t s);
 
+// ---- norm of many tensors and clipping by it ------------------------------------------
+struct GradTensor {
+  const void *x;
+  void *y;
+  int64_t count;
+  int type;        // 0 fp32, 1 bf16, 2 fp16
+  int first;       // its first chunk within a group
+};
+constexpr int kGradList = 120;   // tensors of one launch's list: 4 KB of arguments hold 128
+struct GradList {
+  GradTensor t[kGradList];
+};
+struct GradChunk {
+  const void *x;
+  void *y;
+  int count;
+  int type;
+  int group;
+  int lead;        // the one of its group that writes the norm
+};
+struct GradPlan {
+  GradChunk *table;   // [groups][stride]
+  double *sums;       // likewise
+  int groups;
+  int stride;         // chunks of a group
+  int chunk;          // elements of a chunk
+};
+// Chunks of tensors base .. base + n - 1 of the call into the table.
+hipError_t launch_grad_chunks(const GradList &l, int n, const GradPlan &p, int base, hipStream_t s);
+// norm [groups]; max_norm (nullable): clipped into every y.
+hipError_t launch_grad_norm(const GradPlan &p, const float *max_norm, float *norm, hipStream_t s);
+
 }  // namespace qlora

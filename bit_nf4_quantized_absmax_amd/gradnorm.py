@@ -1,0 +1,91 @@
+"""The norm of many gradients and clipping by it (formulas and rules in the C
+ABI's header).  Argument marshalling only, as in ops.py; a model's gradients are
+hundreds of small tensors, so they are looked at attribute by attribute, over
+the whole list at a time."""
+
+import ctypes
+from operator import attrgetter
+
+import torch
+
+from ._capi import check, lib
+from .adapters import _on
+from .ops import _ptr, _stream, _workspace
+
+TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+_dtype = attrgetter("dtype")
+_shape = attrgetter("shape")
+
+
+def _listed(tensors, name):
+    """(data pointers, element counts, types, device index or None) of a list of tensors."""
+    for t in tensors:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("%s must be tensors" % name)
+    try:
+        types = list(map(TYPES.__getitem__, map(_dtype, tensors)))
+    except KeyError as e:
+        raise TypeError("%s must be float32, bfloat16 or float16, got %s" % (name, e.args[0])) from None
+    if not all(map(torch.Tensor.is_contiguous, tensors)):
+        raise ValueError("%s must be contiguous" % name)
+    devices = set(map(torch.Tensor.get_device, tensors))
+    if len(devices) > 1 or -1 in devices:
+        raise ValueError("%s must be on one GPU device" % name)
+    return list(map(torch.Tensor.data_ptr, tensors)), list(map(torch.Tensor.numel, tensors)), types, devices.pop() if devices else None
+
+
+def _call(grads, max_norm, groups, out, workspace):
+    grads = list(grads)
+    ptrs, counts, types, device = _listed(grads, "grads")
+    groups = int(groups)
+    if groups < 1:
+        raise ValueError("groups must be at least 1")
+    if device is None:
+        raise ValueError("no gradients: the norm has no device to go to")
+    if groups > 1:
+        for t in grads:
+            if t.dim() == 0 or t.shape[0] % groups:
+                raise ValueError("every gradient's first axis must hold %d equal parts, got shape %s" % (groups, tuple(t.shape)))
+    to = ptrs
+    if max_norm is not None:
+        if out is not None:
+            out = list(out)
+            to, _, to_types, to_device = _listed(out, "out")
+            if to_types != types or list(map(_shape, out)) != list(map(_shape, grads)) or to_device != device:
+                raise ValueError("out must be one tensor of the same shape, type and device for every gradient")
+        used = [p for p, n in zip(to, counts) if n]
+        if len(set(used)) != len(used):
+            raise ValueError("a tensor is written twice")
+    n = len(grads)
+    flat = [0] * (4 * n)
+    flat[0::4], flat[1::4], flat[2::4], flat[3::4] = ptrs, to, counts, types
+    table = (ctypes.c_int64 * (4 * n))(*flat)     # qlora_grad_tensor [n]
+    first = grads[0]
+    norm = torch.empty(groups, dtype=torch.float32, device=first.device)
+    ws, ws_bytes = _workspace(workspace, lib().qlora_grad_norm_workspace_bytes(n, table, groups), first.device)
+    with _on(first.device, ws):
+        if max_norm is None:
+            check(lib().qlora_grad_norm(n, table, groups, _ptr(norm), _ptr(ws), ws_bytes, _stream(first)), "qlora_grad_norm")
+        else:
+            check(lib().qlora_clip_grad_norm(n, table, groups, float(max_norm), _ptr(norm), _ptr(ws), ws_bytes, _stream(first)),
+                  "qlora_clip_grad_norm")
+    return norm
+
+
+def grad_norm(grads, groups=1, workspace=None):
+    """The norm (float32 [groups]) of the elements of all tensors (float32,
+    bfloat16 or float16, contiguous, on one device).  groups > 1: every tensor's
+    first axis holds that many equal parts, as stacked adapters' gradients do, and
+    part g counts for norm g (qlora_grad_norm)."""
+    return _call(grads, None, groups, None, workspace)
+
+
+def clip_grad_norm(grads, max_norm, groups=1, out=None, workspace=None):
+    """grad_norm, and the gradients times min(1, max_norm / (norm + 1e-6)), in
+    place or into `out` (a tensor for every gradient, which overlaps no gradient but
+    its own).  Returns the norms before clipping (qlora_clip_grad_norm)."""
+    max_norm = float(max_norm)
+    if not max_norm >= 0.0:
+        raise ValueError("max_norm must not be negative or NaN")
+    return _call(grads, max_norm, groups, out, workspace)

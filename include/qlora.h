@@ -733,6 +733,39 @@ int qlora_head_scale(const float *D, int64_t M, int64_t V, int64_t K, const int6
 int qlora_head_cross_entropy_dW(const uint16_t *X, int64_t M, const uint16_t *W, int64_t V, int64_t K, const int64_t *target,
                                 const float *lse, const float *weight, uint16_t *dW, void *ws, size_t ws_bytes, void *stream);
 
+/* ---- The norm of many gradients, and clipping by it ------------------------------------
+ * What stands between a step's backward passes and its optimizer: the gradients of
+ * every adapter pair (lora_grads, adapter_linear_bwd: hundreds of small tensors) scaled so that their
+ * common norm is max_norm at most.
+ *   norm_g = sqrt(sum of x^2 over group g)      out = x min(1, max_norm / (norm_g + 1e-6))
+ * Every tensor holds `groups` equal parts one behind the other, part g of group g: 1 for
+ * one norm of all, the number of adapters for stacked gradients [count][...] whose
+ * adapters are clipped each by its own norm.  Squares are summed in 64 bits in a fixed order.
+ * A NaN or an infinity makes its group's norm NaN or infinite, and so the
+ * group's results NaN (x times 0 for the finite ones under an infinite norm). */
+
+/* One contiguous tensor: count elements of `type` (0: fp32, else QLORA_IN_BF16 or
+ * QLORA_IN_FP16), aligned to its element.  out (clipping only): where the
+ * result goes, of the same type, x itself or storage that overlaps no x of the call. */
+typedef struct {
+  const void *x;
+  void *out;
+  int64_t count;
+  int64_t type;
+} qlora_grad_tensor;
+
+/* Workspace bytes of the two calls (0 for bad arguments or where no element is given). */
+size_t qlora_grad_norm_workspace_bytes(int32_t count, const qlora_grad_tensor *t, int32_t groups);
+
+/* norm [groups] fp32.  t is a host array, read before the call returns.  count may be
+ * 0; every tensor's count is a multiple of groups (else UNSUPPORTED_SHAPE, as
+ * over 65536 tensors, 4096 groups or 2^23 parts of tensors are). */
+int qlora_grad_norm(int32_t count, const qlora_grad_tensor *t, int32_t groups, float *norm, void *ws, size_t ws_bytes, void *stream);
+
+/* The same, and every tensor's clipped values in its out; no tensor twice.  max_norm >= 0, or infinite. */
+int qlora_clip_grad_norm(int32_t count, const qlora_grad_tensor *t, int32_t groups, float max_norm, float *norm, void *ws, size_t ws_bytes,
+                         void *stream);
+
 #ifdef __cplusplus
 }
 #endif
