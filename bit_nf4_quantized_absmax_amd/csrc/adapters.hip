@@ -472,25 +472,26 @@ __global__ __launch_bounds__(256) void k_ad_bare(AdPlan p, int M, int n, int r, 
 // blocks have one adapter and accumulate in place; in the others the product is
 // formed apart and added in the lanes whose token has this adapter.
 // Kc, L's row pitch: a multiple of 64; NN: columns N .. Kc - 1 of L are zero.
-template <bool kNN>
-__global__ __launch_bounds__(gemm16::kThreads) void k_ad_matmul(const uint16_t *__restrict__ L, int Kc,
+template <class S, bool kNN>
+__global__ __launch_bounds__(S::kThreads, 2) void k_ad_matmul(const uint16_t *__restrict__ L, int Kc,
                                                                 const uint16_t *__restrict__ Wd, int M, int N, int K,
                                                                 const uint16_t *__restrict__ T, const uint16_t *__restrict__ U, int r,
                                                                 AdPlan p, uint16_t *__restrict__ out) {
   using namespace gemm16;
-  __shared__ __attribute__((aligned(16))) uint8_t smem[kLds];
+  __shared__ __attribute__((aligned(16))) uint8_t smem[S::kLds];
   const int cols = kNN ? K : N;
   int tr, tc;
-  if (!place(blockIdx.x, (M + kBM - 1) / kBM, (cols + kBN - 1) / kBN, tr, tc)) return;
-  const int m0 = tr * kBM, c0 = tc * kBN;
-  f32x16_t acc[4][2];
-  tile<kNN>(smem, L, Kc, [&](int row) { return p.perm[min(m0 + row, M - 1)]; }, Wd, K, c0, cols - 1, N - 1, Kc / kBK, acc);
+  if (!place(blockIdx.x, (M + S::kBM - 1) / S::kBM, (cols + S::kBN - 1) / S::kBN, tr, tc)) return;
+  const int m0 = tr * S::kBM, c0 = tc * S::kBN;
+  Acc<S> acc;
+  tile<S, kNN>(smem, L, Kc, [&](int row) { return p.perm[min(m0 + row, M - 1)]; }, Wd, K, c0, cols - 1, N - 1, Kc / kBK, acc);
 
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave >> 2, wn = wave & 3, lr = lane & 31, lh = lane >> 5;
+  const Place<S> w;
+  const int lr = w.lr, lh = w.lh, cw = c0 + w.col0();
+  static_assert(S::kFN == 2, "two column fragments a wave");
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int at = min(m0 + 128 * wm + 32 * i + lr, M - 1);
+  for (int i = 0; i < S::kFM; ++i) {
+    const int at = min(m0 + w.row0() + 32 * i + lr, M - 1);
     const int a = p.who[at];
     const uint16_t *trow = T + static_cast<int64_t>(p.perm[at]) * r;
     uint64_t left = __ballot(a >= 0);
@@ -498,8 +499,8 @@ __global__ __launch_bounds__(gemm16::kThreads) void k_ad_matmul(const uint16_t *
       const int a0 = __builtin_amdgcn_readlane(a, __builtin_ctzll(left));
       const uint64_t mask = __ballot(a == a0);
       left &= ~mask;
-      const uint16_t *u0 = U + (static_cast<int64_t>(a0) * cols + min(c0 + 64 * wn + lr, cols - 1)) * r;
-      const uint16_t *u1 = U + (static_cast<int64_t>(a0) * cols + min(c0 + 64 * wn + 32 + lr, cols - 1)) * r;
+      const uint16_t *u0 = U + (static_cast<int64_t>(a0) * cols + min(cw + lr, cols - 1)) * r;
+      const uint16_t *u1 = U + (static_cast<int64_t>(a0) * cols + min(cw + 32 + lr, cols - 1)) * r;
       const bool whole = mask == ~uint64_t{0};
       f32x16_t part[2];
 #pragma unroll
@@ -523,7 +524,7 @@ __global__ __launch_bounds__(gemm16::kThreads) void k_ad_matmul(const uint16_t *
         for (int e = 0; e < 16; ++e) acc[i][j][e] = whole ? part[j][e] : acc[i][j][e] + (mine ? part[j][e] : 0.f);
     }
   }
-  store_bf16(acc, smem, [&](int row, int col, uint4 v) {
+  store_bf16<S>(acc, smem, [&](int row, int col, uint4 v) {
     if (m0 + row < M && c0 + col < cols)          // cols % 8 == 0
       *reinterpret_cast<uint4 *>(out + static_cast<int64_t>(p.perm[m0 + row]) * cols + c0 + col) = v;
   });
@@ -768,13 +769,19 @@ hipError_t launch_ad_down(const uint16_t *P, int M, int D, const uint16_t *Q, co
   return hipGetLastError();
 }
 
+template <class S, bool kNN>
+static hipError_t launch_ad_tiles(const uint16_t *L, int Kc, int M, int N, int K, const uint16_t *Wd, const uint16_t *T, const uint16_t *U,
+                                  int r, const AdPlan &p, uint16_t *out, hipStream_t s) {
+  const int cols = kNN ? K : N;
+  const int tiles = ((M + S::kBM - 1) / S::kBM) * ((cols + S::kBN - 1) / S::kBN);
+  hipLaunchKernelGGL((k_ad_matmul<S, kNN>), dim3(tiles), dim3(S::kThreads), 0, s, L, Kc, Wd, M, N, K, T, U, r, p, out);
+  return hipGetLastError();
+}
 template <bool kNN>
 static hipError_t launch_ad_matmul(const uint16_t *L, int Kc, int M, int N, int K, const uint16_t *Wd, const uint16_t *T,
                                    const uint16_t *U, int r, const AdPlan &p, uint16_t *out, hipStream_t s) {
-  const int cols = kNN ? K : N;
-  const int tiles = ((M + gemm16::kBM - 1) / gemm16::kBM) * ((cols + gemm16::kBN - 1) / gemm16::kBN);
-  hipLaunchKernelGGL(k_ad_matmul<kNN>, dim3(tiles), dim3(gemm16::kThreads), 0, s, L, Kc, Wd, M, N, K, T, U, r, p, out);
-  return hipGetLastError();
+  if (gemm16::use_mid(M, kNN ? K : N)) return launch_ad_tiles<gemm16::Mid, kNN>(L, Kc, M, N, K, Wd, T, U, r, p, out, s);
+  return launch_ad_tiles<gemm16::Big, kNN>(L, Kc, M, N, K, Wd, T, U, r, p, out, s);
 }
 hipError_t launch_ad_matmul_fwd(const uint16_t *X, int M, int N, int K, const uint16_t *Wd, const uint16_t *T, const uint16_t *B, int r,
                                 const AdPlan &p, uint16_t *Y, hipStream_t s) {

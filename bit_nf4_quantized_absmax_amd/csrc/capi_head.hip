@@ -4,7 +4,6 @@
 #include <algorithm>
 
 #include "capi_util.h"
-#include "gemm16.h"
 
 using namespace qlora;
 
@@ -12,16 +11,11 @@ namespace {
 
 constexpr int64_t kMaxRows = int64_t{1} << 22;
 constexpr int64_t kMaxK = int64_t{1} << 18;
-constexpr int kCUs = 256;
 
 int check_shape(int64_t M, int64_t V, int64_t K) {
   if (M < 0 || V < 1 || K < 1) return QLORA_ERR_INVALID_ARG;
   if (K % 64 != 0 || K > kMaxK || V > kMaxElems || M > kMaxRows || M > kMaxElems / K) return QLORA_ERR_UNSUPPORTED_SHAPE;
   return QLORA_OK;
-}
-
-int64_t tiles(int64_t rows, int64_t cols) {
-  return (rows + gemm16::kBM - 1) / gemm16::kBM * ((cols + gemm16::kBN - 1) / gemm16::kBN);
 }
 
 // Words of a piece: as many as keep `budget` values of it, a multiple of 256 (one
@@ -34,14 +28,7 @@ int64_t piece_words(int64_t M, int64_t V, int64_t K, int64_t budget) {
 
 // E of a piece: 2^26 values, which stay in the 256 MB of memory-side cache between the two products that
 // write and read it.  Without a gradient only the group sums are kept, 8 bytes for 64 words.
-constexpr int64_t kPieceE = int64_t{1} << 26, kPieceSums = int64_t{1} << 28;
-
-// Splits of the second product's words: where the gradient has few tiles,
-// as many as fill the compute units, each at least 8 steps of 64 long.
-int head_splits(int64_t M, int64_t K, int64_t words) {
-  const int64_t s = kCUs / std::max<int64_t>(1, tiles(M, K));
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({s, words / 512, 16})));
-}
+constexpr int64_t kPieceE = int64_t{1} << 27, kPieceSums = int64_t{1} << 28;
 
 struct Parts {
   HeadRows h;
@@ -50,7 +37,7 @@ struct Parts {
   float *C;
   uint16_t *Zt;
   int64_t words;
-  int splits;
+  HeadCut cut;
 };
 
 size_t carve(void *ws, int64_t M, int64_t V, int64_t K, int32_t pass, Parts *p) {
@@ -72,11 +59,10 @@ size_t carve(void *ws, int64_t M, int64_t V, int64_t K, int32_t pass, Parts *p) 
   p->words = piece_words(M, V, K, pass == QLORA_HEAD_DX ? kPieceE : kPieceSums);
   p->pc.rows = static_cast<int>(M);
   p->pc.part = c.take<float2>((p->words + 63) / 64 * M);
-  p->splits = 0;
   if (pass == QLORA_HEAD_DX) {
-    p->splits = head_splits(M, K, p->words);
+    p->cut = head_cut(M, K, p->words);
     p->pc.E = c.take<uint16_t>(p->words * M);
-    p->C = c.take<float>(static_cast<size_t>(p->splits) * M * K);
+    p->C = c.take<float>(static_cast<size_t>(p->cut.most) * M * K);
   }
   return c.used;
 }
@@ -107,14 +93,21 @@ int qlora_head_cross_entropy(const uint16_t *X, int64_t M, const uint16_t *W, in
   if (!ws || !aligned(ws, 16) || ws_bytes < need) return QLORA_ERR_WORKSPACE;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const int m = static_cast<int>(M), k = static_cast<int>(K), v = static_cast<int>(V);
-  hipError_t e = launch_head_rows(target, m, v, p.h, s);
-  if (e == hipSuccess) e = launch_head_gather(X, m, k, p.h, p.Xc, s);
+  const bool small = M <= kHeadSmall;
+  hipError_t e = hipSuccess;
+  if (!small) {
+    e = launch_head_rows(target, m, v, p.h, s);
+    if (e == hipSuccess) e = launch_head_gather(X, m, k, p.h, p.Xc, s);
+  }
   for (int64_t v0 = 0; v0 < V && e == hipSuccess; v0 += p.words) {
     const int words = static_cast<int>(std::min<int64_t>(p.words, V - v0));
     p.pc.pitch = static_cast<int>(round_up(words, 64));
-    e = launch_head_piece(p.Xc, m, W, v, k, static_cast<int>(v0), words, v0 == 0, p.h, p.pc, p.splits, dX ? p.C : nullptr, s);
+    if (small)
+      e = launch_head_small_piece(X, target, m, W, v, k, static_cast<int>(v0), words, v0 == 0, p.h, p.pc, p.cut, dX ? p.C : nullptr, s);
+    else
+      e = launch_head_piece(p.Xc, m, W, v, k, static_cast<int>(v0), words, v0 == 0, p.h, p.pc, p.cut, dX ? p.C : nullptr, s);
   }
-  if (e == hipSuccess) e = launch_head_finish(W, M, k, weight, p.h, p.splits, p.C, loss, lse, dX, dX ? 1 + dx_fp32 : 0, s);
+  if (e == hipSuccess) e = launch_head_finish(W, M, k, weight, p.h, p.cut, p.C, loss, lse, dX, dX ? 1 + dx_fp32 : 0, s);
   return from_hip(e);
 }
 

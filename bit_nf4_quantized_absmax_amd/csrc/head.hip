@@ -8,12 +8,12 @@
 // to the gradient in fp32 (k_head_acc): two products in all for loss and dX, as
 // the sum over the rows of W weighted by e^z needs no division before its end.
 //
-//  * ref is a multiple of 32 near the largest logit of a row's 64 words (within
-//    16 of it), so that almost always the words of a row, and its pieces, have the same: e^16
-//    and what lies 71 below the largest fit into fp32 and bf16 alike, whose
-//    relative precision does not depend on the scale.  Where they differ, the sums (k_head_refs)
-//    and E (there too) are brought to the largest, and the gradient so far by
-//    the next product's epilogue.
+//  * ref is the multiple of 64 ln 2 nearest to the largest logit of a row's 64
+//    words, so that hardly ever two groups of words of a row differ in it: e^22, and
+//    what lies 65 below the largest, fit into fp32 and bf16 alike, whose relative
+//    precision does not depend on the scale.  Where they differ, the sums and E are
+//    brought to the largest (k_head_refs; E by a power of 2^64, which rounds
+//    nothing a second time), and the gradient so far by the next product's epilogue.
 //  * The target's own term is left out of E and of the sums, and joins them in 64
 //    bits at the end (k_head_finish): the loss is log(1 + sum / e^(z_t - ref)), and
 //    (p_t - 1) W_t is added in fp32, where a rounded p_t near 1 would lose both.  E's rounding to bf16 is
@@ -34,15 +34,49 @@ namespace qlora {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kBucket = 32.f;
+constexpr float kBucket = 44.361419555836498f;   // 64 ln 2
+constexpr float kWide = 0x1p20f;                 // above it a multiple of kBucket has no bits left to be near anything
 
-// e^x through the hardware's 2^x (x <= 16 here; what underflows is 0).
+// e^x through the hardware's 2^x (x <= 23 here; what underflows is 0).
 __device__ __forceinline__ float exp_f(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
 
 // The reference of words whose largest logit is top; 0 where that is no number.
 __device__ __forceinline__ float ref_of(float top) {
-  const float r = kBucket * rintf(top * (1.f / kBucket));
-  return fabsf(top) <= 3.0e38f ? r : 0.f;
+  if (!(fabsf(top) <= 3.0e38f)) return 0.f;
+  return fabsf(top) < kWide ? kBucket * rintf(top * (1.f / kBucket)) : top;
+}
+
+// e^(from - to) for values that are rounded to bf16 already: between two multiples of kBucket (as fp32 holds them) a power of 2^64.
+__device__ __forceinline__ float shift_of(float from, float to) {
+  if (fabsf(from) < kWide && fabsf(to) < kWide) return __builtin_amdgcn_exp2f(64.f * rintf((from - to) * (1.f / kBucket)));
+  return exp_f(from - to);
+}
+
+// Splits of the second product's words: the fewest that come within 2 % of the
+// least time, in rounds of the workgroups that the chip holds at once.
+// The number of rows that count is known on the device alone.  slots 0: all of them.
+__host__ __device__ __forceinline__ int splits_for(int tiles, const HeadCut &cut) {
+  if (cut.slots == 0) return cut.most;
+  int best = 1;
+  float least = 3.4e38f;
+  for (int s = 1; s <= cut.most; ++s) {
+    const float t = static_cast<float>((tiles * s + cut.slots - 1) / cut.slots) / s;
+    if (t < 0.98f * least) {
+      least = t;
+      best = s;
+    }
+  }
+  return best;
+}
+
+// *at = v, or f *at + v.
+__device__ __forceinline__ void add_to(f32x4_t *at, f32x4_t v, int first, float f) {
+  if (!first) {
+    const f32x4_t o = *at;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] += f * o[e];
+  }
+  *at = v;
 }
 
 __device__ __forceinline__ float swap_halves(float v) { return __shfl_xor(v, 32, 64); }
@@ -98,25 +132,25 @@ __global__ __launch_bounds__(256) void k_head_gather(const uint16_t *__restrict_
 // (ref, sum of e^(z - ref)) without the target, the target's logit where it is
 // among them, and with kE the matrix E [row][pitch], pitch = words filled up to 64,
 // zero there and at the target.
-template <bool kE>
-__global__ __launch_bounds__(gemm16::kThreads) void k_head_logits(const uint16_t *__restrict__ Xc, const uint16_t *__restrict__ W, int K,
+template <class S, bool kE>
+__global__ __launch_bounds__(S::kThreads, 2) void k_head_logits(const uint16_t *__restrict__ Xc, const uint16_t *__restrict__ W, int K,
                                                                   int v0, int words, HeadRows h, HeadPiece pc) {
   using namespace gemm16;
-  __shared__ __attribute__((aligned(16))) uint8_t smem[kLds];
+  __shared__ __attribute__((aligned(16))) uint8_t smem[S::kLds];
   const int count = h.count[0];
   int tr, tc;
-  if (!place(blockIdx.x, (count + kBM - 1) / kBM, (words + kBN - 1) / kBN, tr, tc)) return;
-  const int m0 = tr * kBM, c0 = tc * kBN;
-  f32x16_t acc[4][2];
-  tile<false>(smem, Xc, K, [&](int row) { return min(m0 + row, count - 1); }, W + static_cast<int64_t>(v0) * K, K, c0, words - 1, 0,
+  if (!place(blockIdx.x, (count + S::kBM - 1) / S::kBM, (words + S::kBN - 1) / S::kBN, tr, tc)) return;
+  const int m0 = tr * S::kBM, c0 = tc * S::kBN;
+  Acc<S> acc;
+  tile<S, false>(smem, Xc, K, [&](int row) { return min(m0 + row, count - 1); }, W + static_cast<int64_t>(v0) * K, K, c0, words - 1, 0,
               K / kBK, acc);
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave >> 2, wn = wave & 3, lr = lane & 31, lh = lane >> 5;
-  const int cw = c0 + 64 * wn;                       // first word (of the piece) of this wave
+  const Place<S> w;
+  const int lr = w.lr, lh = w.lh;
+  const int cw = c0 + w.col0();                       // first word (of the piece) of this wave
   const bool edge = cw + 64 > words;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = m0 + 128 * wm + 32 * i + lr;
+  for (int i = 0; i < S::kFM; ++i) {
+    const int row = m0 + w.row0() + 32 * i + lr;
     const bool live = row < count;
     const int rel = live ? h.tgt[row] - v0 - cw - 4 * lh : -1;   // of this half's words: 0 .. 3, 8 .. 11, ...
     if (edge) {
@@ -126,6 +160,19 @@ __global__ __launch_bounds__(gemm16::kThreads) void k_head_logits(const uint16_t
         for (int e = 0; e < 16; ++e)
           if (cw + 32 * j + 8 * (e >> 2) + 4 * lh + (e & 3) >= words) acc[i][j][e] = -INFINITY;
     }
+    const bool hit = rel >= 0 && rel < 64 && (rel & 4) == 0;
+    if (__ballot(hit) != 0) {                          // the target: kept, and out of the words
+      float zt = 0.f;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (rel == 32 * j + 8 * (e >> 2) + (e & 3)) {
+            zt = acc[i][j][e];
+            acc[i][j][e] = -INFINITY;
+          }
+      if (hit) h.zt[row] = zt;
+    }
     float top = acc[i][0][0];
 #pragma unroll
     for (int j = 0; j < 2; ++j)
@@ -134,16 +181,6 @@ __global__ __launch_bounds__(gemm16::kThreads) void k_head_logits(const uint16_t
     top = fmaxf(top, swap_halves(top));
     const float ref = ref_of(top);
     float sum = 0.f;
-    const bool hit = rel >= 0 && rel < 64 && (rel & 4) == 0;
-    const bool any = __ballot(hit) != 0;
-    float zt = 0.f;
-    if (any) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (rel == 32 * j + 8 * (e >> 2) + (e & 3)) zt = acc[i][j][e];
-    }
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -152,22 +189,11 @@ __global__ __launch_bounds__(gemm16::kThreads) void k_head_logits(const uint16_t
         sum += x;
         acc[i][j][e] = x;
       }
-    if (any) {                                       // again without the target
-      sum = 0.f;
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          if (rel == 32 * j + 8 * (e >> 2) + (e & 3)) acc[i][j][e] = 0.f;
-          sum += acc[i][j][e];
-        }
-    }
     sum += swap_halves(sum);
-    if (live && hit) h.zt[row] = zt;
     if (live && lh == 0 && cw < words) pc.part[static_cast<int64_t>(cw >> 6) * pc.rows + row] = make_float2(ref, sum);
   }
   if constexpr (kE)
-    store_bf16(acc, smem, [&](int row, int col, uint4 v) {
+    store_bf16<S>(acc, smem, [&](int row, int col, uint4 v) {
       if (m0 + row < count && c0 + col < pc.pitch)
         *reinterpret_cast<uint4 *>(pc.E + static_cast<int64_t>(m0 + row) * pc.pitch + c0 + col) = v;
     });
@@ -175,113 +201,406 @@ __global__ __launch_bounds__(gemm16::kThreads) void k_head_logits(const uint16_t
 
 // ---------------------------------------------------------------------------
 // A row's sum with this piece's groups, at the largest of their references and
-// its own so far: state [row] = (ref, sum), factor [row] = e^(old ref - ref) for
-// the gradient so far (0 at the first piece).  Groups of E at a smaller reference are
-// brought to this one.  Workgroup: 64 rows, 4 waves share the groups.
+// its own so far: ref and sum [row], factor [row] = e^(old ref - ref) for the
+// gradient so far (0 at the first piece).  Groups of E at a smaller reference are
+// brought to this one, in a second pass that hardly any row needs.  Workgroup:
+// kRows rows, 256 / kRows threads share a row's groups.
+template <int kRows>
 __global__ __launch_bounds__(256) void k_head_refs(HeadRows h, HeadPiece pc, int groups, int first, int scale_e) {
-  __shared__ float top[4][64];
-  __shared__ double sums[4][64];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int row = blockIdx.x * 64 + lane, count = h.count[0];
+  constexpr int kShare = 256 / kRows;
+  __shared__ float sRef[4][kRows], sLow[4][kRows];
+  __shared__ double sSum[4][kRows];
+  const int lrow = threadIdx.x % kRows, w = threadIdx.x / kRows;
+  const int row = blockIdx.x * kRows + lrow, count = h.count[0];
+  if (static_cast<int>(blockIdx.x) * kRows >= count) return;
   const bool live = row < count;
-  const float2 *part = pc.part + row;
-  float ref = -3.4e38f;
-  if (live)
-    for (int g = w; g < groups; g += 4) {
-      const float2 v = part[static_cast<int64_t>(g) * pc.rows];
-      if (v.y != 0.f) ref = fmaxf(ref, v.x);
-    }
-  top[w][lane] = ref;
-  __syncthreads();
-  ref = fmaxf(fmaxf(top[0][lane], top[1][lane]), fmaxf(top[2][lane], top[3][lane]));
-  float old_ref = -3.4e38f;
-  double old = 0.0;
-  if (live && !first) {
-    old_ref = h.ref[row];
-    old = h.sum[row];
-  }
-  ref = fmaxf(ref, old_ref);
+  const float2 *part = pc.part + (live ? row : 0);
+  const int64_t pitch = pc.rows;
+  float ref = -3.4e38f, low = 3.4e38f;
   double sum = 0.0;
-  if (live)
-    for (int g = w; g < groups; g += 4) {
-      const float2 v = part[static_cast<int64_t>(g) * pc.rows];
-      if (v.y == 0.f) continue;
-      const float f = v.x == ref ? 1.f : exp_f(v.x - ref);
-      sum += static_cast<double>(v.y) * f;
-      if (scale_e && f != 1.f) {
-        uint16_t *e = pc.E + static_cast<int64_t>(row) * pc.pitch + 64 * g;
-        for (int c = 0; c < 64; c += 2) {
-          const uint32_t u = *reinterpret_cast<uint32_t *>(e + c);
-          *reinterpret_cast<uint32_t *>(e + c) = pack_bf16x2(u2f(u << 16) * f, u2f(u & 0xffff0000u) * f);
-        }
+  constexpr int kBatch = 8;
+  for (int g0 = w; g0 < groups; g0 += kShare * kBatch) {
+    float2 v[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) v[u] = part[pitch * min(g0 + kShare * u, groups - 1)];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (g0 + kShare * u >= groups || v[u].y == 0.f) continue;
+      low = fminf(low, v[u].x);
+      if (v[u].x > ref) {
+        sum *= exp_f(ref - v[u].x);
+        ref = v[u].x;
+      }
+      sum += static_cast<double>(v[u].y) * (v[u].x == ref ? 1.f : exp_f(v[u].x - ref));
+    }
+  }
+  // The shares of a row are lanes of a wave kRows apart, then waves: joined in a fixed order.
+  auto join = [&](float r2, double s2) {
+    if (s2 == 0.0) return;
+    if (sum == 0.0) {
+      ref = r2;
+      sum = s2;
+    } else if (r2 > ref) {
+      sum = sum * exp_f(ref - r2) + s2;
+      ref = r2;
+    } else {
+      sum += r2 == ref ? s2 : s2 * exp_f(r2 - ref);
+    }
+  };
+#pragma unroll
+  for (int o = kRows; o < 64; o <<= 1) {
+    const float r2 = __shfl_xor(ref, o, 64);
+    const double s2 = __shfl_xor(sum, o, 64);
+    const float l2 = __shfl_xor(low, o, 64);
+    const bool lower = (threadIdx.x & o) == 0;         // the same order in both lanes
+    if (lower) {
+      join(r2, s2);
+    } else {
+      const float r1 = ref;
+      const double s1 = sum;
+      ref = r2;
+      sum = s2;
+      join(r1, s1);
+    }
+    low = fminf(low, l2);
+  }
+  if ((threadIdx.x & 63) < kRows) {
+    sRef[threadIdx.x >> 6][lrow] = ref;
+    sLow[threadIdx.x >> 6][lrow] = low;
+    sSum[threadIdx.x >> 6][lrow] = sum;
+  }
+  __syncthreads();
+  ref = sRef[0][lrow];
+  sum = sSum[0][lrow];
+  low = sLow[0][lrow];
+#pragma unroll
+  for (int i = 1; i < 4; ++i) {
+    join(sRef[i][lrow], sSum[i][lrow]);
+    low = fminf(low, sLow[i][lrow]);
+  }
+  const float new_ref = ref;                         // of this piece
+  const float old_ref = live && !first ? h.ref[row] : -3.4e38f;
+  const double old = live && !first ? h.sum[row] : 0.0;
+  const float top = old == 0.0 ? new_ref : fmaxf(new_ref, old_ref);
+  if (live && scale_e && low < top)
+    for (int g = w; g < groups; g += kShare) {
+      const float2 v = part[pitch * g];
+      if (v.y == 0.f || v.x == top) continue;
+      const float f = shift_of(v.x, top);
+      uint4 *e = reinterpret_cast<uint4 *>(pc.E + static_cast<int64_t>(row) * pc.pitch + 64 * g);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const uint4 u = e[c];
+        const uint32_t uu[4] = {u.x, u.y, u.z, u.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) o[q] = pack_bf16x2(u2f(uu[q] << 16) * f, u2f(uu[q] & 0xffff0000u) * f);
+        e[c] = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
-  sums[w][lane] = sum;
-  __syncthreads();
+  __syncthreads();                                   // all threads of the row have read its state
   if (w == 0 && live) {
-    const float f = old_ref == ref ? 1.f : (old == 0.0 ? 0.f : exp_f(old_ref - ref));
-    h.ref[row] = ref;
-    h.sum[row] = old * f + (sums[0][lane] + sums[1][lane]) + (sums[2][lane] + sums[3][lane]);
-    h.factor[row] = first ? 0.f : f;
+    const float f = old == 0.0 ? 0.f : old_ref == top ? 1.f : exp_f(old_ref - top);
+    h.ref[row] = top;
+    h.sum[row] = old * f + (sum == 0.0 || new_ref == top ? sum : sum * exp_f(new_ref - top));
+    h.factor[row] = f;
   }
 }
 
 // ---------------------------------------------------------------------------
 // C [split][row][K] (fp32) = factor C + sum over the split's words of E W.
-__global__ __launch_bounds__(gemm16::kThreads) void k_head_acc(const uint16_t *__restrict__ W, int V, int K, int v0, int splits, int first,
+template <class S>
+__global__ __launch_bounds__(S::kThreads, 2) void k_head_acc(const uint16_t *__restrict__ W, int V, int K, int v0, HeadCut cut, int first,
                                                                HeadRows h, HeadPiece pc, float *__restrict__ C) {
   using namespace gemm16;
-  __shared__ __attribute__((aligned(16))) uint8_t smem[kLds];
+  __shared__ __attribute__((aligned(16))) uint8_t smem[S::kLds];
   const int count = h.count[0];
-  const int trows = (count + kBM - 1) / kBM, tcols = (K + kBN - 1) / kBN;
-  // splits of one tile are apart by a multiple of the tiles, so that an XCD's tiles share a split's words
-  int tr, tc;
+  const int trows = (count + S::kBM - 1) / S::kBM, tcols = (K + S::kBN - 1) / S::kBN;
   const int tiles = trows * tcols;
   if (tiles == 0) return;
-  const int split = blockIdx.x / tiles;
-  if (split >= splits || !place(blockIdx.x - split * tiles, trows, tcols, tr, tc)) return;
+  const int splits = splits_for(tiles, cut);
   const int KT = pc.pitch / kBK;
+  // A split after the other, so that the tiles at work share its words.
+  const int split = blockIdx.x / tiles;
+  int tr, tc;
+  if (split >= splits || !place(blockIdx.x - split * tiles, trows, tcols, tr, tc)) return;
   const int k0 = static_cast<int>(static_cast<int64_t>(KT) * split / splits);
   const int k1 = static_cast<int>(static_cast<int64_t>(KT) * (split + 1) / splits);
-  const int m0 = tr * kBM, c0 = tc * kBN;
-  f32x16_t acc[4][2];
+  const int m0 = tr * S::kBM, c0 = tc * S::kBN;
+  Acc<S> acc;
   if (k1 > k0)
-    tile<true>(smem, pc.E + static_cast<int64_t>(kBK) * k0, pc.pitch, [&](int row) { return min(m0 + row, count - 1); },
-               W + (static_cast<int64_t>(v0) + kBK * k0) * K, K, c0, K - 1, V - 1 - v0 - kBK * k0, k1 - k0, acc);
+    tile<S, true>(smem, pc.E + static_cast<int64_t>(kBK) * k0, pc.pitch, [&](int row) { return min(m0 + row, count - 1); },
+                  W + (static_cast<int64_t>(v0) + kBK * k0) * K, K, c0, K - 1, V - 1 - v0 - kBK * k0, k1 - k0, acc);
   else
-    clear(acc);
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave >> 2, wn = wave & 3, lr = lane & 31, lh = lane >> 5;
+    clear<S>(acc);
+  const Place<S> w;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = m0 + 128 * wm + 32 * i + lr;
+  for (int i = 0; i < S::kFM; ++i) {
+    const int row = m0 + w.row0() + 32 * i + w.lr;
     if (row >= count) continue;
     const float f = first ? 0.f : h.factor[row];
     float *c = C + (static_cast<int64_t>(split) * pc.rows + row) * K;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < S::kFN; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int k = c0 + 64 * wn + 32 * j + 8 * q + 4 * lh;
-        if (k >= K) continue;
-        f32x4_t v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-        f32x4_t *at = reinterpret_cast<f32x4_t *>(c + k);
-        if (!first) {
-          const f32x4_t o = *at;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] += f * o[e];
-        }
-        *at = v;
+        const int k = c0 + w.col0() + 32 * j + 8 * q + 4 * w.lh;
+        if (k < K)
+          add_to(reinterpret_cast<f32x4_t *>(c + k), f32x4_t{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]},
+                 first, f);
       }
   }
 }
 
 // ---------------------------------------------------------------------------
-// One workgroup a row of X: its loss and (ref, log sum); with kGrad 1 (bf16) or 2
+// Up to kHeadSmall rows: bound by reading W, once for the logits and once more for the
+// gradient, so both kernels keep three steps of it in flight in a ring of four
+// stages, and the few rows of X or E go along from L2.
+namespace {
+constexpr int kSmThreads = 256;
+constexpr int kSmRing = 4;
+constexpr int kSmWords = 64;      // words of a workgroup (k_head_small)
+constexpr int kSmCols = 128;      // columns of a workgroup (k_head_small_acc)
+
+template <int kMB>
+constexpr int sm_row_dma() { return (2 * kMB + 3) / 4; }   // DMA instructions a wave and stage for 16 kMB rows of 128 bytes
+
+// One stage's rows of X or E (row r of the list at off(r), 128 bytes from `col` on); surplus
+// instructions repeat the last 8 rows.
+template <int kMB, class Off>
+__device__ __forceinline__ void sm_rows(uint32_t dst, const void *base, int wave, int lane, Off off) {
+#pragma unroll
+  for (int j = 0; j < sm_row_dma<kMB>(); ++j) {
+    const int u = min(wave * sm_row_dma<kMB>() + j, 2 * kMB - 1);
+    const int row = 8 * u + (lane >> 3);
+    dma16(base, off(j) + 16 * ((lane & 7) ^ ((row & 7) ^ ((row >> 3) & 1))), __builtin_amdgcn_readfirstlane(dst + 1024 * u));
+  }
+}
+
+// Waits until a step has landed while `ahead` later ones (at most 2) of kDma instructions each may be in flight.
+template <int kDma>
+__device__ __forceinline__ void sm_step_barrier(int ahead) {
+  if (ahead >= 2)
+    raw_barrier<wait_imm(2 * kDma, 0)>();
+  else if (ahead == 1)
+    raw_barrier<wait_imm(kDma, 0)>();
+  else
+    raw_barrier<wait_imm(0, 0)>();
+}
+}  // namespace
+
+// k_head_rows and k_head_logits for M <= 16 kMB rows: 64 words a workgroup, 16 a
+// wave, on 16 x 16 tiles (lane: row l % 16, words 4 (l / 16) + e).
+template <int kMB, bool kE>
+__global__ __launch_bounds__(kSmThreads) void k_head_small(const uint16_t *__restrict__ X, const int64_t *__restrict__ target, int M,
+                                                           const uint16_t *__restrict__ W, int V, int K, int v0, int words, HeadRows h,
+                                                           HeadPiece pc) {
+  constexpr int kStage = kSmWords * 128 + kMB * 2048;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[kSmRing * kStage];
+  __shared__ int sRow[64], sTgt[64];
+  __shared__ float sTop[4][16 * kMB], sSum[4][16 * kMB];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t t = lane < M ? target[lane] : -1;
+  const bool real = t >= 0 && t < V;
+  const uint64_t mask = __ballot(real);
+  const int count = __popcll(mask), rank = __popcll(mask & ((uint64_t{1} << lane) - 1));
+  if (wave == 0) {
+    if (real) {
+      sRow[rank] = lane;
+      sTgt[rank] = static_cast<int>(t);
+    }
+    if (blockIdx.x == 0) {
+      if (real) {
+        h.list[rank] = lane;
+        h.tgt[rank] = static_cast<int>(t);
+      }
+      if (lane < M) h.place[lane] = real ? rank : -1;
+      if (lane == 0) h.count[0] = count;
+    }
+  }
+  if (count == 0) return;
+  __syncthreads();
+  const int w0 = blockIdx.x * kSmWords;             // of the piece
+  const uint16_t *Wp = W + static_cast<int64_t>(v0 + w0) * K;
+  uint32_t wo[2], xo[sm_row_dma<kMB>()];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int row = 8 * (2 * wave + j) + (lane >> 3);
+    wo[j] = static_cast<uint32_t>(min(row, words - 1 - w0)) * K * 2 + 16 * ((lane & 7) ^ ((row & 7) ^ ((row >> 3) & 1)));
+  }
+#pragma unroll
+  for (int j = 0; j < sm_row_dma<kMB>(); ++j) {
+    const int u = min(wave * sm_row_dma<kMB>() + j, 2 * kMB - 1);
+    xo[j] = static_cast<uint32_t>(sRow[min(8 * u + (lane >> 3), count - 1)]) * K * 2;
+  }
+  const uint32_t lds0 = lds_addr(smem);
+  auto issue = [&](int kt) __attribute__((always_inline)) {
+    const uint32_t dst = lds0 + (kt & (kSmRing - 1)) * kStage;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) dma16(Wp + 64 * kt, wo[j], __builtin_amdgcn_readfirstlane(dst + (2 * wave + j) * 1024));
+    sm_rows<kMB>(dst + kSmWords * 128, X + 64 * kt, wave, lane, [&](int j) { return xo[j]; });
+  };
+  constexpr int kDma = 2 + sm_row_dma<kMB>();
+  const int KT = K / 64;
+  f32x4_t acc[kMB];
+#pragma unroll
+  for (int mb = 0; mb < kMB; ++mb) acc[mb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int kt = 0; kt < min(3, KT); ++kt) issue(kt);
+  const int lr = lane & 15, lg = lane >> 4;
+  for (int kt = 0; kt < KT; ++kt) {
+    sm_step_barrier<kDma>(KT - 1 - kt);
+    if (kt + 3 < KT) issue(kt + 3);
+    const uint8_t *ws = smem + (kt & (kSmRing - 1)) * kStage, *xs = ws + kSmWords * 128;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const bf16x8_t a = *reinterpret_cast<const bf16x8_t *>(ws + swz128(16 * wave + lr, 4 * s + lg));
+#pragma unroll
+      for (int mb = 0; mb < kMB; ++mb)
+        acc[mb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, *reinterpret_cast<const bf16x8_t *>(xs + swz128(16 * mb + lr, 4 * s + lg)),
+                                                          acc[mb], 0, 0, 0);
+    }
+  }
+  const int first_word = w0 + 16 * wave + 4 * lg;    // of this lane, in the piece
+#pragma unroll
+  for (int mb = 0; mb < kMB; ++mb) {
+    const int row = 16 * mb + lr;
+    const int rel = row < count ? sTgt[row] - v0 - first_word : -1;
+    float top = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (rel == e) h.zt[row] = acc[mb][e];
+      if (rel == e || first_word + e >= words) acc[mb][e] = -INFINITY;
+      top = fmaxf(top, acc[mb][e]);
+    }
+    top = fmaxf(top, __shfl_xor(top, 16, 64));
+    top = fmaxf(top, __shfl_xor(top, 32, 64));
+    if (lg == 0) sTop[wave][row] = top;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int mb = 0; mb < kMB; ++mb) {
+    const int row = 16 * mb + lr;
+    const float ref = ref_of(fmaxf(fmaxf(sTop[0][row], sTop[1][row]), fmaxf(sTop[2][row], sTop[3][row])));
+    float sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      acc[mb][e] = exp_f(acc[mb][e] - ref);
+      sum += acc[mb][e];
+    }
+    sum += __shfl_xor(sum, 16, 64);
+    sum += __shfl_xor(sum, 32, 64);
+    if (lg == 0) sSum[wave][row] = sum;
+    if constexpr (kE)
+      if (row < count)
+        *reinterpret_cast<uint2 *>(pc.E + static_cast<int64_t>(row) * pc.pitch + first_word) =
+            make_uint2(pack_bf16x2(acc[mb][0], acc[mb][1]), pack_bf16x2(acc[mb][2], acc[mb][3]));
+  }
+  __syncthreads();
+  if (static_cast<int>(threadIdx.x) < count) {
+    const int row = threadIdx.x;
+    const float ref = ref_of(fmaxf(fmaxf(sTop[0][row], sTop[1][row]), fmaxf(sTop[2][row], sTop[3][row])));
+    pc.part[static_cast<int64_t>(blockIdx.x) * pc.rows + row] = make_float2(ref, (sSum[0][row] + sSum[1][row]) + (sSum[2][row] + sSum[3][row]));
+  }
+}
+
+// k_head_acc for M <= 16 kMB rows: 128 columns a workgroup, 32 a wave, over one of
+// cut.most parts of the piece's words.
+template <int kMB>
+__global__ __launch_bounds__(kSmThreads) void k_head_small_acc(const uint16_t *__restrict__ W, int V, int K, int v0, HeadCut cut, int first,
+                                                               HeadRows h, HeadPiece pc, float *__restrict__ C) {
+  constexpr int kStage = 64 * 2 * kSmCols + kMB * 2048;
+  __shared__ __attribute__((aligned(16))) uint8_t smem[kSmRing * kStage];
+  const int count = h.count[0];
+  if (count == 0) return;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int cols = (K + kSmCols - 1) / kSmCols;
+  const int split = blockIdx.x / cols, c0 = blockIdx.x % cols * kSmCols;
+  const int KT = pc.pitch / 64;
+  const int k0 = static_cast<int>(static_cast<int64_t>(KT) * split / cut.most);
+  const int n = static_cast<int>(static_cast<int64_t>(KT) * (split + 1) / cut.most) - k0;
+  const uint16_t *Wp = W + (static_cast<int64_t>(v0) + 64 * k0) * K;
+  const uint16_t *Ep = pc.E + 64 * k0;
+  const int last = V - 1 - v0 - 64 * k0;             // rows of W past it are repeated: E is zero there
+  // rows of 256 bytes, four a DMA instruction
+  auto wrow = [&](int j) { return 4 * (4 * wave + j) + (lane >> 4); };
+  uint32_t wo[4], eo[sm_row_dma<kMB>()];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int row = wrow(j);
+    const int chunk = (lane & 15) ^ (((row & 3) << 2) | ((row >> 2) & 3));
+    wo[j] = 2 * static_cast<uint32_t>(min(c0 + 8 * chunk, K - 8));
+  }
+#pragma unroll
+  for (int j = 0; j < sm_row_dma<kMB>(); ++j) {
+    const int u = min(wave * sm_row_dma<kMB>() + j, 2 * kMB - 1);
+    eo[j] = static_cast<uint32_t>(min(8 * u + (lane >> 3), count - 1)) * pc.pitch * 2;
+  }
+  const uint32_t lds0 = lds_addr(smem);
+  auto issue = [&](int kt) __attribute__((always_inline)) {
+    const uint32_t dst = lds0 + (kt & (kSmRing - 1)) * kStage;
+    const uint16_t *base = Wp + static_cast<int64_t>(64) * kt * K;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      dma16(base, static_cast<uint32_t>(min(wrow(j), last - 64 * kt)) * K * 2 + wo[j],
+            __builtin_amdgcn_readfirstlane(dst + (4 * wave + j) * 1024));
+    sm_rows<kMB>(dst + 64 * 2 * kSmCols, Ep + 64 * kt, wave, lane, [&](int j) { return eo[j]; });
+  };
+  constexpr int kDma = 4 + sm_row_dma<kMB>();
+  f32x4_t acc[2][kMB];
+#pragma unroll
+  for (int b = 0; b < 2; ++b)
+#pragma unroll
+    for (int mb = 0; mb < kMB; ++mb) acc[b][mb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  const int lr = lane & 15, lg = lane >> 4;
+  uint32_t to[2][2];                                 // transposed reads: columns 32 wave + 16 b + l % 16, words 8 lg + 4 h .. +3
+#pragma unroll
+  for (int b = 0; b < 2; ++b)
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh)
+      to[b][hh] = static_cast<uint32_t>(
+          gemm16::swz_wide<gemm16::Mid>(8 * lg + 4 * hh + (lr >> 2), 4 * wave + 2 * b + ((lr & 3) >> 1)) + 8 * (lr & 1));
+  static_assert(gemm16::Mid::kBN == kSmCols, "rows of 256 bytes");
+  for (int kt = 0; kt < min(3, n); ++kt) issue(kt);
+  for (int kt = 0; kt < n; ++kt) {
+    sm_step_barrier<kDma>(n - 1 - kt);
+    if (kt + 3 < n) issue(kt + 3);
+    const uint8_t *ws = smem + (kt & (kSmRing - 1)) * kStage, *es = ws + 64 * 2 * kSmCols;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      bf16x8_t x[kMB];
+#pragma unroll
+      for (int mb = 0; mb < kMB; ++mb) x[mb] = *reinterpret_cast<const bf16x8_t *>(es + swz128(16 * mb + lr, 4 * s + lg));
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const gemm16::bf16x4_t lo = gemm16::ds_tr16(ws + to[b][0] + 64 * kSmCols * s);
+        const gemm16::bf16x4_t hi = gemm16::ds_tr16(ws + to[b][1] + 64 * kSmCols * s);
+        const bf16x8_t a = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+#pragma unroll
+        for (int mb = 0; mb < kMB; ++mb) acc[b][mb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, x[mb], acc[b][mb], 0, 0, 0);
+      }
+    }
+  }
+#pragma unroll
+  for (int mb = 0; mb < kMB; ++mb) {
+    const int row = 16 * mb + lr;
+    if (row >= count) continue;
+    const float f = first ? 0.f : h.factor[row];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int k = c0 + 32 * wave + 16 * b + 4 * lg;
+      if (k < K) add_to(reinterpret_cast<f32x4_t *>(C + (static_cast<int64_t>(split) * pc.rows + row) * K + k), acc[b][mb], first, f);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// A workgroup a row of X and 2048 columns: its loss and (ref, log sum); with kGrad 1 (bf16) or 2
 // (fp32) its gradient, weight (C / sum + (p_t - 1) W_t).
 template <int kGrad>
 __global__ __launch_bounds__(256) void k_head_finish(const uint16_t *__restrict__ W, int K, const float *__restrict__ weight, HeadRows h,
-                                                     int rows, int splits, const float *__restrict__ C, float *__restrict__ loss,
+                                                     int rows, HeadCut cut, const float *__restrict__ C, float *__restrict__ loss,
                                                      float *__restrict__ lse, void *__restrict__ dX) {
   const int64_t m = blockIdx.x;
   const int at = h.place[m];
@@ -297,7 +616,7 @@ __global__ __launch_bounds__(256) void k_head_finish(const uint16_t *__restrict_
     lg = static_cast<float>(loss64 + (zt - ref));
     l = static_cast<float>(loss64);
   }
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 0 && blockIdx.y == 0) {
     loss[m] = l;
     lse[2 * m] = ref;
     lse[2 * m + 1] = lg;
@@ -305,18 +624,28 @@ __global__ __launch_bounds__(256) void k_head_finish(const uint16_t *__restrict_
   if constexpr (kGrad != 0) {
     const float g = at < 0 ? 0.f : (weight ? weight[m] : 1.f);
     const float pt = expm1f(-l);                     // p_t - 1
+    const int splits = splits_for((h.count[0] + cut.bm - 1) / cut.bm * ((K + cut.bn - 1) / cut.bn), cut);
     const uint16_t *wt = W + static_cast<int64_t>(at < 0 ? 0 : h.tgt[at]) * K;
-    for (int k = 8 * threadIdx.x; k < K; k += 8 * 256) {
+    const int k = 8 * (blockIdx.y * 256 + threadIdx.x);
+    if (k < K) {
       float v[8] = {};
       if (at >= 0) {
-        for (int s = 0; s < splits; ++s) {
-          const f32x4_t *c = reinterpret_cast<const f32x4_t *>(C + (static_cast<int64_t>(s) * rows + at) * K + k);
-          const f32x4_t c0 = c[0], c1 = c[1];
+        for (int s0 = 0; s0 < splits; s0 += 8) {       // 8 splits' loads at once, added in order
+          f32x4_t c[8][2];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            v[e] += c0[e];
-            v[4 + e] += c1[e];
+          for (int u = 0; u < 8; ++u) {
+            const f32x4_t *p = reinterpret_cast<const f32x4_t *>(C + (static_cast<int64_t>(min(s0 + u, splits - 1)) * rows + at) * K + k);
+            c[u][0] = p[0];
+            c[u][1] = p[1];
           }
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            if (s0 + u < splits)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                v[e] += c[u][0][e];
+                v[4 + e] += c[u][1][e];
+              }
         }
         const uint4 wv = *reinterpret_cast<const uint4 *>(wt + k);
         const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w};
@@ -358,18 +687,19 @@ __global__ __launch_bounds__(256) void k_head_scale(const float *__restrict__ D,
 // ---------------------------------------------------------------------------
 // dz^T [word][pitch] of words v0 .. v0 + words - 1 and the listed rows, in bf16;
 // zeros in the columns count .. (count filled up to 64) - 1.
-__global__ __launch_bounds__(gemm16::kThreads) void k_head_dz(const uint16_t *__restrict__ Xc, const uint16_t *__restrict__ W, int K, int v0,
+template <class S>
+__global__ __launch_bounds__(S::kThreads, 2) void k_head_dz(const uint16_t *__restrict__ Xc, const uint16_t *__restrict__ W, int K, int v0,
                                                               int words, HeadRows h, const float *__restrict__ lse,
                                                               const float *__restrict__ weight, int64_t pitch, uint16_t *__restrict__ Zt) {
   using namespace gemm16;
-  __shared__ __attribute__((aligned(16))) uint8_t smem[kLds];
-  __shared__ float sRef[kBN], sRest[kBN], sG[kBN];
-  __shared__ int sT[kBN];
+  __shared__ __attribute__((aligned(16))) uint8_t smem[S::kLds];
+  __shared__ float sRef[S::kBN], sRest[S::kBN], sG[S::kBN];
+  __shared__ int sT[S::kBN];
   const int count = h.count[0];
   int tr, tc;
-  if (!place(blockIdx.x, (words + kBM - 1) / kBM, (count + kBN - 1) / kBN, tr, tc)) return;
-  const int w0 = tr * kBM, c0 = tc * kBN;
-  if (threadIdx.x < kBN) {
+  if (!place(blockIdx.x, (words + S::kBM - 1) / S::kBM, (count + S::kBN - 1) / S::kBN, tr, tc)) return;
+  const int w0 = tr * S::kBM, c0 = tc * S::kBN;
+  if (threadIdx.x < S::kBN) {
     const int at = c0 + threadIdx.x;
     const bool live = at < count;
     const int64_t m = live ? h.list[at] : 0;
@@ -378,57 +708,83 @@ __global__ __launch_bounds__(gemm16::kThreads) void k_head_dz(const uint16_t *__
     sG[threadIdx.x] = live ? (weight ? weight[m] : 1.f) : 0.f;
     sT[threadIdx.x] = live ? h.tgt[at] - v0 : -1;
   }
-  f32x16_t acc[4][2];
-  tile<false>(smem, W + static_cast<int64_t>(v0) * K, K, [&](int row) { return min(w0 + row, words - 1); }, Xc, K, c0, count - 1, 0,
+  Acc<S> acc;
+  tile<S, false>(smem, W + static_cast<int64_t>(v0) * K, K, [&](int row) { return min(w0 + row, words - 1); }, Xc, K, c0, count - 1, 0,
               K / kBK, acc);
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave >> 2, wn = wave & 3, lr = lane & 31, lh = lane >> 5;
+  const Place<S> w;
+  const int lr = w.lr, lh = w.lh;
   const int top = count - c0;
 #pragma unroll
   for (int j = 0; j < 2; ++j)
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-      const int c = 64 * wn + 32 * j + 8 * (e >> 2) + 4 * lh + (e & 3);
+      const int c = w.col0() + 32 * j + 8 * (e >> 2) + 4 * lh + (e & 3);
       const float ref = sRef[c], rest = sRest[c], g = sG[c];
       const int t = sT[c];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < S::kFM; ++i) {
         const float p = exp_f((acc[i][j][e] - ref) - rest);
-        acc[i][j][e] = c < top ? g * (t == w0 + 128 * wm + 32 * i + lr ? p - 1.f : p) : 0.f;
+        acc[i][j][e] = c < top ? g * (t == w0 + w.row0() + 32 * i + lr ? p - 1.f : p) : 0.f;
       }
     }
-  store_bf16(acc, smem, [&](int row, int col, uint4 v) {
+  store_bf16<S>(acc, smem, [&](int row, int col, uint4 v) {
     if (w0 + row < words && c0 + col < pitch) *reinterpret_cast<uint4 *>(Zt + (w0 + row) * pitch + c0 + col) = v;
   });
 }
 
 // dW rows v0 .. v0 + words - 1 = dz^T X over the listed rows.
-__global__ __launch_bounds__(gemm16::kThreads) void k_head_dw(const uint16_t *__restrict__ Zt, int64_t pitch,
+template <class S>
+__global__ __launch_bounds__(S::kThreads, 2) void k_head_dw(const uint16_t *__restrict__ Zt, int64_t pitch,
                                                               const uint16_t *__restrict__ Xc, int K, int v0, int words, HeadRows h,
                                                               uint16_t *__restrict__ dW) {
   using namespace gemm16;
-  __shared__ __attribute__((aligned(16))) uint8_t smem[kLds];
+  __shared__ __attribute__((aligned(16))) uint8_t smem[S::kLds];
   const int KT = (h.count[0] + kBK - 1) / kBK;
   int tr, tc;
-  if (!place(blockIdx.x, (words + kBM - 1) / kBM, (K + kBN - 1) / kBN, tr, tc)) return;
-  const int w0 = tr * kBM, c0 = tc * kBN;
-  f32x16_t acc[4][2];
+  if (!place(blockIdx.x, (words + S::kBM - 1) / S::kBM, (K + S::kBN - 1) / S::kBN, tr, tc)) return;
+  const int w0 = tr * S::kBM, c0 = tc * S::kBN;
+  Acc<S> acc;
   if (KT > 0)
-    tile<true>(smem, Zt, static_cast<uint32_t>(pitch), [&](int row) { return min(w0 + row, words - 1); }, Xc, K, c0, K - 1, KT * kBK - 1,
+    tile<S, true>(smem, Zt, static_cast<uint32_t>(pitch), [&](int row) { return min(w0 + row, words - 1); }, Xc, K, c0, K - 1, KT * kBK - 1,
                KT, acc);
   else
-    clear(acc);
-  store_bf16(acc, smem, [&](int row, int col, uint4 v) {
+    clear<S>(acc);
+  store_bf16<S>(acc, smem, [&](int row, int col, uint4 v) {
     if (w0 + row < words && c0 + col < K) *reinterpret_cast<uint4 *>(dW + static_cast<int64_t>(v0 + w0 + row) * K + c0 + col) = v;
   });
 }
 
 // ---------------------------------------------------------------------------
 namespace {
+template <class S>
 int tiles_of(int64_t rows, int64_t cols) {
-  return static_cast<int>(((rows + gemm16::kBM - 1) / gemm16::kBM) * ((cols + gemm16::kBN - 1) / gemm16::kBN));
+  return static_cast<int>(((rows + S::kBM - 1) / S::kBM) * ((cols + S::kBN - 1) / S::kBN));
 }
+using gemm16::Big;
+using gemm16::Mid;
 }  // namespace
+
+HeadCut head_cut(int64_t M, int64_t K, int64_t words) {
+  HeadCut c;
+  if (M <= kHeadSmall) {
+    // one or two workgroups a compute unit, as their stages allow
+    c.mid = 0;
+    c.bm = c.bn = 1;
+    c.slots = 0;
+    const int64_t cols = (K + kSmCols - 1) / kSmCols;
+    c.most = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({(M <= 32 ? 512 : 256) / cols, words / 512, 64})));
+    return c;
+  }
+  // Splits fill the chip with either tile; Mid ones where Big would be half empty
+  // (300 x 32000 x 4096: 280 us with Big, 317 with Mid; 100 x 32000 x 4096: 208 and 189).
+  c.mid = M <= Mid::kBM ? 1 : 0;
+  c.bm = c.mid ? Mid::kBM : Big::kBM;
+  c.bn = c.mid ? Mid::kBN : Big::kBN;
+  c.slots = c.mid ? 512 : 256;
+  // each at least 8 steps of 64 words long, their sums within 512 MB
+  c.most = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({32, words / 512, (int64_t{1} << 27) / (M * K)})));
+  return c;
+}
 
 hipError_t launch_head_rows(const int64_t *target, int M, int V, const HeadRows &h, hipStream_t s) {
   hipLaunchKernelGGL(k_head_rows, dim3(1), dim3(1024), 0, s, target, M, V, h);
@@ -441,32 +797,75 @@ hipError_t launch_head_gather(const uint16_t *X, int M, int K, const HeadRows &h
   return hipGetLastError();
 }
 
-hipError_t launch_head_piece(const uint16_t *Xc, int M, const uint16_t *W, int V, int K, int v0, int words, bool first, const HeadRows &h,
-                             const HeadPiece &pc, int splits, float *C, hipStream_t s) {
-  const int tiles = tiles_of(M, words);
-  if (C)
-    hipLaunchKernelGGL(k_head_logits<true>, dim3(tiles), dim3(gemm16::kThreads), 0, s, Xc, W, K, v0, words, h, pc);
-  else
-    hipLaunchKernelGGL(k_head_logits<false>, dim3(tiles), dim3(gemm16::kThreads), 0, s, Xc, W, K, v0, words, h, pc);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(k_head_refs, dim3((M + 63) / 64), dim3(256), 0, s, h, pc, (words + 63) / 64, first ? 1 : 0, C ? 1 : 0);
-  e = hipGetLastError();
-  if (e != hipSuccess || !C) return e;
-  hipLaunchKernelGGL(k_head_acc, dim3(tiles_of(M, K) * splits), dim3(gemm16::kThreads), 0, s, W, V, K, v0, splits, first ? 1 : 0, h, pc, C);
+template <class S, bool kE>
+static hipError_t launch_head_logits(const uint16_t *Xc, int M, const uint16_t *W, int K, int v0, int words, const HeadRows &h,
+                                     const HeadPiece &pc, hipStream_t s) {
+  hipLaunchKernelGGL((k_head_logits<S, kE>), dim3(tiles_of<S>(M, words)), dim3(S::kThreads), 0, s, Xc, W, K, v0, words, h, pc);
   return hipGetLastError();
 }
 
-hipError_t launch_head_finish(const uint16_t *W, int64_t M, int K, const float *weight, const HeadRows &h, int splits, const float *C,
+template <int kMB>
+static hipError_t launch_head_small(const uint16_t *X, const int64_t *target, int M, const uint16_t *W, int V, int K, int v0, int words,
+                                    bool first, const HeadRows &h, const HeadPiece &pc, const HeadCut &cut, float *C, hipStream_t s) {
+  const dim3 g((words + kSmWords - 1) / kSmWords), t(kSmThreads);
+  if (C)
+    hipLaunchKernelGGL((k_head_small<kMB, true>), g, t, 0, s, X, target, M, W, V, K, v0, words, h, pc);
+  else
+    hipLaunchKernelGGL((k_head_small<kMB, false>), g, t, 0, s, X, target, M, W, V, K, v0, words, h, pc);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(k_head_refs<1>, dim3(M), dim3(256), 0, s, h, pc, (words + 63) / 64, first ? 1 : 0, C ? 1 : 0);
+  e = hipGetLastError();
+  if (e != hipSuccess || !C) return e;
+  hipLaunchKernelGGL(k_head_small_acc<kMB>, dim3((K + kSmCols - 1) / kSmCols * cut.most), t, 0, s, W, V, K, v0, cut, first ? 1 : 0, h, pc, C);
+  return hipGetLastError();
+}
+
+hipError_t launch_head_small_piece(const uint16_t *X, const int64_t *target, int M, const uint16_t *W, int V, int K, int v0, int words,
+                                   bool first, const HeadRows &h, const HeadPiece &pc, const HeadCut &cut, float *C, hipStream_t s) {
+  switch ((M + 15) / 16) {
+    case 1: return launch_head_small<1>(X, target, M, W, V, K, v0, words, first, h, pc, cut, C, s);
+    case 2: return launch_head_small<2>(X, target, M, W, V, K, v0, words, first, h, pc, cut, C, s);
+    case 3: return launch_head_small<3>(X, target, M, W, V, K, v0, words, first, h, pc, cut, C, s);
+    default: return launch_head_small<4>(X, target, M, W, V, K, v0, words, first, h, pc, cut, C, s);
+  }
+}
+
+hipError_t launch_head_piece(const uint16_t *Xc, int M, const uint16_t *W, int V, int K, int v0, int words, bool first, const HeadRows &h,
+                             const HeadPiece &pc, const HeadCut &cut, float *C, hipStream_t s) {
+  const bool mid = gemm16::use_mid(M, words);
+  hipError_t e = C ? (mid ? launch_head_logits<Mid, true>(Xc, M, W, K, v0, words, h, pc, s)
+                          : launch_head_logits<Big, true>(Xc, M, W, K, v0, words, h, pc, s))
+                   : (mid ? launch_head_logits<Mid, false>(Xc, M, W, K, v0, words, h, pc, s)
+                          : launch_head_logits<Big, false>(Xc, M, W, K, v0, words, h, pc, s));
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(k_head_refs<16>, dim3((M + 15) / 16), dim3(256), 0, s, h, pc, (words + 63) / 64, first ? 1 : 0, C ? 1 : 0);
+  e = hipGetLastError();
+  if (e != hipSuccess || !C) return e;
+  // workgroups for any number of rows that have a target
+  const int trows = (M + cut.bm - 1) / cut.bm, tcols = (K + cut.bn - 1) / cut.bn;
+  int items = trows * tcols;
+  for (int r = 1; r <= trows && r * tcols <= 50 * cut.slots; ++r) items = std::max(items, r * tcols * splits_for(r * tcols, cut));
+  const dim3 grid(items);
+  if (cut.mid)
+    hipLaunchKernelGGL(k_head_acc<Mid>, grid, dim3(Mid::kThreads), 0, s, W, V, K, v0, cut, first ? 1 : 0, h,
+                       pc, C);
+  else
+    hipLaunchKernelGGL(k_head_acc<Big>, grid, dim3(Big::kThreads), 0, s, W, V, K, v0, cut, first ? 1 : 0, h,
+                       pc, C);
+  return hipGetLastError();
+}
+
+hipError_t launch_head_finish(const uint16_t *W, int64_t M, int K, const float *weight, const HeadRows &h, const HeadCut &cut, const float *C,
                               float *loss, float *lse, void *dX, int grad, hipStream_t s) {
-  const dim3 g(static_cast<unsigned>(M)), t(grad ? 256 : 64);
+  const dim3 g(static_cast<unsigned>(M), grad ? (K + 2047) / 2048 : 1), t(grad ? 256 : 64);
   const int rows = static_cast<int>(M);
   if (grad == 0)
-    hipLaunchKernelGGL(k_head_finish<0>, g, t, 0, s, W, K, weight, h, rows, splits, C, loss, lse, dX);
+    hipLaunchKernelGGL(k_head_finish<0>, g, t, 0, s, W, K, weight, h, rows, cut, C, loss, lse, dX);
   else if (grad == 1)
-    hipLaunchKernelGGL(k_head_finish<1>, g, t, 0, s, W, K, weight, h, rows, splits, C, loss, lse, dX);
+    hipLaunchKernelGGL(k_head_finish<1>, g, t, 0, s, W, K, weight, h, rows, cut, C, loss, lse, dX);
   else
-    hipLaunchKernelGGL(k_head_finish<2>, g, t, 0, s, W, K, weight, h, rows, splits, C, loss, lse, dX);
+    hipLaunchKernelGGL(k_head_finish<2>, g, t, 0, s, W, K, weight, h, rows, cut, C, loss, lse, dX);
   return hipGetLastError();
 }
 
@@ -478,10 +877,18 @@ hipError_t launch_head_scale(const float *D, int64_t M, int K, const int64_t *ta
 hipError_t launch_head_dw(const uint16_t *Xc, int M, const uint16_t *W, int K, int v0, int words, const HeadRows &h, const float *lse,
                           const float *weight, uint16_t *Zt, uint16_t *dW, hipStream_t s) {
   const int64_t pitch = (static_cast<int64_t>(M) + 63) / 64 * 64;
-  hipLaunchKernelGGL(k_head_dz, dim3(tiles_of(words, M)), dim3(gemm16::kThreads), 0, s, Xc, W, K, v0, words, h, lse, weight, pitch, Zt);
+  if (gemm16::use_mid(words, M))
+    hipLaunchKernelGGL(k_head_dz<Mid>, dim3(tiles_of<Mid>(words, M)), dim3(Mid::kThreads), 0, s, Xc, W, K, v0, words, h, lse, weight, pitch,
+                       Zt);
+  else
+    hipLaunchKernelGGL(k_head_dz<Big>, dim3(tiles_of<Big>(words, M)), dim3(Big::kThreads), 0, s, Xc, W, K, v0, words, h, lse, weight, pitch,
+                       Zt);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(k_head_dw, dim3(tiles_of(words, K)), dim3(gemm16::kThreads), 0, s, Zt, pitch, Xc, K, v0, words, h, dW);
+  if (gemm16::use_mid(words, K))
+    hipLaunchKernelGGL(k_head_dw<Mid>, dim3(tiles_of<Mid>(words, K)), dim3(Mid::kThreads), 0, s, Zt, pitch, Xc, K, v0, words, h, dW);
+  else
+    hipLaunchKernelGGL(k_head_dw<Big>, dim3(tiles_of<Big>(words, K)), dim3(Big::kThreads), 0, s, Zt, pitch, Xc, K, v0, words, h, dW);
   return hipGetLastError();
 }
 

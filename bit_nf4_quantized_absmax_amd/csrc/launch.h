@@ -374,14 +374,24 @@ struct HeadPiece {
   int rows;        // M
   int pitch;       // the piece's words filled up to 64
 };
+// How the second product is cut: its tiles, workgroups at once, splits at most.
+struct HeadCut {
+  int bm, bn, slots, most;
+  int mid;
+};
+constexpr int kHeadSmall = 64;   // rows up to which W's bytes count
+HeadCut head_cut(int64_t M, int64_t K, int64_t words);
 hipError_t launch_head_rows(const int64_t *target, int M, int V, const HeadRows &h, hipStream_t s);
 // Xc [M filled up to 64, K]
 hipError_t launch_head_gather(const uint16_t *X, int M, int K, const HeadRows &h, uint16_t *Xc, hipStream_t s);
-// Words v0 .. v0 + words - 1; C [splits][M][K] fp32, or nullptr without a gradient.
+// Words v0 .. v0 + words - 1; C [cut.most][M][K] fp32, or nullptr without a gradient.
 hipError_t launch_head_piece(const uint16_t *Xc, int M, const uint16_t *W, int V, int K, int v0, int words, bool first, const HeadRows &h,
-                             const HeadPiece &pc, int splits, float *C, hipStream_t s);
+                             const HeadPiece &pc, const HeadCut &cut, float *C, hipStream_t s);
+// M <= kHeadSmall, straight from X and target (it fills in h too).
+hipError_t launch_head_small_piece(const uint16_t *X, const int64_t *target, int M, const uint16_t *W, int V, int K, int v0, int words,
+                                   bool first, const HeadRows &h, const HeadPiece &pc, const HeadCut &cut, float *C, hipStream_t s);
 // grad 0: none, 1: dX in bf16, 2: in fp32.
-hipError_t launch_head_finish(const uint16_t *W, int64_t M, int K, const float *weight, const HeadRows &h, int splits, const float *C,
+hipError_t launch_head_finish(const uint16_t *W, int64_t M, int K, const float *weight, const HeadRows &h, const HeadCut &cut, const float *C,
                               float *loss, float *lse, void *dX, int grad, hipStream_t s);
 hipError_t launch_head_scale(const float *D, int64_t M, int K, const int64_t *target, int V, const float *g, uint16_t *dX, hipStream_t s);
 // Rows v0 .. v0 + words - 1 of dW; Zt [words, M filled up to 64].

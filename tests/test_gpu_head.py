@@ -6,7 +6,9 @@ below 2^24).  e^(z - ref) adds 2^-20 (the argument, at most 16 log2(e) or small
 against the largest, times 2^-24, and the hardware's exponential), so p_j is off by
 e_p = 2 e_z + 2^-19 of itself, the loss by 2 e_z + 2^-19 and its own rounding.  For dX
 each p_j but the target's is rounded to bf16, 2^-8 of it, and for dW each dz_mj;
-then the gradient is rounded once, 2^-8 again; the fp32 sums between add n 2^-23 of
+words whose reference differs from their row's are brought to it by a power of two, while
+the references, multiples of 64 ln 2 in fp32, are each off by 2^-23 of themselves: 2^-22 max |z|
+of such a p_j for dX alone; then the gradient is rounded once, 2^-8 again; the fp32 sums between add n 2^-23 of
 their terms for n terms.  What is below fp32's normal range, 2^-126, may be flushed to 0:
 for dW at most 2^-126 a dz_mj and a product, for dX (e^(z - ref), against a largest of
 e^-16 or more) at most 2^-126 e^16 < 2^-102 a p_j."""
@@ -74,7 +76,8 @@ def _check(X, W, t, weight, whole=False, dW=True):
     one[np.arange(M), np.where(real, tt, 0)] = real
     ag = np.abs(np.where(real, g, 0))[:, None]
     terms = ag * ((off + np.abs(p - 1) * one) @ np.abs(w))
-    e = ag * ((R + ep[:, None] + V * S) * (off @ np.abs(w)) + (ep[:, None] + 4 * S) * ((p * one) @ np.abs(w))) + 4 * S * terms
+    ez2 = 2.0 ** -22 * np.abs(np.where(real[:, None], x, 0) @ w.T).max(1)
+    e = ag * ((R + (ep + ez2)[:, None] + V * S) * (off @ np.abs(w)) + (ep[:, None] + 4 * S) * ((p * one) @ np.abs(w))) + 4 * S * terms
     e = e + 2.0 ** -102 * ag * np.abs(w).sum(0) + 2.0 ** -126
     _close(got[2], dX, R * (np.abs(dX) + e) + e, "dX")
     D = torch.empty(M, K, dtype=FP32, device=DEV)
