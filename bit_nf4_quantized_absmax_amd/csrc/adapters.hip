@@ -6,12 +6,8 @@
 // with a = index[m], A [n, r, K], B [n, N, r].  A token whose index is outside
 // [0, n) has no adapter.
 //
-// Up to kAdSmall tokens (decoding) two kernels do it: k_ad_down forms T, one
-// workgroup per adapter in use and 16 of its rows; k_ad_small multiplies the
-// packed weight and adds each token's own T B^T.  A wave finds the tokens of
-// an adapter by a ballot over the indices: nothing is sorted.
-//
-// Above that the tokens are sorted by adapter once (k_ad_sort, by rank and so
+// Here for more than kAdSmall tokens, and for every backward pass (fewer tokens
+// forward: adapters_small.hip).  The tokens are sorted by adapter once (k_ad_sort, by rank and so
 // in a fixed order); T and G are products over 32-token tiles of one adapter
 // (k_ad_down_tiles); the wide products run on 256 x 256 tiles of sorted tokens,
 // gathered by the DMA, whose epilogue adds the adapters' term 32 tokens at a
@@ -26,14 +22,7 @@
 
 namespace qlora {
 
-__constant__ uint32_t cAdQ4Level[3 * 16] = {QLORA_Q4_LEVEL_BITS};
-__constant__ uint32_t cAdT8Level[256] = {QLORA_T8_LEVEL_BITS};
-
 namespace {
-
-constexpr int kAdWaves = 16;
-constexpr int kAdThreads = kAdWaves * 64;
-constexpr int kAdRows = 16;        // weight rows of a workgroup of k_ad_small
 
 __device__ __forceinline__ int adapter_of(const int64_t *index, int m, int n) {
   const int64_t a = index[m];
@@ -41,213 +30,6 @@ __device__ __forceinline__ int adapter_of(const int64_t *index, int m, int n) {
 }
 
 }  // namespace
-
-// ---------------------------------------------------------------------------
-// Decoding, T [M, r]: workgroup (token m, 16 adapter rows).  The first token of
-// an adapter does the work of all of them, 16 tokens an MFMA tile; the 16
-// waves split K and are summed in LDS in wave order.
-template <int kMB>
-__global__ __launch_bounds__(kAdThreads) void k_ad_down(const uint16_t *__restrict__ X, int M, int K, const uint16_t *__restrict__ A,
-                                                        int r, const float *__restrict__ scale, const int64_t *__restrict__ index,
-                                                        int n, uint16_t *__restrict__ T) {
-  __shared__ float red[kAdWaves][16][17];
-  __shared__ int tok[64];
-  const int jt = blockIdx.x, m0 = blockIdx.y;
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int nl = lane & 15, g = lane >> 4;
-  const int mine = lane < M ? adapter_of(index, lane, n) : -1;
-  const int a = __shfl(mine, m0, 64);
-  if (a < 0) {
-    if (threadIdx.x < 16 && 16 * jt + threadIdx.x < r) T[static_cast<int64_t>(m0) * r + 16 * jt + threadIdx.x] = 0;
-    return;
-  }
-  const uint64_t mask = __ballot(mine == a);
-  if (__builtin_ctzll(mask) != m0) return;
-  const int cnt = __popcll(mask);
-  if (wave == 0 && mine == a) tok[__popcll(mask & ((uint64_t{1} << lane) - 1))] = lane;
-  __syncthreads();
-  const int j = 16 * jt + nl;
-  const uint16_t *arow = A + (static_cast<int64_t>(a) * r + min(j, r - 1)) * K;
-  const float s = scale[a];
-  const int steps = K >> 5;                       // K % 64 == 0
-#pragma unroll 1
-  for (int t0 = 0; t0 < cnt; t0 += 16 * kMB) {
-    const uint16_t *xrow[kMB];
-#pragma unroll
-    for (int mb = 0; mb < kMB; ++mb) xrow[mb] = X + static_cast<int64_t>(tok[min(t0 + 16 * mb + nl, cnt - 1)]) * K;
-    f32x4_t acc[kMB];
-#pragma unroll
-    for (int mb = 0; mb < kMB; ++mb) acc[mb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    constexpr int kBatch = 8;
-    for (int b = wave; b < steps; b += kAdWaves * kBatch) {
-      bf16x8_t av[kBatch], xv[kBatch][kMB];
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int k = 32 * min(b + u * kAdWaves, steps - 1) + 8 * g;
-        av[u] = *reinterpret_cast<const bf16x8_t *>(arow + k);
-#pragma unroll
-        for (int mb = 0; mb < kMB; ++mb) xv[u][mb] = *reinterpret_cast<const bf16x8_t *>(xrow[mb] + k);
-      }
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        if (b + u * kAdWaves >= steps) break;     // uniform
-#pragma unroll
-        for (int mb = 0; mb < kMB; ++mb) acc[mb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv[u][mb], av[u], acc[mb], 0, 0, 0);
-      }
-    }
-    // lane: column (adapter row) nl, tokens 4 g + e
-#pragma unroll
-    for (int mb = 0; mb < kMB; ++mb) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) red[wave][4 * g + e][nl] = acc[mb][e];
-      __syncthreads();
-      if (threadIdx.x < 256) {
-        const int row = threadIdx.x >> 4, c = threadIdx.x & 15, at = t0 + 16 * mb + row;
-        float v = 0.f;
-#pragma unroll
-        for (int w = 0; w < kAdWaves; ++w) v += red[w][row][c];
-        if (at < cnt && 16 * jt + c < r) T[static_cast<int64_t>(tok[at]) * r + 16 * jt + c] = f32_to_bf16(s * v);
-      }
-      __syncthreads();
-    }
-  }
-}
-
-// ---------------------------------------------------------------------------
-// Decoding, Y: workgroup = 16 weight rows x the whole K.  Wave w takes the
-// blocks w, w + 16, ...; lane (row n = l % 16, g = l / 16) expands codes 16 g ..
-// +15 of its row's block through a byte -> bf16x2 table and each block's partial
-// product is scaled by its constant in fp32, so the weight is bf16(level) times
-// the constant, as in the framework's other decoding kernels.  The adapters in
-// use go to the waves in turn; a token takes the product with its own adapter
-// only.  The 16 waves' sums are added in LDS in wave order and rounded once.
-template <int kMB>
-__global__ __launch_bounds__(kAdThreads) void k_ad_small(const uint16_t *__restrict__ X, int M, NF4View w,
-                                                         const uint16_t *__restrict__ T, const uint16_t *__restrict__ B, int r,
-                                                         const int64_t *__restrict__ index, int nad, uint16_t *__restrict__ Y) {
-  constexpr int kBlk = kMB == 1 ? 6 : (kMB == 2 ? 3 : (kMB == 3 ? 2 : 1));
-  __shared__ uint32_t sLut[256 * 64];
-  __shared__ float sT8[256];
-  __shared__ float red[kAdWaves][kMB * 16][kAdRows + 1];
-  const int N = w.N, K = w.K;
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int nl = lane & 15, g = lane >> 4;
-  const int n0 = blockIdx.x * kAdRows;
-  const int n = min(n0 + nl, N - 1);
-  const int KB = K >> 6;
-  const float mean = w.mean[0];
-  const float t8v = u2f(cAdT8Level[threadIdx.x & 255]);
-  const int mine = lane < M ? adapter_of(index, lane, nad) : -1;
-
-  uint2 pk[kBlk];
-  uint32_t code[kBlk];
-  float c2v[kBlk];
-  bf16x8_t xb[kBlk][kMB][2];
-  const uint8_t *prow = w.packed + static_cast<int64_t>(n) * (K >> 1);
-  const int64_t rowblk = static_cast<int64_t>(n) * KB;
-  auto load_batch = [&](int b0) __attribute__((always_inline)) {
-#pragma unroll
-    for (int u = 0; u < kBlk; ++u) {
-      const int b = min(b0 + u * kAdWaves, KB - 1);
-      pk[u] = *reinterpret_cast<const uint2 *>(prow + 32 * b + 8 * g);
-      code[u] = w.code8[rowblk + b];
-      c2v[u] = w.c2[(rowblk + b) >> 8];
-    }
-#pragma unroll
-    for (int u = 0; u < kBlk; ++u) {
-      const int k = 64 * min(b0 + u * kAdWaves, KB - 1) + 16 * g;
-#pragma unroll
-      for (int mb = 0; mb < kMB; ++mb)
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-          xb[u][mb][t] = *reinterpret_cast<const bf16x8_t *>(X + static_cast<int64_t>(min(16 * mb + nl, M - 1)) * K + k + 8 * t);
-    }
-  };
-  load_batch(min(wave, KB - 1));
-  {
-    const uint32_t *lvt = cAdQ4Level + 16 * w.qtype;
-    const float lo = u2f(lvt[wave]);
-#pragma unroll
-    for (int j = 0; j < 16; ++j) sLut[64 * (wave + 16 * j) + lane] = pack_bf16x2(lo, u2f(lvt[j]));
-  }
-  sT8[threadIdx.x & 255] = t8v;                 // four threads write each entry, same value
-  raw_barrier<wait_imm(63, 0)>();
-
-  f32x4_t acc[kMB];
-#pragma unroll
-  for (int mb = 0; mb < kMB; ++mb) acc[mb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  for (int b0 = wave; b0 < KB; b0 += kAdWaves * kBlk) {
-    if (b0 != wave) load_batch(b0);
-#pragma unroll
-    for (int u = 0; u < kBlk; ++u) {
-      if (b0 + u * kAdWaves >= KB) break;       // uniform
-      const float chat = decode_absmax(sT8[code[u]], c2v[u], mean);
-      const uint32_t words[2] = {pk[u].x, pk[u].y};
-      bf16x8_t wop[2];
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        uint32_t o[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = sLut[64 * ((words[t] >> (8 * i)) & 0xffu) + lane];
-        wop[t] = __builtin_bit_cast(bf16x8_t, o);
-      }
-#pragma unroll
-      for (int mb = 0; mb < kMB; ++mb) {
-        f32x4_t part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb[u][mb][0], wop[0], f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
-        part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xb[u][mb][1], wop[1], part, 0, 0, 0);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[mb][e] = __builtin_fmaf(chat, part[e], acc[mb][e]);
-      }
-    }
-  }
-
-  // The adapters in use, this wave's share of them.
-  uint64_t left = __ballot(mine >= 0);
-  for (int d = 0; left; ++d) {
-    const int a = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
-    const uint64_t mask = __ballot(mine == a);
-    left &= ~mask;
-    if ((d & (kAdWaves - 1)) != wave) continue;
-    const uint16_t *brow = B + (static_cast<int64_t>(a) * N + n) * r;
-    f32x4_t part[kMB];
-#pragma unroll
-    for (int mb = 0; mb < kMB; ++mb) part[mb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    for (int j0 = 0; j0 < r; j0 += 32) {
-      const int j = j0 + 8 * g;
-      const bool ok = j < r;                    // r % 8 == 0
-      bf16x8_t bop = *reinterpret_cast<const bf16x8_t *>(brow + (ok ? j : 0));
-      if (!ok) bop = bf16x8_t{};
-#pragma unroll
-      for (int mb = 0; mb < kMB; ++mb) {
-        bf16x8_t top = *reinterpret_cast<const bf16x8_t *>(T + static_cast<int64_t>(min(16 * mb + nl, M - 1)) * r + (ok ? j : 0));
-        if (!ok) top = bf16x8_t{};
-        part[mb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(top, bop, part[mb], 0, 0, 0);
-      }
-    }
-#pragma unroll
-    for (int mb = 0; mb < kMB; ++mb)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if ((mask >> (16 * mb + 4 * g + e)) & 1) acc[mb][e] += part[mb][e];
-  }
-
-#pragma unroll
-  for (int mb = 0; mb < kMB; ++mb)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) red[wave][16 * mb + 4 * g + e][nl] = acc[mb][e];
-  __syncthreads();
-  for (int idx = threadIdx.x; idx < kMB * 16 * kAdRows; idx += kAdThreads) {
-    const int m = idx / kAdRows, c = idx % kAdRows;
-    if (m < M && n0 + c < N) {
-      float v = red[0][m][c];
-#pragma unroll
-      for (int q = 1; q < kAdWaves; ++q) v += red[q][m][c];
-      Y[static_cast<int64_t>(m) * N + n0 + c] = f32_to_bf16(v);
-    }
-  }
-}
 
 // ---------------------------------------------------------------------------
 // Tokens sorted by adapter, in order of their number within one; tokens without
@@ -732,24 +514,6 @@ __global__ __launch_bounds__(kGdThreads) void k_ad_grads(AdGradArgs g, AdPlan p)
 }
 
 // ---------------------------------------------------------------------------
-hipError_t launch_ad_small(const uint16_t *X, int M, const NF4View &w, const AdapterSet &ad, uint16_t *T, uint16_t *Y, hipStream_t s) {
-  const dim3 down((ad.r + 15) / 16, M), main((w.N + kAdRows - 1) / kAdRows), th(kAdThreads);
-  const int mb = (M + 15) / 16;
-  if (mb == 1)
-    hipLaunchKernelGGL(k_ad_down<1>, down, th, 0, s, X, M, w.K, ad.A, ad.r, ad.scale, ad.index, ad.n, T);
-  else
-    hipLaunchKernelGGL(k_ad_down<2>, down, th, 0, s, X, M, w.K, ad.A, ad.r, ad.scale, ad.index, ad.n, T);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  switch (mb) {
-    case 1: hipLaunchKernelGGL(k_ad_small<1>, main, th, 0, s, X, M, w, T, ad.B, ad.r, ad.index, ad.n, Y); break;
-    case 2: hipLaunchKernelGGL(k_ad_small<2>, main, th, 0, s, X, M, w, T, ad.B, ad.r, ad.index, ad.n, Y); break;
-    case 3: hipLaunchKernelGGL(k_ad_small<3>, main, th, 0, s, X, M, w, T, ad.B, ad.r, ad.index, ad.n, Y); break;
-    default: hipLaunchKernelGGL(k_ad_small<4>, main, th, 0, s, X, M, w, T, ad.B, ad.r, ad.index, ad.n, Y); break;
-  }
-  return hipGetLastError();
-}
-
 hipError_t launch_ad_sort(const AdapterSet &ad, int M, const AdPlan &p, hipStream_t s) {
   hipLaunchKernelGGL(k_ad_sort, dim3(1), dim3(kSortThreads), 0, s, ad.index, M, ad.n, p);
   return hipGetLastError();

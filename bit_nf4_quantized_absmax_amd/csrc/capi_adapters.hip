@@ -41,10 +41,11 @@ AdPlan take_plan(Carve &c, int64_t M, int64_t n) {
   return p;
 }
 
-// Forward: T (when the caller keeps none) | above the decoding sizes the order
-// of the tokens and the dequantized weight.
+// Forward: T (when the caller keeps none) | the decoding kernels' sums, or above
+// their sizes the order of the tokens and the dequantized weight.
 struct FwdParts {
   uint16_t *T, *Wd;
+  char *sums;
   AdPlan plan;
 };
 size_t carve_fwd(void *ws, int64_t M, int64_t N, int64_t K, int32_t n, int32_t r, FwdParts *f) {
@@ -53,6 +54,8 @@ size_t carve_fwd(void *ws, int64_t M, int64_t N, int64_t K, int32_t n, int32_t r
   if (M > kAdSmall) {
     f->plan = take_plan(c, M, n);
     f->Wd = c.take<uint16_t>(N * K);
+  } else {
+    f->sums = c.take<char>(ad_small_ws_bytes(static_cast<int>(M), static_cast<int>(N), static_cast<int>(K), r));
   }
   return c.used;
 }
@@ -107,7 +110,7 @@ int qlora_adapter_linear_fwd(const uint16_t *X, int64_t M, const qlora_nf4_weigh
   const NF4View w = view_of(W);
   uint16_t *T = T_out ? T_out : f.T;
   const int m = static_cast<int>(M);
-  if (M <= kAdSmall) return from_hip(launch_ad_small(X, m, w, set, T, Y, s));
+  if (M <= kAdSmall) return from_hip(launch_ad_small(X, m, w, set, T, Y, f.sums, s));
   hipError_t e = launch_ad_sort(set, m, f.plan, s);
   if (e == hipSuccess) e = launch_ad_down(X, m, w.K, set.A, set, f.plan, T, s);
   if (e == hipSuccess) e = dequantize(w, f.Wd, s);

@@ -336,8 +336,10 @@ struct AdPlan {
 };
 // 32-token tiles of one adapter each that M tokens of n adapters can make.
 inline int64_t ad_tiles_max(int64_t M, int64_t n) { return (M + 31) / 32 + (M < n ? M : n); }
-// M <= kAdSmall.  T [M, r] is written too.
-hipError_t launch_ad_small(const uint16_t *X, int M, const NF4View &w, const AdapterSet &ad, uint16_t *T, uint16_t *Y, hipStream_t s);
+// M <= kAdSmall.  T [M, r] is written too; ws: ad_small_ws_bytes.
+size_t ad_small_ws_bytes(int M, int N, int K, int r);
+hipError_t launch_ad_small(const uint16_t *X, int M, const NF4View &w, const AdapterSet &ad, uint16_t *T, uint16_t *Y, void *ws,
+                           hipStream_t s);
 hipError_t launch_ad_sort(const AdapterSet &ad, int M, const AdPlan &p, hipStream_t s);
 // out [M, r] = scale_a P Q_a^T, P [M, D], Q [n, r, D], D % 64 == 0; zeros for tokens without an adapter.
 hipError_t launch_ad_down(const uint16_t *P, int M, int D, const uint16_t *Q, const AdapterSet &ad, const AdPlan &p, uint16_t *out,

@@ -3,7 +3,7 @@ ABI's header).  Argument marshalling only, as in ops.py; a model's gradients are
 hundreds of small tensors, so they are looked at attribute by attribute, over
 the whole list at a time."""
 
-import ctypes
+import struct
 from operator import attrgetter
 
 import torch
@@ -13,26 +13,25 @@ from .adapters import _on
 from .ops import _ptr, _stream, _workspace
 
 TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+PLAIN = {torch.Tensor, torch.nn.Parameter}
 
 _dtype = attrgetter("dtype")
-_shape = attrgetter("shape")
 
 
 def _listed(tensors, name):
     """(data pointers, element counts, types, device index or None) of a list of tensors."""
-    for t in tensors:
-        if not isinstance(t, torch.Tensor):
-            raise TypeError("%s must be tensors" % name)
-    try:
-        types = list(map(TYPES.__getitem__, map(_dtype, tensors)))
-    except KeyError as e:
-        raise TypeError("%s must be float32, bfloat16 or float16, got %s" % (name, e.args[0])) from None
+    if not set(map(type, tensors)) <= PLAIN and not all(isinstance(t, torch.Tensor) for t in tensors):
+        raise TypeError("%s must be tensors" % name)
+    types = list(map(_dtype, tensors))
+    for t in set(types) - TYPES.keys():
+        raise TypeError("%s must be float32, bfloat16 or float16, got %s" % (name, t))
     if not all(map(torch.Tensor.is_contiguous, tensors)):
         raise ValueError("%s must be contiguous" % name)
     devices = set(map(torch.Tensor.get_device, tensors))
     if len(devices) > 1 or -1 in devices:
         raise ValueError("%s must be on one GPU device" % name)
-    return list(map(torch.Tensor.data_ptr, tensors)), list(map(torch.Tensor.numel, tensors)), types, devices.pop() if devices else None
+    return (list(map(torch.Tensor.data_ptr, tensors)), list(map(torch.Tensor.numel, tensors)), list(map(TYPES.get, types)),
+            devices.pop() if devices else None)
 
 
 def _call(grads, max_norm, groups, out, workspace):
@@ -50,17 +49,17 @@ def _call(grads, max_norm, groups, out, workspace):
     to = ptrs
     if max_norm is not None:
         if out is not None:
-            out = list(out)
-            to, _, to_types, to_device = _listed(out, "out")
-            if to_types != types or list(map(_shape, out)) != list(map(_shape, grads)) or to_device != device:
-                raise ValueError("out must be one tensor of the same shape, type and device for every gradient")
-        used = [p for p, n in zip(to, counts) if n]
-        if len(set(used)) != len(used):
-            raise ValueError("a tensor is written twice")
+            to, to_counts, to_types, to_device = _listed(list(out), "out")
+            if to_types != types or to_counts != counts or to_device != device:
+                raise ValueError("out must be one tensor of the same size, type and device for every gradient")
+        if len(set(to)) != len(to):
+            used = [p for p, n in zip(to, counts) if n]
+            if len(set(used)) != len(used):
+                raise ValueError("a tensor is written twice")
     n = len(grads)
     flat = [0] * (4 * n)
     flat[0::4], flat[1::4], flat[2::4], flat[3::4] = ptrs, to, counts, types
-    table = (ctypes.c_int64 * (4 * n))(*flat)     # qlora_grad_tensor [n]
+    table = struct.pack("%dq" % (4 * n), *flat)     # qlora_grad_tensor [n]
     first = grads[0]
     norm = torch.empty(groups, dtype=torch.float32, device=first.device)
     ws, ws_bytes = _workspace(workspace, lib().qlora_grad_norm_workspace_bytes(n, table, groups), first.device)
@@ -83,8 +82,8 @@ def grad_norm(grads, groups=1, workspace=None):
 
 def clip_grad_norm(grads, max_norm, groups=1, out=None, workspace=None):
     """grad_norm, and the gradients times min(1, max_norm / (norm + 1e-6)), in
-    place or into `out` (a tensor for every gradient, which overlaps no gradient but
-    its own).  Returns the norms before clipping (qlora_clip_grad_norm)."""
+    place or into `out` (for every gradient a tensor of its size and type, which
+    overlaps no gradient but its own).  Returns the norms before clipping (qlora_clip_grad_norm)."""
     max_norm = float(max_norm)
     if not max_norm >= 0.0:
         raise ValueError("max_norm must not be negative or NaN")
