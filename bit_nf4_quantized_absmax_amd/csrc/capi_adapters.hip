@@ -42,10 +42,11 @@ AdPlan take_plan(Carve &c, int64_t M, int64_t n) {
 }
 
 // Forward: T (when the caller keeps none) | the decoding kernels' sums, or above
-// their sizes the order of the tokens and the dequantized weight.
+// their sizes the order of the tokens, the dequantized weight and T's partial sums.
 struct FwdParts {
   uint16_t *T, *Wd;
   char *sums;
+  float *part, *tiles;
   AdPlan plan;
 };
 size_t carve_fwd(void *ws, int64_t M, int64_t N, int64_t K, int32_t n, int32_t r, FwdParts *f) {
@@ -54,16 +55,19 @@ size_t carve_fwd(void *ws, int64_t M, int64_t N, int64_t K, int32_t n, int32_t r
   if (M > kAdSmall) {
     f->plan = take_plan(c, M, n);
     f->Wd = c.take<uint16_t>(N * K);
+    f->part = c.take<float>(ad_down_splits(M, K, n) * M * r);
+    f->tiles = c.take<float>(ad_matmul_part_floats(M, N, K));
   } else {
     f->sums = c.take<char>(ad_small_ws_bytes(static_cast<int>(M), static_cast<int>(N), static_cast<int>(K), r));
   }
   return c.used;
 }
 
-// Backward, with Np = N filled up to 64: T (recomputed) | G | the order | W |
-// A transposed | B transposed | dY with filled rows (where Np > N).
+// Backward, with Np = N filled up to 64: T (recomputed) | G | their partial sums | the order | W |
+// A transposed | B transposed | dY with filled rows (where Np > N) | split tiles.
 struct BwdParts {
   uint16_t *T, *G, *Wd, *At, *Bt, *dYp;
+  float *part, *tiles;
   AdPlan plan;
 };
 size_t carve_bwd(void *ws, int64_t M, int64_t N, int64_t K, int32_t n, int32_t r, BwdParts *b) {
@@ -71,16 +75,14 @@ size_t carve_bwd(void *ws, int64_t M, int64_t N, int64_t K, int32_t n, int32_t r
   Carve c(ws);
   b->T = c.take<uint16_t>(M * r);
   b->G = c.take<uint16_t>(M * r);
+  b->part = c.take<float>(std::max(ad_down_splits(M, K, n), ad_down_splits(M, Np, n)) * M * r);
   b->plan = take_plan(c, M, n);
   b->Wd = c.take<uint16_t>(N * K);
   b->At = c.take<uint16_t>(static_cast<int64_t>(n) * r * K);
   b->Bt = c.take<uint16_t>(static_cast<int64_t>(n) * r * Np);
   b->dYp = c.take<uint16_t>(Np > N ? M * Np : 0);
+  b->tiles = c.take<float>(ad_matmul_part_floats(M, K, Np));
   return c.used;
-}
-
-hipError_t dequantize(const NF4View &w, uint16_t *Wd, hipStream_t s) {
-  return launch_dequantize(w.packed, w.code8, w.c2, w.mean, static_cast<int64_t>(w.N) * w.K, w.qtype, Wd, s);
 }
 
 }  // namespace
@@ -111,10 +113,17 @@ int qlora_adapter_linear_fwd(const uint16_t *X, int64_t M, const qlora_nf4_weigh
   uint16_t *T = T_out ? T_out : f.T;
   const int m = static_cast<int>(M);
   if (M <= kAdSmall) return from_hip(launch_ad_small(X, m, w, set, T, Y, f.sums, s));
-  hipError_t e = launch_ad_sort(set, m, f.plan, s);
-  if (e == hipSuccess) e = launch_ad_down(X, m, w.K, set.A, set, f.plan, T, s);
-  if (e == hipSuccess) e = dequantize(w, f.Wd, s);
-  if (e == hipSuccess) e = launch_ad_matmul_fwd(X, m, w.N, w.K, f.Wd, T, set.B, set.r, f.plan, Y, s);
+  AdPrepare prep{};
+  prep.index = set.index;
+  prep.plan = f.plan;
+  prep.w = w;
+  prep.Wd = f.Wd;
+  prep.M = m;
+  prep.n = set.n;
+  prep.r = set.r;
+  hipError_t e = launch_ad_prepare(prep, s);
+  if (e == hipSuccess) e = launch_ad_down(X, m, w.K, set.A, set, f.plan, f.part, T, s);
+  if (e == hipSuccess) e = launch_ad_matmul_fwd(X, m, w.N, w.K, f.Wd, T, set.B, set.r, f.plan, f.tiles, Y, s);
   return from_hip(e);
 }
 
@@ -134,26 +143,37 @@ int qlora_adapter_linear_bwd(const uint16_t *dY, const uint16_t *X, const uint16
   const AdapterSet set = set_of(ad);
   const NF4View w = view_of(W);
   const int m = static_cast<int>(M), Np = static_cast<int>(round_up(N, 64));
-  hipError_t e = launch_ad_sort(set, m, b.plan, s);
-  if (e == hipSuccess && dB && !T) {
-    e = launch_ad_down(X, m, w.K, set.A, set, b.plan, b.T, s);
-    T = b.T;
-  }
+  AdPrepare prep{};
+  prep.index = set.index;
+  prep.plan = b.plan;
+  prep.w = w;
+  prep.M = m;
+  prep.n = set.n;
+  prep.r = set.r;
+  prep.Np = Np;
   const uint16_t *dYp = dY;
   if (dX || dA) {
+    prep.B = set.B;
+    prep.Bt = b.Bt;
     if (Np > N) {
-      if (e == hipSuccess) e = launch_ad_pad(dY, m, w.N, Np, b.dYp, s);
+      prep.dY = dY;
+      prep.dYp = b.dYp;
       dYp = b.dYp;
     }
-    if (e == hipSuccess) e = launch_ad_transpose(set.B, set.n, w.N, set.r, Np, b.Bt, s);
-    if (e == hipSuccess) e = launch_ad_down(dYp, m, Np, b.Bt, set, b.plan, b.G, s);
   }
   if (dX) {
-    if (e == hipSuccess) e = dequantize(w, b.Wd, s);
-    if (e == hipSuccess) e = launch_ad_transpose(set.A, set.n, set.r, w.K, set.r, b.At, s);
-    if (e == hipSuccess) e = launch_ad_matmul_dx(dYp, Np, m, w.N, w.K, b.Wd, b.G, b.At, set.r, b.plan, dX, s);
+    prep.A = set.A;
+    prep.At = b.At;
+    prep.Wd = b.Wd;
   }
-  if (e == hipSuccess && (dA || dB)) e = launch_ad_grads(X, dY, b.G, T, w.N, w.K, set, b.plan, dA, dB, s);
+  hipError_t e = launch_ad_prepare(prep, s);
+  if (e == hipSuccess && dB && !T) {
+    e = launch_ad_down(X, m, w.K, set.A, set, b.plan, b.part, b.T, s);
+    T = b.T;
+  }
+  if (e == hipSuccess && (dX || dA)) e = launch_ad_down(dYp, m, Np, b.Bt, set, b.plan, b.part, b.G, s);
+  if (e == hipSuccess && dX) e = launch_ad_matmul_dx(dYp, Np, m, w.N, w.K, b.Wd, b.G, b.At, set.r, b.plan, b.tiles, dX, s);
+  if (e == hipSuccess && (dA || dB)) e = launch_ad_grads(X, dY, b.G, T, m, w.N, w.K, set, b.plan, dA, dB, s);
   return from_hip(e);
 }
 

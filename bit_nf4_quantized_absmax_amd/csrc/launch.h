@@ -325,7 +325,7 @@ struct AdapterSet {
   int n;
   int r;
 };
-// The sorted order of the tokens (see k_ad_sort).
+// The sorted order of the tokens (see ad_sort).
 struct AdPlan {
   int *perm;
   int *who;
@@ -340,22 +340,35 @@ inline int64_t ad_tiles_max(int64_t M, int64_t n) { return (M + 31) / 32 + (M < 
 size_t ad_small_ws_bytes(int M, int N, int K, int r);
 hipError_t launch_ad_small(const uint16_t *X, int M, const NF4View &w, const AdapterSet &ad, uint16_t *T, uint16_t *Y, void *ws,
                            hipStream_t s);
-hipError_t launch_ad_sort(const AdapterSet &ad, int M, const AdPlan &p, hipStream_t s);
-// out [M, r] = scale_a P Q_a^T, P [M, D], Q [n, r, D], D % 64 == 0; zeros for tokens without an adapter.
-hipError_t launch_ad_down(const uint16_t *P, int M, int D, const uint16_t *Q, const AdapterSet &ad, const AdPlan &p, uint16_t *out,
-                          hipStream_t s);
+// The order, and with Wd the dequantized weight, with At and Bt the adapters transposed
+// (Bt's rows filled up to Np), with dYp dY's rows filled up to Np.
+struct AdPrepare {
+  const int64_t *index;
+  AdPlan plan;
+  NF4View w;
+  uint16_t *Wd;
+  const uint16_t *A, *B, *dY;
+  uint16_t *At, *Bt, *dYp;
+  int M, n, r, Np;
+  int deq, trA, trB, pad;   // workgroups of each part (set by the launch)
+};
+hipError_t launch_ad_prepare(AdPrepare a, hipStream_t s);
+// out [M, r] = scale_a P Q_a^T, P [M, D], Q [n, r, D], D % 64 == 0; zeros for tokens
+// without an adapter; part: [ad_down_splits][M][r].
+constexpr int kAdSplits = 8;
+int ad_down_splits(int64_t M, int64_t D, int n);
+hipError_t launch_ad_down(const uint16_t *P, int M, int D, const uint16_t *Q, const AdapterSet &ad, const AdPlan &p, float *part,
+                          uint16_t *out, hipStream_t s);
+// part: ad_matmul_part_floats of the product's M, columns and contraction (K, or Np).
+size_t ad_matmul_part_floats(int64_t M, int64_t cols, int64_t Kc);
 // Y [M, N] = X Wd^T + T B_a^T; dX [M, K] = dY Wd + G A_a with At [n, K, r] and dY's
 // rows filled up to Np, a multiple of 64, with zeros.
 hipError_t launch_ad_matmul_fwd(const uint16_t *X, int M, int N, int K, const uint16_t *Wd, const uint16_t *T, const uint16_t *B, int r,
-                                const AdPlan &p, uint16_t *Y, hipStream_t s);
+                                const AdPlan &p, float *part, uint16_t *Y, hipStream_t s);
 hipError_t launch_ad_matmul_dx(const uint16_t *dY, int Np, int M, int N, int K, const uint16_t *Wd, const uint16_t *G,
-                               const uint16_t *At, int r, const AdPlan &p, uint16_t *dX, hipStream_t s);
-// n matrices [rows, cols] -> [cols, pitch], pitch >= rows, zeros behind.
-hipError_t launch_ad_transpose(const uint16_t *src, int n, int rows, int cols, int pitch, uint16_t *dst, hipStream_t s);
-// dst [M, pitch] = src [M, cols], zeros behind; multiples of 8.
-hipError_t launch_ad_pad(const uint16_t *src, int M, int cols, int pitch, uint16_t *dst, hipStream_t s);
+                               const uint16_t *At, int r, const AdPlan &p, float *part, uint16_t *dX, hipStream_t s);
 // dA [n, r, K] and dB [n, N, r], either nullable.
-hipError_t launch_ad_grads(const uint16_t *X, const uint16_t *dY, const uint16_t *G, const uint16_t *T, int N, int K, const AdapterSet &ad,
+hipError_t launch_ad_grads(const uint16_t *X, const uint16_t *dY, const uint16_t *G, const uint16_t *T, int M, int N, int K, const AdapterSet &ad,
                            const AdPlan &p, uint16_t *dA, uint16_t *dB, hipStream_t s);
 
 // ---- cross entropy through the output head ------------------------------------------------
