@@ -13,6 +13,10 @@ from .ops import NF4Weight, _mat, _need, _out, _ptr, _stream, _workspace
 
 _SAME_DEVICE = contextlib.nullcontext()
 
+# The current device without torch.cuda's look at its own state first (0.1 us a
+# call instead of 0.6); not part of the documented interface, as ops._raw_stream.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
 
 def _on(device, *tensors):
     """The context in which work on `device` is launched; every tensor given (or None) has to be there."""
@@ -20,7 +24,7 @@ def _on(device, *tensors):
     for t in tensors:
         if t is not None and t.get_device() != index:
             raise ValueError("tensors on different devices: %s and %s" % (device, t.device))
-    return _SAME_DEVICE if torch.cuda.current_device() == index else torch.cuda.device(device)
+    return _SAME_DEVICE if _current_device() == index else torch.cuda.device(device)
 
 
 def _checks(X, w, A, B, scale, index):

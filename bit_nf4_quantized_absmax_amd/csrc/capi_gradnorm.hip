@@ -63,18 +63,21 @@ int run(int32_t count, const qlora_grad_tensor *t, int32_t groups, const float *
   if (need > 0 && (!ws || !aligned(ws, 16) || ws_bytes < need)) return QLORA_ERR_WORKSPACE;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   GradList list;
-  int n = 0, base = 0;
+  list.n = 0;
   int64_t first = 0;
+  bool lead = true;
   hipError_t e = hipSuccess;
   for (int32_t i = 0; i < count && e == hipSuccess; ++i) {
     if (t[i].count > 0) {
-      list.t[n++] = GradTensor{t[i].x, t[i].out, t[i].count, static_cast<int>(t[i].type), static_cast<int>(first)};
-      first += (t[i].count / groups + plan.chunk - 1) / plan.chunk;
+      const int64_t part = t[i].count / groups;
+      list.t[list.n++] = GradTensor{t[i].x, max_norm ? t[i].out : nullptr, part, static_cast<int>(t[i].type), static_cast<int>(first)};
+      first += (part + plan.chunk - 1) / plan.chunk;
     }
-    if (n > 0 && (n == kGradList || i + 1 == count)) {
-      e = launch_grad_chunks(list, n, g, base, s);
-      base += n;
-      n = 0;
+    if (list.n > 0 && (list.n == kGradList || i + 1 == count)) {
+      list.chunks = static_cast<int>(first) - list.t[0].first;
+      e = launch_grad_squares(list, g, lead, s);
+      lead = false;
+      list.n = 0;
     }
   }
   if (e == hipSuccess) e = launch_grad_norm(g, max_norm, norm, s);

@@ -13,8 +13,9 @@
 //    multiply-add a value keeps up with the stream (4 T of either a second).
 //  * A workgroup takes a chunk of one part of one tensor and leaves one partial
 //    sum; the order of all sums is fixed, so results repeat.  The list of
-//    tensors is an argument of k_grad_chunks, a workgroup a tensor, which writes
-//    the table of chunks that the other kernels read: nothing is copied from the host.
+//    tensors is an argument of the launch that sums them (kGradList of them, one
+//    launch after the other), which also writes the table of chunks that the
+//    clipping kernel reads: nothing is copied from the host.
 //  * The clipping kernel's workgroups each add up their group's partial sums
 //    (2048 or so, from L2): one launch less.  Where nothing has to change and the
 //    result goes where it came from, a workgroup ends there.
@@ -127,38 +128,38 @@ __device__ __forceinline__ void scaled(const T *x, T *y, int64_t count, Factor f
 
 }  // namespace
 
-// The chunks of tensor blockIdx.x: entry c of group g is chunk c % per of its part g.
-__global__ __launch_bounds__(kGnThreads) void k_grad_chunks(const GradList l, GradPlan p, int base) {
-  const GradTensor t = l.t[blockIdx.x];
-  const int64_t part = t.count / p.groups;
-  const int per = static_cast<int>((part + p.chunk - 1) / p.chunk);
-  const int64_t width = t.type == 0 ? 4 : 2;
-  for (int i = threadIdx.x; i < per * p.groups; i += kGnThreads) {
-    const int g = i / per, c = i % per;
-    const int64_t at = g * part + static_cast<int64_t>(c) * p.chunk;
-    GradChunk k;
-    k.x = static_cast<const char *>(t.x) + at * width;
-    k.y = static_cast<char *>(t.y) + at * width;
-    k.count = static_cast<int>(min(static_cast<int64_t>(p.chunk), part - static_cast<int64_t>(c) * p.chunk));
-    k.type = t.type;
-    k.group = g;
-    k.lead = base + blockIdx.x == 0 && c == 0;
-    p.table[static_cast<int64_t>(g) * p.stride + t.first + c] = k;
-  }
-}
-
-__global__ __launch_bounds__(kGnThreads) void k_grad_squares(GradPlan p) {
+// One list's chunks: workgroup (group, chunk of the list's share of a group) finds its
+// tensor, writes its entry of the table and its sum of squares.
+__global__ __launch_bounds__(kGnThreads) void k_grad_squares(const GradList l, GradPlan p, int lead) {
   __shared__ double sh[kGnThreads / 64];
-  const GradChunk k = p.table[blockIdx.x];
+  const int g = blockIdx.x / l.chunks, c = l.t[0].first + blockIdx.x % l.chunks;
+  int lo = 0, hi = l.n - 1;                      // the last tensor whose first chunk is not behind this one
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (l.t[mid].first <= c)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  const GradTensor t = l.t[lo];
+  const int64_t part = t.part, in = static_cast<int64_t>(c - t.first) * p.chunk;
+  const int64_t at = g * part + in;
+  const int count = static_cast<int>(min(static_cast<int64_t>(p.chunk), part - in));
+  const int64_t place = static_cast<int64_t>(g) * p.stride + c;
+  if (threadIdx.x == 0 && t.y) {
+    const int64_t bytes = at * (t.type == 0 ? 4 : 2);
+    p.table[place] = GradChunk{static_cast<const char *>(t.x) + bytes, static_cast<char *>(t.y) + bytes, count, t.type, g,
+                               lead && c == 0 ? 1 : 0};
+  }
   double s;
-  if (k.type == 0)
-    s = squares(static_cast<const float *>(k.x), k.count);
-  else if (k.type == 1)
-    s = squares(static_cast<const uint16_t *>(k.x), k.count);
+  if (t.type == 0)
+    s = squares(static_cast<const float *>(t.x) + at, count);
+  else if (t.type == 1)
+    s = squares(static_cast<const uint16_t *>(t.x) + at, count);
   else
-    s = squares(static_cast<const _Float16 *>(k.x), k.count);
+    s = squares(static_cast<const _Float16 *>(t.x) + at, count);
   s = block_sum(s, sh);
-  if (threadIdx.x == 0) p.sums[blockIdx.x] = s;
+  if (threadIdx.x == 0) p.sums[place] = s;
 }
 
 __device__ __forceinline__ double group_norm(const GradPlan &p, int group, double *sh) {
@@ -190,20 +191,14 @@ __global__ __launch_bounds__(kGnThreads) void k_grad_clip(GradPlan p, float max_
 }
 
 // ---------------------------------------------------------------------------
-hipError_t launch_grad_chunks(const GradList &l, int n, const GradPlan &p, int base, hipStream_t s) {
-  hipLaunchKernelGGL(k_grad_chunks, dim3(n), dim3(kGnThreads), 0, s, l, p, base);
+hipError_t launch_grad_squares(const GradList &l, const GradPlan &p, bool lead, hipStream_t s) {
+  hipLaunchKernelGGL(k_grad_squares, dim3(l.chunks * p.groups), dim3(kGnThreads), 0, s, l, p, lead ? 1 : 0);
   return hipGetLastError();
 }
 
 hipError_t launch_grad_norm(const GradPlan &p, const float *max_norm, float *norm, hipStream_t s) {
-  const int chunks = p.stride * p.groups;
-  if (chunks > 0) {
-    hipLaunchKernelGGL(k_grad_squares, dim3(chunks), dim3(kGnThreads), 0, s, p);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  if (max_norm && chunks > 0)
-    hipLaunchKernelGGL(k_grad_clip, dim3(chunks), dim3(kGnThreads), 0, s, p, *max_norm, norm);
+  if (max_norm && p.stride > 0)
+    hipLaunchKernelGGL(k_grad_clip, dim3(p.stride * p.groups), dim3(kGnThreads), 0, s, p, *max_norm, norm);
   else
     hipLaunchKernelGGL(k_grad_norm, dim3(p.groups), dim3(kGnThreads), 0, s, p, norm);
   return hipGetLastError();

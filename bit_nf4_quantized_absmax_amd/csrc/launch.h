@@ -416,14 +416,15 @@ hipError_t launch_head_dw(const uint16_t *Xc, int M, const uint16_t *W, int K, i
 // ---- norm of many tensors and clipping by it ------------------------------------------
 struct GradTensor {
   const void *x;
-  void *y;
-  int64_t count;
+  void *y;         // nullptr where only the norm is asked for
+  int64_t part;    // elements of a group
   int type;        // 0 fp32, 1 bf16, 2 fp16
   int first;       // its first chunk within a group
 };
 constexpr int kGradList = 120;   // tensors of one launch's list: 4 KB of arguments hold 128
 struct GradList {
   GradTensor t[kGradList];
+  int n, chunks;   // tensors; chunks of a group
 };
 struct GradChunk {
   const void *x;
@@ -440,8 +441,8 @@ struct GradPlan {
   int stride;         // chunks of a group
   int chunk;          // elements of a chunk
 };
-// Chunks of tensors base .. base + n - 1 of the call into the table.
-hipError_t launch_grad_chunks(const GradList &l, int n, const GradPlan &p, int base, hipStream_t s);
+// The sums of a list's chunks, and their entries in the table; lead: the call's first list.
+hipError_t launch_grad_squares(const GradList &l, const GradPlan &p, bool lead, hipStream_t s);
 // norm [groups]; max_norm (nullable): clipped into every y.
 hipError_t launch_grad_norm(const GradPlan &p, const float *max_norm, float *norm, hipStream_t s);
 
