@@ -244,14 +244,20 @@ constexpr int kDtWaves = 4;
 constexpr int kDtThreads = kDtWaves * 64;
 constexpr int kDtSlots = 3;
 
-template <int kJB>
-constexpr int dt_slot() { return (1 + kJB) * 4096; }   // 32 rows of P, 32 kJB rows of Q, 128 bytes each
+template <int kQ>
+constexpr int dt_slot() { return (4 + kQ) * 1024; }   // 32 rows of P, 8 kQ rows of Q, 128 bytes each
 }  // namespace
 
-template <int kJB>
+// kQ: adapter rows / 8 that are fetched (1 to 4: all of them; 8: 64 at a time, those past r repeated).
+template <int kQ>
 __global__ __launch_bounds__(kDtThreads) void k_ad_down_tiles(const uint16_t *__restrict__ P, int D, const uint16_t *__restrict__ Q,
                                                               int r, int M, int splits, AdPlan p, float *__restrict__ part) {
-  __shared__ __attribute__((aligned(16))) uint8_t smem[kDtWaves][kDtSlots][dt_slot<kJB>()];
+  constexpr int kJB = kQ > 4 ? 2 : 1;
+  // the waves' sums at the end take 4 kJB KB; the operands of rows past 8 kQ are read from what follows a slot and not stored
+  constexpr int kPad = 4096 * (1 + kJB) - dt_slot<kQ>();
+  constexpr int kWaveLds = kDtSlots * dt_slot<kQ>() + kPad;
+  static_assert(kWaveLds >= 4096 * kJB, "a wave's sums");
+  __shared__ __attribute__((aligned(16))) uint8_t smem[kDtWaves][kWaveLds];
   if (static_cast<int>(blockIdx.x) >= p.ntile[0]) return;
   const int4 tl = p.tile[blockIdx.x];
   const int a = tl.x, p0 = tl.y, cnt = tl.z;
@@ -265,7 +271,7 @@ __global__ __launch_bounds__(kDtThreads) void k_ad_down_tiles(const uint16_t *__
   const int n_i = wave < steps ? (steps - wave + kDtWaves - 1) / kDtWaves : 0;
 
   // 8 rows of 128 bytes a DMA instruction; the chunk that belongs at a lane's position.
-  uint32_t po[4], qo[4 * kJB];
+  uint32_t po[4], qo[kQ];
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const int row = 8 * u + (lane >> 3);
@@ -273,21 +279,21 @@ __global__ __launch_bounds__(kDtThreads) void k_ad_down_tiles(const uint16_t *__
     po[u] = static_cast<uint32_t>(p.perm[p0 + min(row, cnt - 1)]) * D * 2 + 16 * chunk;
   }
 #pragma unroll
-  for (int u = 0; u < 4 * kJB; ++u) {
+  for (int u = 0; u < kQ; ++u) {
     const int row = 8 * u + (lane >> 3);
     const int chunk = (lane & 7) ^ ((row & 7) ^ ((row >> 3) & 1));
     qo[u] = static_cast<uint32_t>(min(j0 + row, r - 1)) * D * 2 + 16 * chunk;   // rows past r: columns never stored
   }
-  const uint32_t ring = lds_addr(smem[wave][0]);
+  const uint32_t ring = lds_addr(smem[wave]);
   auto issue = [&](int i, int slot) __attribute__((always_inline)) {
     const int64_t k = 64 * (first + wave + static_cast<int64_t>(kDtWaves) * i);
-    const uint32_t dst = __builtin_amdgcn_readfirstlane(ring + slot * dt_slot<kJB>());
+    const uint32_t dst = __builtin_amdgcn_readfirstlane(ring + slot * dt_slot<kQ>());
 #pragma unroll
     for (int u = 0; u < 4; ++u) dma16(P + k, po[u], dst + u * 1024);
 #pragma unroll
-    for (int u = 0; u < 4 * kJB; ++u) dma16(Qa + k, qo[u], dst + 4096 + u * 1024);
+    for (int u = 0; u < kQ; ++u) dma16(Qa + k, qo[u], dst + 4096 + u * 1024);
   };
-  constexpr int kDma = 4 + 4 * kJB;
+  constexpr int kDma = 4 + kQ;
   f32x16_t acc[kJB];
 #pragma unroll
   for (int jb = 0; jb < kJB; ++jb)
@@ -310,7 +316,7 @@ __global__ __launch_bounds__(kDtThreads) void k_ad_down_tiles(const uint16_t *__
       __builtin_amdgcn_s_waitcnt(wait_imm(0, 15));
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
     __builtin_amdgcn_sched_barrier(0);
-    const uint8_t *ps = smem[wave][slot], *qs = ps + 4096;
+    const uint8_t *ps = smem[wave] + slot * dt_slot<kQ>(), *qs = ps + 4096;
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       const bf16x8_t x = *reinterpret_cast<const bf16x8_t *>(ps + swz128(lr, 2 * s + lh));
@@ -327,7 +333,7 @@ __global__ __launch_bounds__(kDtThreads) void k_ad_down_tiles(const uint16_t *__
     __builtin_amdgcn_sched_barrier(0);
   }
   // lane: column (adapter row) lr of block jb, token 8 (e / 4) + 4 lh + e % 4.
-  float *red = reinterpret_cast<float *>(smem[wave][0]);
+  float *red = reinterpret_cast<float *>(smem[wave]);
 #pragma unroll
   for (int jb = 0; jb < kJB; ++jb)
 #pragma unroll
@@ -336,9 +342,9 @@ __global__ __launch_bounds__(kDtThreads) void k_ad_down_tiles(const uint16_t *__
   for (int idx = threadIdx.x; idx < 32 * 8 * kJB; idx += kDtThreads) {
     const int row = idx / (8 * kJB), c = idx % (8 * kJB), j = j0 + 4 * c;
     if (row >= cnt || j >= r) continue;          // r % 8 == 0
-    f32x4_t v = reinterpret_cast<const f32x4_t *>(smem[0][0])[row * 8 * kJB + c];
+    f32x4_t v = reinterpret_cast<const f32x4_t *>(smem[0])[row * 8 * kJB + c];
 #pragma unroll
-    for (int w = 1; w < kDtWaves; ++w) v += reinterpret_cast<const f32x4_t *>(smem[w][0])[row * 8 * kJB + c];
+    for (int w = 1; w < kDtWaves; ++w) v += reinterpret_cast<const f32x4_t *>(smem[w])[row * 8 * kJB + c];
     *reinterpret_cast<f32x4_t *>(part + (static_cast<int64_t>(split) * M + p.perm[p0 + row]) * r + j) = v;
   }
 }
@@ -672,10 +678,14 @@ int ad_down_splits(int64_t M, int64_t D, int n) {
 hipError_t launch_ad_down(const uint16_t *P, int M, int D, const uint16_t *Q, const AdapterSet &ad, const AdPlan &p, float *part,
                           uint16_t *out, hipStream_t s) {
   const int tiles = static_cast<int>(ad_tiles_max(M, ad.n)), splits = ad_down_splits(M, D, ad.n);
-  if (ad.r <= 32)
-    hipLaunchKernelGGL(k_ad_down_tiles<1>, dim3(tiles, 1, splits), dim3(kDtThreads), 0, s, P, D, Q, ad.r, M, splits, p, part);
-  else
-    hipLaunchKernelGGL(k_ad_down_tiles<2>, dim3(tiles, (ad.r + 63) / 64, splits), dim3(kDtThreads), 0, s, P, D, Q, ad.r, M, splits, p, part);
+  const dim3 grid(tiles, (ad.r + 63) / 64, splits), th(kDtThreads);
+  switch (ad.r <= 32 ? ad.r / 8 : 8) {
+    case 1: hipLaunchKernelGGL(k_ad_down_tiles<1>, grid, th, 0, s, P, D, Q, ad.r, M, splits, p, part); break;
+    case 2: hipLaunchKernelGGL(k_ad_down_tiles<2>, grid, th, 0, s, P, D, Q, ad.r, M, splits, p, part); break;
+    case 3: hipLaunchKernelGGL(k_ad_down_tiles<3>, grid, th, 0, s, P, D, Q, ad.r, M, splits, p, part); break;
+    case 4: hipLaunchKernelGGL(k_ad_down_tiles<4>, grid, th, 0, s, P, D, Q, ad.r, M, splits, p, part); break;
+    default: hipLaunchKernelGGL(k_ad_down_tiles<8>, grid, th, 0, s, P, D, Q, ad.r, M, splits, p, part); break;
+  }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t quads = static_cast<int64_t>(M) * ad.r / 4;

@@ -46,8 +46,8 @@ size_t carve(void *ws, int64_t M, int64_t V, int64_t K, int32_t pass, Parts *p) 
   p->h.list = c.take<int>(M);
   p->h.tgt = c.take<int>(M);
   p->h.count = c.take<int>(1);
-  p->Xc = c.take<uint16_t>(round_up(M, 64) * K);
   if (pass == QLORA_HEAD_DW) {
+    p->Xc = c.take<uint16_t>(round_up(M, 64) * K);
     p->words = piece_words(round_up(M, 64), V, K, kPieceE);
     p->Zt = c.take<uint16_t>(p->words * round_up(M, 64));
     return c.used;
@@ -93,21 +93,19 @@ int qlora_head_cross_entropy(const uint16_t *X, int64_t M, const uint16_t *W, in
   if (!ws || !aligned(ws, 16) || ws_bytes < need) return QLORA_ERR_WORKSPACE;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const int m = static_cast<int>(M), k = static_cast<int>(K), v = static_cast<int>(V);
-  const bool small = M <= kHeadSmall;
+  const bool small = M <= kHeadSmall, at_once = small && !dX && p.words >= V;
   hipError_t e = hipSuccess;
-  if (!small) {
-    e = launch_head_rows(target, m, v, p.h, s);
-    if (e == hipSuccess) e = launch_head_gather(X, m, k, p.h, p.Xc, s);
-  }
+  if (!small) e = launch_head_rows(target, m, v, p.h, s);
   for (int64_t v0 = 0; v0 < V && e == hipSuccess; v0 += p.words) {
     const int words = static_cast<int>(std::min<int64_t>(p.words, V - v0));
     p.pc.pitch = static_cast<int>(round_up(words, 64));
     if (small)
-      e = launch_head_small_piece(X, target, m, W, v, k, static_cast<int>(v0), words, v0 == 0, p.h, p.pc, p.cut, dX ? p.C : nullptr, s);
+      e = launch_head_small_piece(X, target, m, W, v, k, static_cast<int>(v0), words, v0 == 0, p.h, p.pc, p.cut, dX ? p.C : nullptr,
+                                  at_once ? loss : nullptr, at_once ? lse : nullptr, s);
     else
-      e = launch_head_piece(p.Xc, m, W, v, k, static_cast<int>(v0), words, v0 == 0, p.h, p.pc, p.cut, dX ? p.C : nullptr, s);
+      e = launch_head_piece(X, m, W, v, k, static_cast<int>(v0), words, v0 == 0, p.h, p.pc, p.cut, dX ? p.C : nullptr, s);
   }
-  if (e == hipSuccess) e = launch_head_finish(W, M, k, weight, p.h, p.cut, p.C, loss, lse, dX, dX ? 1 + dx_fp32 : 0, s);
+  if (e == hipSuccess && !at_once) e = launch_head_finish(W, M, k, weight, p.h, p.cut, p.C, loss, lse, dX, dX ? 1 + dx_fp32 : 0, s);
   return from_hip(e);
 }
 

@@ -19,7 +19,8 @@
 //    (p_t - 1) W_t is added in fp32, where a rounded p_t near 1 would lose both.  E's rounding to bf16 is
 //    the operand type of the second product; its error is that of one output rounding, averaged over words.
 //  * Rows without a target take no part: the rows that have one are listed
-//    first (k_head_rows) and copied together (k_head_gather).
+//    first (k_head_rows), and the DMA gathers them; for dW, where they are the
+//    contraction, they are copied together (k_head_gather).
 //  * dW, where the head is tuned as well, makes its logits a second time, for
 //    dz needs the whole row's sum: dz^T piece by piece in bf16 (k_head_dz), then
 //    dz^T X (k_head_dw).
@@ -53,14 +54,15 @@ __device__ __forceinline__ float shift_of(float from, float to) {
 }
 
 // Splits of the second product's words: the fewest that come within 2 % of the
-// least time, in rounds of the workgroups that the chip holds at once.
+// least time, in rounds of the workgroups that the chip holds at once and the
+// writing and reading of a split's sums (cut.cost of a round of the whole words).
 // The number of rows that count is known on the device alone.  slots 0: all of them.
 __host__ __device__ __forceinline__ int splits_for(int tiles, const HeadCut &cut) {
   if (cut.slots == 0) return cut.most;
   int best = 1;
   float least = 3.4e38f;
   for (int s = 1; s <= cut.most; ++s) {
-    const float t = static_cast<float>((tiles * s + cut.slots - 1) / cut.slots) / s;
+    const float t = static_cast<float>((tiles * s + cut.slots - 1) / cut.slots) / s + cut.cost * tiles * s;
     if (t < 0.98f * least) {
       least = t;
       best = s;
@@ -68,6 +70,21 @@ __host__ __device__ __forceinline__ int splits_for(int tiles, const HeadCut &cut
   }
   return best;
 }
+
+// A row's loss and log-sum-exp (ref + rest) from the sum s of all words but the
+// target at a reference (0: there are none) and the target's logit; inv: 1 / the whole sum at that reference.
+struct RowResult {
+  float loss, ref, rest, inv;
+  __device__ __forceinline__ RowResult(double s, double zt, float at) : ref(at) {
+    const double u = static_cast<double>(at) - zt;
+    double l = s == 0.0 ? 0.0 : u > 0.0 ? u + log(s + exp(-u)) : log1p(s * exp(u));
+    if (!(fabs(zt) < INFINITY) || !(s < INFINITY)) l = NAN;
+    inv = s == 0.0 ? 0.f : static_cast<float>(exp(u - l));
+    if (s == 0.0 || zt > at + kBucket) ref = ref_of(static_cast<float>(zt));
+    rest = static_cast<float>(l + (zt - ref));
+    loss = static_cast<float>(l);
+  }
+};
 
 // *at = v, or f *at + v.
 __device__ __forceinline__ void add_to(f32x4_t *at, f32x4_t v, int first, float f) {
@@ -87,30 +104,41 @@ __device__ __forceinline__ float swap_halves(float v) { return __shfl_xor(v, 32,
 // Rows with a target, in order: list [count] of row numbers, tgt [count], place
 // [M] of a row in the list (-1: none).  One workgroup.
 __global__ __launch_bounds__(1024) void k_head_rows(const int64_t *__restrict__ target, int M, int V, HeadRows h) {
-  __shared__ int wsum[16];
+  __shared__ int wsum[2][16];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  constexpr int kBatch = 8;                          // targets of a thread in flight
   int base = 0;
-  for (int64_t m0 = 0; m0 < M; m0 += 1024) {
-    const int64_t m = m0 + threadIdx.x;
-    const int64_t t = m < M ? target[m] : -1;
-    const bool real = t >= 0 && t < V;
-    const uint64_t mask = __ballot(real);
-    if (lane == 0) wsum[wave] = __popcll(mask);
-    __syncthreads();
-    int before = base, all = 0;
-    for (int w = 0; w < 16; ++w) {
-      if (w < wave) before += wsum[w];
-      all += wsum[w];
+  for (int64_t b0 = 0; b0 < M; b0 += 1024 * kBatch) {
+    int64_t t[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int64_t m = b0 + 1024 * u + threadIdx.x;
+      t[u] = target[m < M ? m : M - 1];
     }
-    const int at = before + static_cast<int>(__popcll(mask & ((uint64_t{1} << lane) - 1)));
-    if (m < M) h.place[m] = real ? at : -1;
-    if (real) {
-      h.list[at] = static_cast<int>(m);
-      h.tgt[at] = static_cast<int>(t);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int64_t m = b0 + 1024 * u + threadIdx.x;
+      if (b0 + 1024 * u >= M) break;                 // uniform
+      const bool real = m < M && t[u] >= 0 && t[u] < V;
+      const uint64_t mask = __ballot(real);
+      if (lane == 0) wsum[u & 1][wave] = __popcll(mask);
+      __syncthreads();                               // one a round: the sums alternate
+      int before = base, all = 0;
+#pragma unroll
+      for (int w = 0; w < 16; ++w) {
+        const int x = wsum[u & 1][w];
+        if (w < wave) before += x;
+        all += x;
+      }
+      const int at = before + static_cast<int>(__popcll(mask & ((uint64_t{1} << lane) - 1)));
+      if (m < M) h.place[m] = real ? at : -1;
+      if (real) {
+        h.list[at] = static_cast<int>(m);
+        h.tgt[at] = static_cast<int>(t[u]);
+      }
+      base += all;
     }
-    base += all;
-    __syncthreads();
   }
   if (threadIdx.x == 0) h.count[0] = base;
 }
@@ -133,7 +161,7 @@ __global__ __launch_bounds__(256) void k_head_gather(const uint16_t *__restrict_
 // among them, and with kE the matrix E [row][pitch], pitch = words filled up to 64,
 // zero there and at the target.
 template <class S, bool kE>
-__global__ __launch_bounds__(S::kThreads, 2) void k_head_logits(const uint16_t *__restrict__ Xc, const uint16_t *__restrict__ W, int K,
+__global__ __launch_bounds__(S::kThreads, 2) void k_head_logits(const uint16_t *__restrict__ X, const uint16_t *__restrict__ W, int K,
                                                                   int v0, int words, HeadRows h, HeadPiece pc) {
   using namespace gemm16;
   __shared__ __attribute__((aligned(16))) uint8_t smem[S::kLds];
@@ -142,8 +170,8 @@ __global__ __launch_bounds__(S::kThreads, 2) void k_head_logits(const uint16_t *
   if (!place(blockIdx.x, (count + S::kBM - 1) / S::kBM, (words + S::kBN - 1) / S::kBN, tr, tc)) return;
   const int m0 = tr * S::kBM, c0 = tc * S::kBN;
   Acc<S> acc;
-  tile<S, false>(smem, Xc, K, [&](int row) { return min(m0 + row, count - 1); }, W + static_cast<int64_t>(v0) * K, K, c0, words - 1, 0,
-              K / kBK, acc);
+  tile<S, false>(smem, X, K, [&](int row) { return h.list[min(m0 + row, count - 1)]; }, W + static_cast<int64_t>(v0) * K, K, c0,
+                 words - 1, 0, K / kBK, acc);
   const Place<S> w;
   const int lr = w.lr, lh = w.lh;
   const int cw = c0 + w.col0();                       // first word (of the piece) of this wave
@@ -206,13 +234,23 @@ __global__ __launch_bounds__(S::kThreads, 2) void k_head_logits(const uint16_t *
 // brought to this one, in a second pass that hardly any row needs.  Workgroup:
 // kRows rows, 256 / kRows threads share a row's groups.
 template <int kRows>
-__global__ __launch_bounds__(256) void k_head_refs(HeadRows h, HeadPiece pc, int groups, int first, int scale_e) {
+__global__ __launch_bounds__(256) void k_head_refs(HeadRows h, HeadPiece pc, int groups, int first, int scale_e, float *__restrict__ loss,
+                                                   float *__restrict__ lse) {
   constexpr int kShare = 256 / kRows;
   __shared__ float sRef[4][kRows], sLow[4][kRows];
   __shared__ double sSum[4][kRows];
   const int lrow = threadIdx.x % kRows, w = threadIdx.x / kRows;
-  const int row = blockIdx.x * kRows + lrow, count = h.count[0];
-  if (static_cast<int>(blockIdx.x) * kRows >= count) return;
+  const int count = h.count[0];
+  int row = blockIdx.x * kRows + lrow;
+  if (loss) {                                        // kRows == 1: a workgroup a row of X
+    row = h.place[blockIdx.x];
+    if (row < 0) {
+      if (threadIdx.x == 0) loss[blockIdx.x] = lse[2 * blockIdx.x] = lse[2 * blockIdx.x + 1] = 0.f;
+      return;
+    }
+  } else if (static_cast<int>(blockIdx.x) * kRows >= count) {
+    return;
+  }
   const bool live = row < count;
   const float2 *part = pc.part + (live ? row : 0);
   const int64_t pitch = pc.rows;
@@ -301,9 +339,17 @@ __global__ __launch_bounds__(256) void k_head_refs(HeadRows h, HeadPiece pc, int
   __syncthreads();                                   // all threads of the row have read its state
   if (w == 0 && live) {
     const float f = old == 0.0 ? 0.f : old_ref == top ? 1.f : exp_f(old_ref - top);
-    h.ref[row] = top;
-    h.sum[row] = old * f + (sum == 0.0 || new_ref == top ? sum : sum * exp_f(new_ref - top));
-    h.factor[row] = f;
+    const double all = old * f + (sum == 0.0 || new_ref == top ? sum : sum * exp_f(new_ref - top));
+    if (loss) {
+      const RowResult r(all, h.zt[row], top);
+      loss[blockIdx.x] = r.loss;
+      lse[2 * blockIdx.x] = r.ref;
+      lse[2 * blockIdx.x + 1] = r.rest;
+    } else {
+      h.ref[row] = top;
+      h.sum[row] = all;
+      h.factor[row] = f;
+    }
   }
 }
 
@@ -606,15 +652,11 @@ __global__ __launch_bounds__(256) void k_head_finish(const uint16_t *__restrict_
   const int at = h.place[m];
   float l = 0.f, lg = 0.f, ref = 0.f, inv = 0.f;
   if (at >= 0) {
-    const double s = h.sum[at], zt = h.zt[at];      // all words but the target, at ref; 0: there are none
-    ref = h.ref[at];
-    const double u = static_cast<double>(ref) - zt;
-    double loss64 = s == 0.0 ? 0.0 : u > 0.0 ? u + log(s + exp(-u)) : log1p(s * exp(u));
-    if (!(fabs(zt) < INFINITY) || !(s < INFINITY)) loss64 = NAN;
-    inv = s == 0.0 ? 0.f : static_cast<float>(exp(-(loss64 - u)));   // loss - u = log of the whole sum at ref
-    if (s == 0.0 || zt > ref + kBucket) ref = ref_of(static_cast<float>(zt));
-    lg = static_cast<float>(loss64 + (zt - ref));
-    l = static_cast<float>(loss64);
+    const RowResult r(h.sum[at], h.zt[at], h.ref[at]);
+    l = r.loss;
+    ref = r.ref;
+    lg = r.rest;
+    inv = r.inv;
   }
   if (threadIdx.x == 0 && blockIdx.y == 0) {
     loss[m] = l;
@@ -771,6 +813,7 @@ HeadCut head_cut(int64_t M, int64_t K, int64_t words) {
     c.mid = 0;
     c.bm = c.bn = 1;
     c.slots = 0;
+    c.cost = 0.f;
     const int64_t cols = (K + kSmCols - 1) / kSmCols;
     c.most = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({(M <= 32 ? 512 : 256) / cols, words / 512, 64})));
     return c;
@@ -781,6 +824,8 @@ HeadCut head_cut(int64_t M, int64_t K, int64_t words) {
   c.bm = c.mid ? Mid::kBM : Big::kBM;
   c.bn = c.mid ? Mid::kBN : Big::kBN;
   c.slots = c.mid ? 512 : 256;
+  // a tile's 4 bytes an element out and in at 5 TB/s, against a step of 64 words of a round: 1.7 us (Mid 0.85 of a pair)
+  c.cost = static_cast<float>(c.bm * c.bn * 8 / 5e6) / ((c.mid ? 0.85f : 1.7f) * static_cast<float>((words + 63) / 64));
   // each at least 8 steps of 64 words long, their sums within 512 MB
   c.most = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({32, words / 512, (int64_t{1} << 27) / (M * K)})));
   return c;
@@ -798,15 +843,16 @@ hipError_t launch_head_gather(const uint16_t *X, int M, int K, const HeadRows &h
 }
 
 template <class S, bool kE>
-static hipError_t launch_head_logits(const uint16_t *Xc, int M, const uint16_t *W, int K, int v0, int words, const HeadRows &h,
+static hipError_t launch_head_logits(const uint16_t *X, int M, const uint16_t *W, int K, int v0, int words, const HeadRows &h,
                                      const HeadPiece &pc, hipStream_t s) {
-  hipLaunchKernelGGL((k_head_logits<S, kE>), dim3(tiles_of<S>(M, words)), dim3(S::kThreads), 0, s, Xc, W, K, v0, words, h, pc);
+  hipLaunchKernelGGL((k_head_logits<S, kE>), dim3(tiles_of<S>(M, words)), dim3(S::kThreads), 0, s, X, W, K, v0, words, h, pc);
   return hipGetLastError();
 }
 
 template <int kMB>
 static hipError_t launch_head_small(const uint16_t *X, const int64_t *target, int M, const uint16_t *W, int V, int K, int v0, int words,
-                                    bool first, const HeadRows &h, const HeadPiece &pc, const HeadCut &cut, float *C, hipStream_t s) {
+                                    bool first, const HeadRows &h, const HeadPiece &pc, const HeadCut &cut, float *C, float *loss, float *lse,
+                                    hipStream_t s) {
   const dim3 g((words + kSmWords - 1) / kSmWords), t(kSmThreads);
   if (C)
     hipLaunchKernelGGL((k_head_small<kMB, true>), g, t, 0, s, X, target, M, W, V, K, v0, words, h, pc);
@@ -814,7 +860,7 @@ static hipError_t launch_head_small(const uint16_t *X, const int64_t *target, in
     hipLaunchKernelGGL((k_head_small<kMB, false>), g, t, 0, s, X, target, M, W, V, K, v0, words, h, pc);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(k_head_refs<1>, dim3(M), dim3(256), 0, s, h, pc, (words + 63) / 64, first ? 1 : 0, C ? 1 : 0);
+  hipLaunchKernelGGL(k_head_refs<1>, dim3(M), dim3(256), 0, s, h, pc, (words + 63) / 64, first ? 1 : 0, C ? 1 : 0, loss, lse);
   e = hipGetLastError();
   if (e != hipSuccess || !C) return e;
   hipLaunchKernelGGL(k_head_small_acc<kMB>, dim3((K + kSmCols - 1) / kSmCols * cut.most), t, 0, s, W, V, K, v0, cut, first ? 1 : 0, h, pc, C);
@@ -822,24 +868,31 @@ static hipError_t launch_head_small(const uint16_t *X, const int64_t *target, in
 }
 
 hipError_t launch_head_small_piece(const uint16_t *X, const int64_t *target, int M, const uint16_t *W, int V, int K, int v0, int words,
-                                   bool first, const HeadRows &h, const HeadPiece &pc, const HeadCut &cut, float *C, hipStream_t s) {
+                                   bool first, const HeadRows &h, const HeadPiece &pc, const HeadCut &cut, float *C, float *loss, float *lse,
+                                   hipStream_t s) {
   switch ((M + 15) / 16) {
-    case 1: return launch_head_small<1>(X, target, M, W, V, K, v0, words, first, h, pc, cut, C, s);
-    case 2: return launch_head_small<2>(X, target, M, W, V, K, v0, words, first, h, pc, cut, C, s);
-    case 3: return launch_head_small<3>(X, target, M, W, V, K, v0, words, first, h, pc, cut, C, s);
-    default: return launch_head_small<4>(X, target, M, W, V, K, v0, words, first, h, pc, cut, C, s);
+    case 1: return launch_head_small<1>(X, target, M, W, V, K, v0, words, first, h, pc, cut, C, loss, lse, s);
+    case 2: return launch_head_small<2>(X, target, M, W, V, K, v0, words, first, h, pc, cut, C, loss, lse, s);
+    case 3: return launch_head_small<3>(X, target, M, W, V, K, v0, words, first, h, pc, cut, C, loss, lse, s);
+    default: return launch_head_small<4>(X, target, M, W, V, K, v0, words, first, h, pc, cut, C, loss, lse, s);
   }
 }
 
-hipError_t launch_head_piece(const uint16_t *Xc, int M, const uint16_t *W, int V, int K, int v0, int words, bool first, const HeadRows &h,
+hipError_t launch_head_piece(const uint16_t *X, int M, const uint16_t *W, int V, int K, int v0, int words, bool first, const HeadRows &h,
                              const HeadPiece &pc, const HeadCut &cut, float *C, hipStream_t s) {
   const bool mid = gemm16::use_mid(M, words);
-  hipError_t e = C ? (mid ? launch_head_logits<Mid, true>(Xc, M, W, K, v0, words, h, pc, s)
-                          : launch_head_logits<Big, true>(Xc, M, W, K, v0, words, h, pc, s))
-                   : (mid ? launch_head_logits<Mid, false>(Xc, M, W, K, v0, words, h, pc, s)
-                          : launch_head_logits<Big, false>(Xc, M, W, K, v0, words, h, pc, s));
+  hipError_t e = C ? (mid ? launch_head_logits<Mid, true>(X, M, W, K, v0, words, h, pc, s)
+                          : launch_head_logits<Big, true>(X, M, W, K, v0, words, h, pc, s))
+                   : (mid ? launch_head_logits<Mid, false>(X, M, W, K, v0, words, h, pc, s)
+                          : launch_head_logits<Big, false>(X, M, W, K, v0, words, h, pc, s));
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(k_head_refs<16>, dim3((M + 15) / 16), dim3(256), 0, s, h, pc, (words + 63) / 64, first ? 1 : 0, C ? 1 : 0);
+  // more threads a row while the rows are few (300 rows, 782 groups: 13 us with 16 threads a row)
+  if (M <= 2048)
+    hipLaunchKernelGGL(k_head_refs<4>, dim3((M + 3) / 4), dim3(256), 0, s, h, pc, (words + 63) / 64, first ? 1 : 0, C ? 1 : 0,
+                       nullptr, nullptr);
+  else
+    hipLaunchKernelGGL(k_head_refs<16>, dim3((M + 15) / 16), dim3(256), 0, s, h, pc, (words + 63) / 64, first ? 1 : 0, C ? 1 : 0,
+                       nullptr, nullptr);
   e = hipGetLastError();
   if (e != hipSuccess || !C) return e;
   // workgroups for any number of rows that have a target

@@ -393,6 +393,7 @@ struct HeadPiece {
 struct HeadCut {
   int bm, bn, slots, most;
   int mid;
+  float cost;      // see splits_for
 };
 constexpr int kHeadSmall = 64;   // rows up to which W's bytes count
 HeadCut head_cut(int64_t M, int64_t K, int64_t words);
@@ -400,11 +401,13 @@ hipError_t launch_head_rows(const int64_t *target, int M, int V, const HeadRows 
 // Xc [M filled up to 64, K]
 hipError_t launch_head_gather(const uint16_t *X, int M, int K, const HeadRows &h, uint16_t *Xc, hipStream_t s);
 // Words v0 .. v0 + words - 1; C [cut.most][M][K] fp32, or nullptr without a gradient.
-hipError_t launch_head_piece(const uint16_t *Xc, int M, const uint16_t *W, int V, int K, int v0, int words, bool first, const HeadRows &h,
+hipError_t launch_head_piece(const uint16_t *X, int M, const uint16_t *W, int V, int K, int v0, int words, bool first, const HeadRows &h,
                              const HeadPiece &pc, const HeadCut &cut, float *C, hipStream_t s);
-// M <= kHeadSmall, straight from X and target (it fills in h too).
+// M <= kHeadSmall, straight from X and target (it fills in h too).  loss, lse: where
+// the piece is the whole vocabulary and no gradient is asked for, the results (else nullptr).
 hipError_t launch_head_small_piece(const uint16_t *X, const int64_t *target, int M, const uint16_t *W, int V, int K, int v0, int words,
-                                   bool first, const HeadRows &h, const HeadPiece &pc, const HeadCut &cut, float *C, hipStream_t s);
+                                   bool first, const HeadRows &h, const HeadPiece &pc, const HeadCut &cut, float *C, float *loss, float *lse,
+                                   hipStream_t s);
 // grad 0: none, 1: dX in bf16, 2: in fp32.
 hipError_t launch_head_finish(const uint16_t *W, int64_t M, int K, const float *weight, const HeadRows &h, const HeadCut &cut, const float *C,
                               float *loss, float *lse, void *dX, int grad, hipStream_t s);

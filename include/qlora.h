@@ -671,7 +671,7 @@ int qlora_distill(const qlora_logits *l, const qlora_teacher *t, const float *we
  * T and G are rounded to bf16 between their products, as in qlora_linear_fwd; those of a
  * token without an adapter are 0.  Tokens need no order.  What one adapter or token holds,
  * NaN and infinities included, reaches no other token's outputs and no other
- * adapter's gradients.  Sums are fp32 and in a fixed order. */
+ * adapter's gradients.  Sums are fp32 and in a fixed order.  Outputs overlap no input. */
 
 /* count adapters of one rank r: A [count][r][K], B [count][N][r] in bf16, scale
  * [count], index [M] (8-byte aligned).  Adapters of smaller rank are filled up with
@@ -711,7 +711,8 @@ int qlora_adapter_linear_bwd(const uint16_t *dY, const uint16_t *X, const uint16
  * whatever X and weight hold there; such rows cost nothing.  The vocabulary is taken in
  * pieces; e^z (dW: dz) is rounded to bf16 between the two products, except the
  * target's own term; sums are fp32, over words 64 bits.  A NaN or an infinity of a row of X
- * makes that row's loss and dX NaN.  K % 64 == 0, M <= 2^22, M K < 2^31, K <= 2^18, V < 2^31. */
+ * makes that row's loss and dX NaN.  Logits stay below 2^127 in size.  Outputs overlap
+ * no input, but for dX, which may be X itself.  K % 64 == 0, M <= 2^22, M K < 2^31, K <= 2^18, V < 2^31. */
 
 typedef enum { QLORA_HEAD_LOSS = 0, QLORA_HEAD_DX = 1, QLORA_HEAD_DW = 2 } qlora_head_pass;
 

@@ -123,7 +123,7 @@ def _check(c, dY, idx):
 SHAPES = [
     (1, 8, 64, 1, 8), (1, 520, 320, 3, 24), (5, 72, 1088, 7, 16), (17, 264, 128, 20, 8), (33, 48, 2048, 5, 40), (64, 136, 704, 64, 128),
     (65, 8, 64, 2, 8), (66, 264, 192, 1, 128), (130, 520, 320, 9, 24), (257, 72, 1088, 300, 16), (300, 320, 64, 3, 72),
-    (513, 256, 256, 1023, 8),
+    (513, 256, 256, 1023, 8), (100, 1160, 128, 3, 16), (70, 136, 2112, 2, 32),
 ]
 
 
@@ -132,6 +132,13 @@ SHAPES = [
 def test_layer(M, N, K, n, r, kind):
     c, dY = _case(M, N, K, n, r, seed=M + N + K)
     _check(c, dY, _index(kind, M, n, seed=n + r))
+
+
+@pytest.mark.parametrize("M,N,K,n,r", [(2304, 4096, 256, 2, 16), (2304, 256, 4096, 4, 24)])
+def test_tiles_of_256(M, N, K, n, r):
+    """Enough tiles for the large ones, forward or backward, and long runs of an adapter."""
+    c, dY = _case(M, N, K, n, r, seed=9)
+    _check(c, dY, _index("mixed", M, n, seed=2))
 
 
 @pytest.mark.parametrize("qtype", ["fp4", "int4"])
