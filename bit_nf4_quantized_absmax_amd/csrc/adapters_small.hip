@@ -1,17 +1,20 @@
 // The linear layer with many adapters for up to 64 tokens (decoding):
 //     Y_m = X_m deq(W)^T + T_m B_a^T,   T_m = bf16(scale_a X_m A_a^T),   a = index[m]
 // Bound by the bytes of the packed weight and of the adapters in use, then by
-// latency: two launches.
+// latency: two launches.  64 tokens x 11008 x 4096 with 64 adapters of rank 16 take
+// 36 us (56 MB, 11 us at the rate of a copy), one token x 4096 x 4096 with rank 64 takes
+// 15 us on the device.
 //
 //  * k_ad_stream: one workgroup per CU, persistent, over equal ranges of
 //    units (kPT x 64 weight rows by 256 columns).  A unit's packed codes, block
 //    codes, group scales and X columns are DMA'd global -> LDS two units ahead; a
-//    wave multiplies 32 rows by one 64-wide block: codes go through a byte ->
+//    wave multiplies 16 rows by one 64-wide block: codes go through a byte ->
 //    bf16x2 table of the levels into 16 x 16 x 32 products, each block's scaled by
 //    its constant in fp32 (the weight is bf16(level) times the constant, as in the
 //    framework's other decoding kernels).  Sums of a row tile go, in fp32, to a slot
 //    for each workgroup that had a part of it.  K is any multiple of 64: columns past
-//    it are zeros of X.
+//    it are zeros of X.  16 waves a workgroup: a wave waits for one table read after
+//    another, so four share a SIMD (64 x 11008 x 4096: 43 us with 8 waves of 32 rows, 36 with 16).
 //  * Beside its first DMAs every wave takes its share of the products X A^T, 16
 //    adapter rows by 512 columns each; the first token of an adapter stands for
 //    all of its tokens, which a ballot over the indices finds.
@@ -34,7 +37,8 @@ __device__ const uint4 gAdZero[1] = {{0, 0, 0, 0}};   // what a DMA past a row r
 
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 1024;               // of k_ad_stream
+constexpr int kEpiThreads = 512;
 constexpr int kRows = 64;                    // weight rows of a tile
 constexpr int kUnitK = 256;
 constexpr int kTileW = kRows * 128;          // packed bytes of a tile and unit
@@ -58,10 +62,12 @@ __device__ __forceinline__ void dma4_far(const void *src, uint32_t dst) {
 __device__ __forceinline__ int wpos(int row, int chunk) { return row * 128 + 16 * (chunk ^ ((row >> 1) & 7)); }
 __device__ __forceinline__ int xpos(int row, int chunk) { return row * 512 + 16 * (chunk ^ (row & 15)); }
 
-// First unit of workgroup w of G over U units, and the workgroup of a unit.
-__device__ __forceinline__ int first_unit(int w, int G, int64_t U) { return static_cast<int>((w * U) / G); }
-__device__ __forceinline__ int workgroup_of(int u, int G, int64_t U) {
-  int w = static_cast<int>((static_cast<int64_t>(u) * G) / U);
+// First unit of workgroup w of G over U units, and the workgroup of a unit (N K < 2^31: U <= 2^20; G <= 256).
+__device__ __forceinline__ int first_unit(int w, int G, int U) {
+  return static_cast<int>(static_cast<uint32_t>(w * U) / static_cast<uint32_t>(G));
+}
+__device__ __forceinline__ int workgroup_of(int u, int G, int U) {
+  int w = static_cast<int>(static_cast<uint32_t>(u * G) / static_cast<uint32_t>(U));
   while (w + 1 < G && first_unit(w + 1, G, U) <= u) ++w;
   while (w > 0 && first_unit(w, G, U) > u) --w;
   return w;
@@ -143,89 +149,102 @@ __global__ __launch_bounds__(kThreads) void k_ad_stream(const StreamArgs a) {
   constexpr int kXS = x_stages<kMB>(), kWS = 3;
   constexpr int kXStage = kMB * 16 * 512;
   constexpr int kWStage = kPT * kTileStage;
-  // A wave's DMA instructions of a unit: kPT (codes), the gathers (block codes and
-  // group scales: 4 kPT of them, to the waves in turn), kMB (X).  At the end of a unit all but
-  // the newest may be in flight: with three X stages W and X of the unit after
-  // next, with two (X is issued before W) only its W.
-  constexpr int kAfter = kXS == 3 ? kPT + kMB : kPT;
   constexpr int kWaves = kThreads / 64;
-  constexpr int kEach = 4 * kPT / kWaves, kMore = 4 * kPT % kWaves;   // gathers of a wave; one more in the first kMore
+  // DMA instructions of a unit, to the waves in turn: 8 kPT of codes and 4 kPT of block
+  // codes and group scales (W), 8 kMB of X.  At the end of a unit all but the newest
+  // may be in flight: with three X stages W and X of the unit after next, with two (X
+  // is issued before W) only its W.
+  constexpr int kDmaW = 12 * kPT, kDmaX = 8 * kMB;
   __shared__ __attribute__((aligned(16))) uint8_t sX[kXS * kXStage];
   __shared__ __attribute__((aligned(16))) uint8_t sW[kWS * kWStage];
   __shared__ uint32_t sLut[256 * kLutCopies];
   __shared__ float sT8[256];
   const int G = gridDim.x, w = blockIdx.x;
-  const int64_t U = static_cast<int64_t>(a.groups) * a.KT;
+  const int U = a.groups * a.KT;
   const int u0 = first_unit(w, G, U), u1 = first_unit(w + 1, G, U);
   if (u0 >= u1) return;                      // (the grid never exceeds the unit count)
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int rh = wave & 1, kq = wave >> 1;
+  const int rq = wave & 3, kq = wave >> 2;       // 16 rows of a tile, block of a unit
   const int nl = lane & 15, g = lane >> 4;
   const int M = a.M, N = a.w.N, K = a.w.K, KB = K >> 6;
   const float mean = a.w.mean[0];
   const float t8v = u2f(cAdT8Level[tid & 255]);
   {
-    // Wave w writes the bytes whose low half is w (lanes 0 .. 31, a copy each) or w + 8: uniform loads.
+    // Wave w writes the bytes whose low half is w, a copy a lane: uniform loads.
+    static_assert(kWaves == 16 && kLutCopies == 32, "a wave a level, two bytes at a time");
     const uint32_t *level = cAdQ4Level + 16 * a.w.qtype;
-    const float lo = u2f(lane < 32 ? level[wave] : level[wave + 8]);
-    uint32_t *dst = sLut + (wave + (lane < 32 ? 0 : 8)) * kLutCopies + (lane & 31);
+    const float lo = u2f(level[wave]);
+    uint32_t *dst = sLut + wave * kLutCopies + (lane & 31);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) dst[16 * kLutCopies * j] = pack_bf16x2(lo, u2f(level[j]));
-    static_assert(kThreads == 512 && kLutCopies == 32, "8 waves of two half waves");
+    for (int j = 0; j < 16; j += 2)
+      dst[16 * kLutCopies * (j + (lane >> 5))] = pack_bf16x2(lo, u2f(lane < 32 ? level[j] : level[j + 1]));
   }
 
   const uint32_t xbase = lds_addr(sX), wbase = lds_addr(sW);
-  // X: wave w fills rows 2 (kMB w + j) and + 1 of a stage, 32 chunks each; rows past M
+  // X: instruction i fills rows 2 i and 2 i + 1 of a stage, 32 chunks each; rows past M
   // repeat the last, chunks past K are zeros.
-  const uint16_t *xsrc[kMB];
-  int xk[kMB];
+  constexpr int kMineX = (kDmaX + kWaves - 1) / kWaves;
+  const uint16_t *xsrc[kMineX];
+  int xk[kMineX];
 #pragma unroll
-  for (int j = 0; j < kMB; ++j) {
-    const int row = 2 * (kMB * wave + j) + (lane >> 5);
+  for (int j = 0; j < kMineX; ++j) {
+    const int row = 2 * (wave + kWaves * j) + (lane >> 5);
     xk[j] = 8 * ((lane & 31) ^ (row & 15));
     xsrc[j] = a.X + static_cast<int64_t>(min(row, M - 1)) * K + xk[j];
   }
   auto dma_x = [&](int q, int kt) __attribute__((always_inline)) {
-    const uint32_t dst = __builtin_amdgcn_readfirstlane(xbase + (q % kXS) * kXStage + kMB * wave * 1024);
+    const uint32_t dst = xbase + (q % kXS) * kXStage;
 #pragma unroll
-    for (int j = 0; j < kMB; ++j) {
+    for (int j = 0; j < kMineX; ++j) {
+      const int i = wave + kWaves * j;
+      if (i >= kDmaX) break;                     // uniform
       const void *src = kUnitK * kt + xk[j] < K ? static_cast<const void *>(xsrc[j] + kUnitK * kt) : gAdZero;
-      dma16(src, dst + j * 1024);
+      dma16(src, __builtin_amdgcn_readfirstlane(dst + i * 1024));
     }
   };
-  // W: wave w fills rows 8 w .. 8 w + 7 of every tile; chunks past K (they meet zeros)
-  // and rows past N (never stored) repeat the last.
-  const int wrow = 8 * wave + (lane >> 3);
-  const int wchunk = (lane & 7) ^ ((wrow >> 1) & 7);
+  // W: instruction 8 t + i fills rows 8 i .. 8 i + 7 of tile t, 8 kPT + 4 t + part the rows'
+  // words of a part: 0, 1 the aligned words that hold the row's block codes 4 kt .. + 3,
+  // 2, 3 the scales of the first's and last's groups.  Chunks past K (they meet
+  // zeros) and rows past N (never stored) repeat the last.
   const int64_t codes = static_cast<int64_t>(N) * KB;
   auto dma_w = [&](int q, int group, int kt) __attribute__((always_inline)) {
-    const uint32_t dst = __builtin_amdgcn_readfirstlane(wbase + (q % kWS) * kWStage);
-    const int byte = min(128 * kt + 16 * wchunk, (K >> 1) - 16);
+    const uint32_t dst = wbase + (q % kWS) * kWStage;
 #pragma unroll
-    for (int t = 0; t < kPT; ++t) {
-      const int n = min(kRows * (kPT * group + t) + wrow, N - 1);
-      dma16(a.w.packed + static_cast<int64_t>(n) * (K >> 1) + byte, dst + t * kTileStage + wave * 1024);
-    }
-#pragma unroll
-    for (int i = wave; i < 4 * kPT; i += kWaves) {
-      // part 0, 1: the aligned words that hold the row's block codes 4 kt .. + 3; 2, 3: the scales of the first's and last's groups
-      const int t = i >> 2, part = i & 3;
-      const int n = min(kRows * (kPT * group + t) + lane, N - 1);
-      const int64_t cb = static_cast<int64_t>(n) * KB + 4 * kt;
-      const void *src;
-      if (part < 2)
-        src = a.w.code8 + min((cb & ~int64_t{3}) + 4 * part, (codes - 1) & ~int64_t{3});
-      else
-        src = a.w.c2 + (min(cb + (part == 2 ? 0 : 3), codes - 1) >> 8);
-      dma4_far(src, dst + t * kTileStage + kTileW + part * 256);
+    for (int i = wave; i < kDmaW; i += kWaves) {
+      if (i < 8 * kPT) {
+        const int t = i >> 3, row = 8 * (i & 7) + (lane >> 3);
+        const int n = min(kRows * (kPT * group + t) + row, N - 1);
+        const int byte = min(128 * kt + 16 * ((lane & 7) ^ ((row >> 1) & 7)), (K >> 1) - 16);
+        dma16(a.w.packed + static_cast<int64_t>(n) * (K >> 1) + byte,
+              __builtin_amdgcn_readfirstlane(dst + t * kTileStage + (i & 7) * 1024));
+      } else {
+        const int t = (i - 8 * kPT) >> 2, part = i & 3;
+        const int n = min(kRows * (kPT * group + t) + lane, N - 1);
+        const int64_t cb = static_cast<int64_t>(n) * KB + 4 * kt;
+        const void *src;
+        if (part < 2)
+          src = a.w.code8 + min((cb & ~int64_t{3}) + 4 * part, (codes - 1) & ~int64_t{3});
+        else
+          src = a.w.c2 + (min(cb + (part == 2 ? 0 : 3), codes - 1) >> 8);
+        dma4_far(src, __builtin_amdgcn_readfirstlane(dst + t * kTileStage + kTileW + part * 256));
+      }
     }
   };
+  // This wave's instructions among those.
+  const int ahead = (kDmaW - wave + kWaves - 1) / kWaves + (kXS == 3 ? (kDmaX - wave + kWaves - 1) / kWaves : 0);
+  constexpr int kAheadMax = (kDmaW + kWaves - 1) / kWaves + (kXS == 3 ? kMineX : 0);
+  static_assert(kAheadMax <= 6, "the cases below");
   auto unit_end = [&]() __attribute__((always_inline)) {
-    if (wave < kMore)
-      raw_barrier<wait_imm(kAfter + kEach + 1, 0)>();
-    else
-      raw_barrier<wait_imm(kAfter + kEach, 0)>();
+    switch (ahead) {                             // uniform
+      case 0: raw_barrier<wait_imm(0, 0)>(); break;
+      case 1: raw_barrier<wait_imm(1, 0)>(); break;
+      case 2: raw_barrier<wait_imm(2, 0)>(); break;
+      case 3: raw_barrier<wait_imm(3, 0)>(); break;
+      case 4: raw_barrier<wait_imm(4, 0)>(); break;
+      case 5: raw_barrier<wait_imm(5, 0)>(); break;
+      default: raw_barrier<wait_imm(6, 0)>(); break;
+    }
   };
 
   const int nq = u1 - u0;
@@ -263,13 +282,11 @@ __global__ __launch_bounds__(kThreads) void k_ad_stream(const StreamArgs a) {
   down_items<kMB>(a, wave * G + w, G * kWaves);
   unit_end();
 
-  f32x4_t acc[kPT][2][kMB];
+  f32x4_t acc[kPT][kMB];
 #pragma unroll
   for (int t = 0; t < kPT; ++t)
 #pragma unroll
-    for (int rg = 0; rg < 2; ++rg)
-#pragma unroll
-      for (int mb = 0; mb < kMB; ++mb) acc[t][rg][mb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    for (int mb = 0; mb < kMB; ++mb) acc[t][mb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   const uint32_t lutl = static_cast<uint32_t>(lane & 31);
 
   for (int q = 0; q < nq; ++q) {
@@ -293,33 +310,30 @@ __global__ __launch_bounds__(kThreads) void k_ad_stream(const StreamArgs a) {
 #pragma unroll
     for (int t = 0; t < kPT; ++t) {
       const uint8_t *ws = ws0 + t * kTileStage;
+      const int row = 16 * rq + nl;
+      const int n = min(kRows * (kPT * group + t) + row, N - 1);
+      const uint32_t cb = static_cast<uint32_t>(n) * static_cast<uint32_t>(KB) + 4 * kt;   // below 2^25
+      const uint32_t at = (cb & 3) + kq;         // byte of the row's two words
+      const int code = ws[kTileW + 256 * (at >> 2) + 4 * row + (at & 3)];
+      const int far = ((cb + kq) >> 8) != (cb >> 8) ? 1 : 0;
+      const float c2 = *reinterpret_cast<const float *>(ws + kTileW + 512 + 256 * far + 4 * row);
+      const uint2 pk = *reinterpret_cast<const uint2 *>(ws + wpos(row, 2 * kq + (g >> 1)) + 8 * (g & 1));
+      const float chat = decode_absmax(sT8[code], c2, mean);
+      const uint32_t words[2] = {pk.x, pk.y};
+      bf16x8_t wop[2];
 #pragma unroll
-      for (int rg = 0; rg < 2; ++rg) {
-        const int row = 32 * rh + 16 * rg + nl;
-        const int n = min(kRows * (kPT * group + t) + row, N - 1);
-        const uint32_t cb = static_cast<uint32_t>(n) * static_cast<uint32_t>(KB) + 4 * kt;   // below 2^25
-        const uint32_t at = (cb & 3) + kq;       // byte of the row's two words
-        const int code = ws[kTileW + 256 * (at >> 2) + 4 * row + (at & 3)];
-        const int far = ((cb + kq) >> 8) != (cb >> 8) ? 1 : 0;
-        const float c2 = *reinterpret_cast<const float *>(ws + kTileW + 512 + 256 * far + 4 * row);
-        const float chat = decode_absmax(sT8[code], c2, mean);
-        const uint2 pk = *reinterpret_cast<const uint2 *>(ws + wpos(row, 2 * kq + (g >> 1)) + 8 * (g & 1));
-        const uint32_t words[2] = {pk.x, pk.y};
-        bf16x8_t wop[2];
+      for (int tt = 0; tt < 2; ++tt) {
+        uint32_t o[4];
 #pragma unroll
-        for (int tt = 0; tt < 2; ++tt) {
-          uint32_t o[4];
+        for (int i = 0; i < 4; ++i) o[i] = sLut[((words[tt] >> (8 * i)) & 0xffu) * kLutCopies + lutl];
+        wop[tt] = __builtin_bit_cast(bf16x8_t, o);
+      }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) o[i] = sLut[((words[tt] >> (8 * i)) & 0xffu) * kLutCopies + lutl];
-          wop[tt] = __builtin_bit_cast(bf16x8_t, o);
-        }
+      for (int mb = 0; mb < kMB; ++mb) {
+        f32x4_t part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xa[mb][0], wop[0], f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+        part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xa[mb][1], wop[1], part, 0, 0, 0);
 #pragma unroll
-        for (int mb = 0; mb < kMB; ++mb) {
-          f32x4_t part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xa[mb][0], wop[0], f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
-          part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xa[mb][1], wop[1], part, 0, 0, 0);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[t][rg][mb][e] = __builtin_fmaf(chat, part[e], acc[t][rg][mb][e]);
-        }
+        for (int e = 0; e < 4; ++e) acc[t][mb][e] = __builtin_fmaf(chat, part[e], acc[t][mb][e]);
       }
     }
     unit_end();
@@ -328,36 +342,28 @@ __global__ __launch_bounds__(kThreads) void k_ad_stream(const StreamArgs a) {
       // A tile's four block quarters are added ((0 + 2) + (1 + 3)) in this unit's X
       // stage, which is consumed and not filled again before the next unit.
       f32x4_t *red = reinterpret_cast<f32x4_t *>(sX + (q % kXS) * kXStage);
-      auto at = [&](int s, int rg, int mb) -> f32x4_t & { return red[(((s * 2 + rh) * 2 + rg) * kMB + mb) * 64 + lane]; };
+      auto at = [&](int s, int mb) -> f32x4_t & { return red[((s * 4 + rq) * kMB + mb) * 64 + lane]; };
 #pragma unroll
       for (int t = 0; t < kPT; ++t) {
 #pragma unroll
-        for (int rg = 0; rg < 2; ++rg)
-#pragma unroll
-          for (int mb = 0; mb < kMB; ++mb)
-            if (kq >= 2) at(kq - 2, rg, mb) = acc[t][rg][mb];
+        for (int mb = 0; mb < kMB; ++mb)
+          if (kq >= 2) at(kq - 2, mb) = acc[t][mb];
         raw_barrier<wait_imm(63, 0)>();
 #pragma unroll
-        for (int rg = 0; rg < 2; ++rg)
-#pragma unroll
-          for (int mb = 0; mb < kMB; ++mb)
-            if (kq < 2) {
-              acc[t][rg][mb] += at(kq, rg, mb);
-              if (kq == 1) at(1, rg, mb) = acc[t][rg][mb];
-            }
+        for (int mb = 0; mb < kMB; ++mb)
+          if (kq < 2) {
+            acc[t][mb] += at(kq, mb);
+            if (kq == 1) at(1, mb) = acc[t][mb];
+          }
         raw_barrier<wait_imm(63, 0)>();
         if (kq == 0) {
           f32x4_t *dst = reinterpret_cast<f32x4_t *>(slot<kMB, kPT>(a.slots, group, t, w));
 #pragma unroll
-          for (int rg = 0; rg < 2; ++rg)
-#pragma unroll
-            for (int mb = 0; mb < kMB; ++mb) dst[((rh * 2 + rg) * kMB + mb) * 64 + lane] = acc[t][rg][mb] + at(1, rg, mb);
+          for (int mb = 0; mb < kMB; ++mb) dst[(rq * kMB + mb) * 64 + lane] = acc[t][mb] + at(1, mb);
         }
         raw_barrier<wait_imm(63, 0)>();          // red is used again by the next tile
 #pragma unroll
-        for (int rg = 0; rg < 2; ++rg)
-#pragma unroll
-          for (int mb = 0; mb < kMB; ++mb) acc[t][rg][mb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        for (int mb = 0; mb < kMB; ++mb) acc[t][mb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
       }
     }
   }
@@ -371,13 +377,13 @@ __global__ __launch_bounds__(kThreads) void k_ad_stream(const StreamArgs a) {
 // slots, the first adapters' rows of B and the partial sums of T are all asked for
 // before the first is used.
 template <int kMB, int kPT, int kH>
-__global__ __launch_bounds__(kThreads) void k_ad_epi(const StreamArgs a, int G, uint16_t *__restrict__ Y, uint16_t *__restrict__ T) {
-  constexpr int kWaves = kThreads / 64;
+__global__ __launch_bounds__(kEpiThreads) void k_ad_epi(const StreamArgs a, int G, uint16_t *__restrict__ Y, uint16_t *__restrict__ T) {
+  constexpr int kWaves = kEpiThreads / 64;
   constexpr int kAtOnce = kMB == 1 ? 2 : 4;            // adapters whose rows of B are in flight
   constexpr int kSeg = 4;                              // slots likewise
   __shared__ __attribute__((aligned(16))) uint16_t sT[64 * 136];   // T, rows of r + 8
   __shared__ float sL[64][17];                         // the adapters' term
-  __shared__ int sAd[64], sTok[kWaves][64];
+  __shared__ int sAd[64], sRank[64], sList[64], sTok[kWaves][64], sCount[kAdMax], sUsed;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int nl = lane & 15, g = lane >> 4;
@@ -394,15 +400,23 @@ __global__ __launch_bounds__(kThreads) void k_ad_epi(const StreamArgs a, int G, 
     for (int i = 0; i < kSeg; ++i)
       seg[i] = reinterpret_cast<const f32x4_t *>(slot<kMB, kPT>(a.slots, group, t, min(wf + i, wl)))[((blockIdx.x & 3) * kMB + wave) * 64 + lane];
   }
-  if (wave == 0) sAd[lane] = mine;
-  // A token's number among those of its adapter; the first of each stands for it.
-  int rank = 0;
-#pragma unroll 8
-  for (int i = 0; i < M - 1; ++i) rank += __builtin_amdgcn_readlane(mine, i) == mine && i < lane ? 1 : 0;
-  const uint64_t firsts = __ballot(mine >= 0 && rank == 0);
-  const int used = __popcll(firsts);
-  if (mine >= 0 && rank == 0) sTok[wave][__popcll(firsts & ((uint64_t{1} << lane) - 1))] = mine;
-  const int list = sTok[wave][lane];                   // lane i: the i-th adapter in use (i < used)
+  // A token's number among those of its adapter (in any order: it is the row of a
+  // product that its sum comes from); the first of each stands for it.
+  if (wave == 0) {
+    sAd[lane] = mine;
+    int rank = 0;
+    if (mine >= 0) {
+      sCount[mine] = 0;
+      rank = atomicAdd(&sCount[mine], 1);
+    }
+    sRank[lane] = rank;
+    const uint64_t firsts = __ballot(mine >= 0 && rank == 0);
+    if (mine >= 0 && rank == 0) sList[__popcll(firsts & ((uint64_t{1} << lane) - 1))] = mine;
+    if (lane == 0) sUsed = __popcll(firsts);
+  }
+  __syncthreads();
+  const int rank = sRank[lane], used = sUsed;
+  const int list = sList[lane];                        // lane i: the i-th adapter in use (i < used)
   bf16x8_t bop[kAtOnce][kH];
   auto fetch = [&](int i0, int j0) __attribute__((always_inline)) {
 #pragma unroll
@@ -417,9 +431,8 @@ __global__ __launch_bounds__(kThreads) void k_ad_epi(const StreamArgs a, int G, 
     }
   };
   if (wave < used) fetch(wave, 0);
-  __syncthreads();                                     // sAd
   // T from its partial sums, in slice order.
-  for (int i = tid; i < M * (r >> 2); i += kThreads) {
+  for (int i = tid; i < M * (r >> 2); i += kEpiThreads) {
     const int m = i / (r >> 2), j = 4 * (i % (r >> 2));
     const int x = sAd[m];
     f32x4_t v = {0.f, 0.f, 0.f, 0.f};
@@ -529,9 +542,9 @@ hipError_t launch_cut(StreamArgs a, uint16_t *T, uint16_t *Y, hipStream_t s) {
   if (e != hipSuccess) return e;
   const dim3 epi((a.w.N + 15) / 16);
   if (a.ad.r <= 32)
-    hipLaunchKernelGGL((k_ad_epi<kMB, kPT, 1>), epi, dim3(kThreads), 0, s, a, grid, Y, T);
+    hipLaunchKernelGGL((k_ad_epi<kMB, kPT, 1>), epi, dim3(kEpiThreads), 0, s, a, grid, Y, T);
   else
-    hipLaunchKernelGGL((k_ad_epi<kMB, kPT, 2>), epi, dim3(kThreads), 0, s, a, grid, Y, T);
+    hipLaunchKernelGGL((k_ad_epi<kMB, kPT, 2>), epi, dim3(kEpiThreads), 0, s, a, grid, Y, T);
   return hipGetLastError();
 }
 
