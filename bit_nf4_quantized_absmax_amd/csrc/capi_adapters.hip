@@ -19,7 +19,8 @@ int check_adapters(int64_t M, const qlora_nf4_weight *W, const qlora_adapters *a
   const int64_t N = W->rows, K = W->cols;
   if (K % 64 != 0 || N % 8 != 0 || N > kMaxElems / K) return QLORA_ERR_UNSUPPORTED_SHAPE;
   if (ad->count > kAdMax || ad->r > 128 || ad->r % 8 != 0) return QLORA_ERR_UNSUPPORTED_SHAPE;
-  if (M > 0 && M > kMaxElems / std::max(round_up(N, 64), static_cast<size_t>(K))) return QLORA_ERR_UNSUPPORTED_SHAPE;
+  // 32-bit byte offsets into X, dY and one adapter
+  if (std::max<int64_t>(M, ad->r) > kMaxElems / std::max<int64_t>(round_up(N, 64), K)) return QLORA_ERR_UNSUPPORTED_SHAPE;
   return QLORA_OK;
 }
 
@@ -91,7 +92,8 @@ extern "C" {
 
 size_t qlora_adapter_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t count, int32_t r, int is_bwd) {
   if (M < 1 || N < 1 || K < 1 || count < 1 || count > kAdMax || r < 8 || r > 128 || r % 8 != 0) return 0;
-  if (K % 64 != 0 || N % 8 != 0 || N > kMaxElems / K || M > kMaxElems / std::max<int64_t>(round_up(N, 64), K)) return 0;
+  if (K % 64 != 0 || N % 8 != 0 || N > kMaxElems / K || std::max<int64_t>(M, r) > kMaxElems / std::max<int64_t>(round_up(N, 64), K))
+    return 0;
   FwdParts f;
   BwdParts b;
   return is_bwd ? carve_bwd(nullptr, M, N, K, count, r, &b) : carve_fwd(nullptr, M, N, K, count, r, &f);

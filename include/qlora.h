@@ -689,7 +689,7 @@ typedef struct {
 size_t qlora_adapter_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t count, int32_t r, int is_bwd);
 
 /* Y [M, N]; T_out [M, r] (nullable) receives T.  Shapes as in qlora_linear_fwd
- * (K % 64 == 0, N % 8 == 0; M times K, and M times N filled up to 64, below 2^31). */
+ * (K % 64 == 0, N % 8 == 0; M and r times K, and times N filled up to 64, below 2^31). */
 int qlora_adapter_linear_fwd(const uint16_t *X, int64_t M, const qlora_nf4_weight *W, const qlora_adapters *ad, uint16_t *Y,
                              uint16_t *T_out, void *ws, size_t ws_bytes, void *stream);
 

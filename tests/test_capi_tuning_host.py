@@ -32,7 +32,7 @@ def test_adapter_sizes():
     assert size(100, 72, 128, 2, 8, 1) >= 100 * 128 * 2                      # rows of dY filled up to 128
     for bad in ((0, 64, 128, 4, 8, 0), (-1, 64, 128, 4, 8, 0), (4, 60, 128, 4, 8, 0), (4, 64, 96, 4, 8, 0), (4, 64, 128, 0, 8, 0),
                 (4, 64, 128, 1024, 8, 0), (4, 64, 128, 4, 12, 0), (4, 64, 128, 4, 136, 0), (4, 64, 128, 4, 0, 0), (1 << 31, 64, 128, 4, 8, 0),
-                (4, 1 << 20, 1 << 11, 4, 8, 0)):
+                (4, 1 << 20, 1 << 11, 4, 8, 0), (4, 8, 1 << 24, 4, 128, 0), (4, 1 << 24, 64, 4, 128, 1)):
         assert size(*bad) == 0, bad
 
 
@@ -49,7 +49,8 @@ def test_adapter_refusals():
                       ({"W": _weight(rows=0)}, INVALID), ({"ad": _set(A=0)}, INVALID), ({"ad": _set(B=0x31008)}, INVALID),
                       ({"ad": _set(scale=0)}, INVALID), ({"ad": _set(index=0)}, INVALID), ({"ad": _set(index=0x33004)}, INVALID),
                       ({"ad": _set(n=0)}, INVALID), ({"ad": _set(n=1024)}, SHAPE), ({"ad": _set(r=4)}, SHAPE), ({"ad": _set(r=136)}, SHAPE),
-                      ({"W": _weight(cols=96)}, SHAPE), ({"W": _weight(rows=60)}, SHAPE), ({"M": 1 << 31}, SHAPE), ({"ws": None}, WS),
+                      ({"W": _weight(cols=96)}, SHAPE), ({"W": _weight(rows=60)}, SHAPE),
+                      ({"W": _weight(rows=8, cols=1 << 24), "ad": _set(r=128)}, SHAPE), ({"M": 1 << 31}, SHAPE), ({"ws": None}, WS),
                       ({"ws": ODD}, WS), ({"bytes": 64}, WS), ({"M": 100, "bytes": 4096}, WS)):
         assert fwd(**bad) == want, bad
     assert fwd(M=0, X=None, Y=None, T=None, ws=None, bytes=0, ad=_set(index=0)) == OK

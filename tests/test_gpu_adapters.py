@@ -77,7 +77,16 @@ def _sizes(c, dY, idx):
     return oad.forward(X, W, A, B, s, i), oad.backward(dY, X, W, A, B, s, i)
 
 
-def _check(c, dY, idx):
+def _check(c, dY, idx, grown=0):
+    """grown: the calls get that many adapters, of which the first and the last are c's two and the others zeros."""
+    own, oidx = c, idx
+    if grown:
+        own = dict(c, scale=torch.ones(grown, device=DEV))
+        for k in ("A", "B"):
+            own[k] = torch.zeros(grown, *c[k].shape[1:], dtype=BF16, device=DEV)
+        for k in ("A", "B", "scale"):
+            own[k][0], own[k][-1] = c[k][0], c[k][1]
+        oidx = torch.where(idx == 1, grown - 1, idx)
     M, K = c["X"].shape
     n, N, r = c["B"].shape
     small = M <= 64
@@ -85,7 +94,7 @@ def _check(c, dY, idx):
     i = idx.cpu().numpy()
     (sY, sT), (sdX, sdA, sdB) = _sizes(c, dY, idx)
     Y, T = oad.forward(host["X"], _weights(c["w"], small), host["A"], host["B"], host["scale"], i)
-    gY, gT = q.adapter_linear_fwd(index=idx, **c)
+    gY, gT = q.adapter_linear_fwd(index=oidx, **own)
     _close(gT, T, R * np.abs(T) + K * S * sT * (1 + R) + 1e-37, "T")
     # T's error goes through B: at most (R + K S) of sum |T| |B|, itself at most sY
     lora = oad.forward(np.abs(host["X"]), np.zeros((N, K)), np.abs(host["A"]), np.abs(host["B"]), np.abs(host["scale"]), i)[0]
@@ -99,7 +108,10 @@ def _check(c, dY, idx):
         return gY, gT
     dYh = _f64(dY)
     dX, dA, dB = oad.backward(dYh, host["X"], _weights(c["w"], False), host["A"], host["B"], host["scale"], i)
-    gdX, gdA, gdB = q.adapter_linear_bwd(dY, c["X"], gT, c["w"], c["A"], c["B"], c["scale"], idx)
+    gdX, gdA, gdB = q.adapter_linear_bwd(dY, own["X"], gT, own["w"], own["A"], own["B"], own["scale"], oidx)
+    if grown:
+        assert not gdA[1:-1].any() and not gdB[1:-1].any()
+        gdA, gdB = gdA[::grown - 1], gdB[::grown - 1]
     G = np.zeros((M, r))
     for m, a in enumerate(i):
         if 0 <= a < n:
@@ -139,6 +151,14 @@ def test_tiles_of_256(M, N, K, n, r):
     """Enough tiles for the large ones, forward or backward, and long runs of an adapter."""
     c, dY = _case(M, N, K, n, r, seed=9)
     _check(c, dY, _index("mixed", M, n, seed=2))
+
+
+@pytest.mark.parametrize("M", [20, 70])
+@pytest.mark.parametrize("N,K", [(72, 16448), (16456, 64)])
+def test_adapters_past_32_bits(M, N, K):
+    """1023 adapters of rank 128 whose A or B has more than 2^31 elements."""
+    c, dY = _case(M, N, K, 2, 128, seed=3)
+    _check(c, dY, _index("mixed", M, 2, seed=4) % 2, grown=1023)
 
 
 @pytest.mark.parametrize("qtype", ["fp4", "int4"])

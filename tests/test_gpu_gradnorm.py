@@ -59,6 +59,16 @@ def test_many_tensors_of_mixed_types_and_sizes(groups, max_norm):
     _check(_grads(shapes, [BF16, FP32, FP16, BF16], 1, size=0.1), max_norm, groups)
 
 
+def test_a_tensor_past_32_bits():
+    """More than 2^32 elements, whole numbers in a few places."""
+    n = 2 ** 32 + 4099
+    x = torch.zeros(n, dtype=BF16, device=DEV)
+    at = torch.tensor([0, 2 ** 31 - 1, 2 ** 31, 2 ** 32 - 1, 2 ** 32, n - 1], device=DEV)
+    x[at] = torch.tensor([1, 2, 3, 4, 5, 3], dtype=BF16, device=DEV)
+    assert q.clip_grad_norm([x], 4.0).item() == 8.0
+    assert x[at].tolist() == [0.5, 1.0, 1.5, 2.0, 2.5, 1.5] and int(x.count_nonzero()) == 6
+
+
 def test_groups_are_clipped_each_by_its_own_norm():
     n = 16
     a, b = _grads([(n, 8, 320), (n, 264, 8)], [BF16], 2)

@@ -105,9 +105,46 @@ def test_loss_and_gradients(M, V, K, whole):
 
 
 def test_pieces_of_the_vocabulary():
-    """More words than one piece at this many rows (16384)."""
+    """More words than one piece at this many rows (32768)."""
     X, W, t, g = _case(4096, 40009, 64, seed=1, whole=True)
     _check(X, W, t, g, whole=True)
+
+
+@pytest.mark.parametrize("M", [2, 70])
+def test_a_head_past_32_bits(M):
+    """More than 2^31 elements of W, all but some rows 0, so that the sums over words have few terms."""
+    V, K, at = 2 ** 25 + 300, 64, 2 ** 25 + 299
+    g = torch.Generator().manual_seed(M)
+    some = torch.cat([torch.tensor([0, 2 ** 24, 2 ** 24 - 1, 2 ** 25 - 1, 2 ** 25, at]), torch.randint(0, V, (60,), generator=g)]).unique()
+    W = torch.zeros(V, K, dtype=BF16, device=DEV)
+    w = torch.randint(-2, 3, (len(some), K), generator=g).double()
+    W[some.to(DEV)] = w.to(BF16).to(DEV)
+    x = torch.randint(-3, 4, (M, K), generator=g) * (torch.rand(M, K, generator=g) < 0.2)
+    X, x = x.to(BF16).to(DEV), x.double()
+    t = torch.full((M,), at)
+    z = x @ w.T                                       # the other logits are 0, as their rows are
+    lse = torch.logsumexp(torch.cat([z, torch.full((M, 1), float(np.log(V - len(some))))], 1).double(), 1)
+    p = torch.exp(z - lse[:, None])
+    last = len(some) - 1                              # of the target
+    loss, l2, dX = q.head_cross_entropy(X, W, t.to(DEV))
+    ep = 2.0 ** -19
+    want = (lse - z[:, last]).numpy()
+    _close(loss, want, ep + S * np.abs(want), "loss")
+    d = p.clone()
+    d[:, last] -= 1
+    e = (R + ep + 2.0 ** -22 * z.abs().max() + len(some) * S) * (d.abs() @ w.abs()) + 2.0 ** -102 * w.abs().sum(0)
+    e, want = e.numpy(), (d @ w).numpy()
+    _close(dX, want, R * (np.abs(want) + e) + e, "dX")
+    dW = q.head_cross_entropy_dW(X, W, t.to(DEV), l2)
+    one = torch.exp(-lse) @ x                         # of a word whose row is 0
+    want = np.concatenate([(d.T @ x).numpy(), one.numpy()[None]])
+    size = torch.cat([d.abs().T @ x.abs(), (torch.exp(-lse) @ x.abs())[None]]).numpy()
+    e = (R + ep + M * S) * size + 2.0 ** -126 * (2 + x.abs().sum(0)).numpy()
+    rows = [int(i) for i in some] + [next(i for i in range(2 ** 24 + 100, V) if i not in set(some.tolist()))]
+    _close(dW[torch.tensor(rows, device=DEV)], want, R * (np.abs(want) + e) + e, "dW")
+    W[:] = dW[rows[-1]]                               # every other row is that one
+    W[some.to(DEV)] = dW[some.to(DEV)]
+    assert torch.equal(W, dW)
 
 
 def test_pieces_whose_largest_logits_are_far_apart():
