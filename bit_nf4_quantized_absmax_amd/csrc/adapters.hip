@@ -7,13 +7,17 @@
 // [0, n) has no adapter.
 //
 // Here for more than kAdSmall tokens, and for every backward pass (fewer tokens
-// forward: adapters_small.hip).  The tokens are sorted by adapter once (k_ad_prepare, by rank and
-// so in a fixed order); T and G are products over 32-token tiles of one adapter
-// (k_ad_down_tiles); the wide products run on 256 x 256 tiles of sorted tokens,
-// gathered by the DMA, whose epilogue adds the adapters' term 32 tokens at a
-// time (k_ad_matmul; k_ad_join where few tiles had their contraction split); dA and dB are products over an adapter's run of tokens
-// (k_ad_grads).  An adapter's numbers meet only its own tokens: a product with
-// another's is dropped, not multiplied by zero, so a NaN in one adapter stays there.
+// forward: adapters_small.hip).  The tokens are sorted by adapter once (k_ad_prepare, by
+// rank and so in a fixed order); T and G are products over 32-token tiles of one adapter
+// (k_ad_down_tiles); the wide products run on tiles of sorted tokens, gathered by
+// the DMA, whose epilogue adds the adapters' term 32 tokens at a time (k_ad_matmul;
+// k_ad_join where few tiles had their contraction split); dA and dB are products
+// over an adapter's run of tokens (k_ad_grads).  An adapter's numbers meet only its
+// own tokens: a product with another's is dropped, not multiplied by zero, so a NaN in
+// one adapter stays there.
+//
+// Bound by the wide products: 8192 x 4096 x 11008 with 8 adapters of rank 64 takes
+// 680 us (690 of 807 in a trace), a step of 8192 x 4096 x 4096 with 32 of rank 16 takes 580.
 #include <algorithm>
 
 #include "common.h"
@@ -168,7 +172,9 @@ __device__ __forceinline__ void ad_transpose(uint16_t *t, const uint16_t *__rest
 //   transpose A [n, r, K] -> At [n, K, r] and B [n, N, r] -> Bt [n, r, N filled up
 //   to 64] (the backward products then read their adapter operand along its rows),
 //   fill up dY's rows to a multiple of 64 with zeros.
-// One after the other the sort, 15 us at 8192 tokens on one compute unit, and four launches would add up.
+// One after the other the sort, 15 us at 8192 tokens on one compute unit, and four
+// launches would add up.  27 to 32 us with the 90 MB written for a weight of 4096 x 11008,
+// 13 with that of 4096 x 4096 (the sort then); 8 to 13 at 777 tokens, the sort's latency.
 __global__ __launch_bounds__(kSortThreads) void k_ad_prepare(const AdPrepare a) {
   __shared__ union {
     SortLds sort;
@@ -236,9 +242,11 @@ __global__ __launch_bounds__(kSortThreads) void k_ad_prepare(const AdPrepare a) 
 // contraction: P [M, D] (X or dY), Q [n, r, D] (A, or B transposed).  Workgroup
 // (tile, 64 adapter rows, split), 4 waves; wave w takes the 64-column steps w, w + 4, ...
 // of the part from a private ring in LDS, so there is no barrier in the loop, and
-// the waves are summed in wave order.  Bound by the stream of P; split so that
-// the tiles, whose number is not a multiple of the compute units, end evenly
-// (8192 tokens, D = 11008, r = 64: 90 us unsplit).
+// the waves are summed in wave order.  Bound by the gather of P in pieces of 128
+// bytes; split so that the tiles, whose number is not a multiple of the compute units, end
+// evenly.  8192 tokens, D = 11008, r = 64: 90 us unsplit, 70 to 77 in 8 parts (180 MB of P
+// at 2.4 TB/s); one or two waves a workgroup, and parts for 256 to 2048 workgroups,
+// are within 3 % of it in the whole layer.  r = 16, D = 4096: 20 to 24 us.
 namespace {
 constexpr int kDtWaves = 4;
 constexpr int kDtThreads = kDtWaves * 64;
@@ -349,7 +357,8 @@ __global__ __launch_bounds__(kDtThreads) void k_ad_down_tiles(const uint16_t *__
   }
 }
 
-// out [M, r] = bf16(scale_a times the sum of the parts), 0 for tokens without an adapter.
+// out [M, r] = bf16(scale_a times the sum of the parts), 0 for tokens without an
+// adapter; all parts' loads at once (3 to 6 us: its launch, and 17 MB at r = 64).
 __global__ __launch_bounds__(256) void k_ad_sum(const float *__restrict__ part, int splits, int M, int r, const int64_t *__restrict__ index,
                                                 int n, const float *__restrict__ scale, uint16_t *__restrict__ out) {
   const int64_t all = static_cast<int64_t>(M) * r;
@@ -378,6 +387,8 @@ __global__ __launch_bounds__(256) void k_ad_sum(const float *__restrict__ part, 
 // bytes a lane are an operand of the matrix instruction).  Sorted tokens: most
 // blocks have one adapter and accumulate in place; in the others the product is
 // formed apart and added in the lanes whose token has this adapter.
+// 8192 tokens: 600 to 690 us for 4096 x 11008 (1.07 to 1.23 PFLOP/s), 231 to 246 for 4096 x
+// 4096, 236 to 268 for its NN form.
 // Kc, L's row pitch: a multiple of 64; NN: columns N .. Kc - 1 of L are zero.
 namespace {
 struct AdMatmul {
@@ -474,7 +485,8 @@ __global__ __launch_bounds__(S::kThreads, 2) void k_ad_matmul(const AdMatmul g) 
   }
 }
 
-// A tile's splits added in order, then as above.
+// A tile's splits added in order, then as above (105 x 3232 x 10944: the layer takes 62 us
+// with the contraction split and this launch, 179 without).
 template <class S>
 __global__ __launch_bounds__(S::kThreads, 2) void k_ad_join(const AdMatmul g) {
   using namespace gemm16;
@@ -507,7 +519,8 @@ __global__ __launch_bounds__(S::kThreads, 2) void k_ad_join(const AdMatmul g) {
 // in a private ring; both operands are read with the transposing LDS load.
 // Places past the run are read from a row of zeros.  Empty runs give zeros.  Short
 // runs take 2 waves: a workgroup then has 37 KB of LDS and a compute unit four of them,
-// over whose starts and ends the others work.
+// over whose starts and ends the others work.  Bound by reading X and dY, 134 MB at
+// 8192 x (4096 + 4096): 29 us where the caches hold part of it, 45 in a step (3 TB/s).
 namespace {
 constexpr int kGdTile = 32 * 128;
 constexpr int kGdSlot = 2 * kGdTile;   // P then Q

@@ -16,14 +16,18 @@
 //    nothing a second time), and the gradient so far by the next product's epilogue.
 //  * The target's own term is left out of E and of the sums, and joins them in 64
 //    bits at the end (k_head_finish): the loss is log(1 + sum / e^(z_t - ref)), and
-//    (p_t - 1) W_t is added in fp32, where a rounded p_t near 1 would lose both.  E's rounding to bf16 is
-//    the operand type of the second product; its error is that of one output rounding, averaged over words.
+//    (p_t - 1) W_t is added in fp32, where a rounded p_t near 1 would lose both.  E's
+//    rounding to bf16 is the operand type of the second product; its error is that of
+//    one output rounding, averaged over words.
 //  * Rows without a target take no part: the rows that have one are listed
 //    first (k_head_rows), and the DMA gathers them; for dW, where they are the
 //    contraction, they are copied together (k_head_gather).
 //  * dW, where the head is tuned as well, makes its logits a second time, for
 //    dz needs the whole row's sum: dz^T piece by piece in bf16 (k_head_dz), then
 //    dz^T X (k_head_dw).
+//  * Bound by the two (with dW four) products: 8192 x 32000 x 4096 with 6144 targets takes
+//    2770 us (1.16 PFLOP/s over the whole call), 2048 x 131072 x 4096 with dW
+//    7500 (1.17); few rows by reading W, 58 us for one of 32000 x 4096 (4.6 TB/s).
 #include <algorithm>
 
 #include "common.h"
@@ -159,7 +163,8 @@ __global__ __launch_bounds__(256) void k_head_gather(const uint16_t *__restrict_
 // Words v0 .. v0 + words - 1 of the listed rows: part [64-word group][row] =
 // (ref, sum of e^(z - ref)) without the target, the target's logit where it is
 // among them, and with kE the matrix E [row][pitch], pitch = words filled up to 64,
-// zero there and at the target.
+// zero there and at the target.  6144 rows x 16384 words x 4096: 667 to 703 us (1.17 to 1.24
+// PFLOP/s).  225 rows x 50001 x 1088, one row of tiles: 35 us (3.7 TB/s of W and E).
 template <class S, bool kE>
 __global__ __launch_bounds__(S::kThreads, 2) void k_head_logits(const uint16_t *__restrict__ X, const uint16_t *__restrict__ W, int K,
                                                                   int v0, int words, HeadRows h, HeadPiece pc) {
@@ -354,7 +359,10 @@ __global__ __launch_bounds__(256) void k_head_refs(HeadRows h, HeadPiece pc, int
 }
 
 // ---------------------------------------------------------------------------
-// C [split][row][K] (fp32) = factor C + sum over the split's words of E W.
+// C [split][row][K] (fp32) = factor C + sum over the split's words of E W.  6144 rows x
+// 16384 words x 4096: 693 to 741 us (1.11 to 1.19 PFLOP/s).  225 rows x 50001 x 1088: 51 us in
+// 32 splits of 5 tiles; 51 and 64 splits, which fill the chip, make the whole call
+// slower by what their sums cost (100, 104 and 108 us), as do Mid tiles (106).
 template <class S>
 __global__ __launch_bounds__(S::kThreads, 2) void k_head_acc(const uint16_t *__restrict__ W, int V, int K, int v0, HeadCut cut, int first,
                                                                HeadRows h, HeadPiece pc, float *__restrict__ C) {
@@ -401,7 +409,9 @@ __global__ __launch_bounds__(S::kThreads, 2) void k_head_acc(const uint16_t *__r
 // ---------------------------------------------------------------------------
 // Up to kHeadSmall rows: bound by reading W, once for the logits and once more for the
 // gradient, so both kernels keep three steps of it in flight in a ring of four
-// stages, and the few rows of X or E go along from L2.
+// stages, and the few rows of X or E go along from L2.  One row x 32000 x 4096: 57 us
+// (4.6 TB/s; the tiles above took 117 and their launches the rest of 150), with the
+// gradient 109 for the whole call; 64 rows with it 117.
 namespace {
 constexpr int kSmThreads = 256;
 constexpr int kSmRing = 4;
@@ -642,8 +652,10 @@ __global__ __launch_bounds__(kSmThreads) void k_head_small_acc(const uint16_t *_
 }
 
 // ---------------------------------------------------------------------------
-// A workgroup a row of X and 2048 columns: its loss and (ref, log sum); with kGrad 1 (bf16) or 2
-// (fp32) its gradient, weight (C / sum + (p_t - 1) W_t).
+// A workgroup a row of X and 2048 columns: its loss and (ref, log sum); with kGrad 1
+// (bf16) or 2 (fp32) its gradient, weight (C / sum + (p_t - 1) W_t).  Bound by reading C:
+// 8192 rows x 4096, 6144 with a target, two splits: 66 to 71 us; 225 rows x 1088, 32
+// splits: 12 (31 MB, eight splits' loads of a thread at once).
 template <int kGrad>
 __global__ __launch_bounds__(256) void k_head_finish(const uint16_t *__restrict__ W, int K, const float *__restrict__ weight, HeadRows h,
                                                      int rows, HeadCut cut, const float *__restrict__ C, float *__restrict__ loss,
@@ -728,7 +740,8 @@ __global__ __launch_bounds__(256) void k_head_scale(const float *__restrict__ D,
 
 // ---------------------------------------------------------------------------
 // dz^T [word][pitch] of words v0 .. v0 + words - 1 and the listed rows, in bf16;
-// zeros in the columns count .. (count filled up to 64) - 1.
+// zeros in the columns count .. (count filled up to 64) - 1.  2048 rows x 65536 words x 4096:
+// 938 to 956 us (1.15 to 1.17 PFLOP/s), as k_head_dw below.
 template <class S>
 __global__ __launch_bounds__(S::kThreads, 2) void k_head_dz(const uint16_t *__restrict__ Xc, const uint16_t *__restrict__ W, int K, int v0,
                                                               int words, HeadRows h, const float *__restrict__ lse,
