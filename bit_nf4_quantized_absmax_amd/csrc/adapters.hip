@@ -17,7 +17,8 @@
 // one adapter stays there.
 //
 // Bound by the wide products: 8192 x 4096 x 11008 with 8 adapters of rank 64 takes
-// 680 us (690 of 807 in a trace), a step of 8192 x 4096 x 4096 with 32 of rank 16 takes 580.
+// 680 us (690 of 807 in a trace), a step of 8192 x 4096 x 4096 with 32 of rank 16 takes 560
+// to 580.
 #include <algorithm>
 
 #include "common.h"
@@ -154,16 +155,28 @@ __device__ __forceinline__ void ad_sort(SortLds &lds, const int64_t *__restrict_
   }
 }
 
-// One 64 x 64 tile of a matrix [rows, cols] into [cols, pitch], zeros in the columns rows .. pitch - 1.
-__device__ __forceinline__ void ad_transpose(uint16_t *t, const uint16_t *__restrict__ src, int rows, int cols, int pitch, int r0, int c0,
-                                             uint16_t *__restrict__ dst) {
-  const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
-  for (int i = y; i < 64; i += kSortWaves)
-    t[i * 65 + x] = r0 + i < rows && c0 + x < cols ? src[static_cast<int64_t>(r0 + i) * cols + c0 + x] : 0;
+// One R x C tile (powers of two, R C = 4096) of a matrix [rows, cols] into [cols, pitch],
+// zeros in the columns rows .. pitch - 1.
+constexpr int kTrTile = 256 * 17;      // R (C + 1) at most
+__device__ __forceinline__ void ad_transpose(uint16_t *t, const uint16_t *__restrict__ src, int rows, int cols, int pitch, int R, int C,
+                                             int r0, int c0, uint16_t *__restrict__ dst) {
+  for (int i = threadIdx.x; i < 4096; i += kSortThreads) {
+    const int y = i / C, x = i & (C - 1);
+    t[y * (C + 1) + x] = r0 + y < rows && c0 + x < cols ? src[static_cast<int64_t>(r0 + y) * cols + c0 + x] : 0;
+  }
   __syncthreads();
-  for (int i = y; i < 64; i += kSortWaves)
-    if (c0 + i < cols && r0 + x < pitch) dst[static_cast<int64_t>(c0 + i) * pitch + r0 + x] = t[x * 65 + i];
+  for (int i = threadIdx.x; i < 4096; i += kSortThreads) {
+    const int y = i / R, x = i & (R - 1);
+    if (c0 + y < cols && r0 + x < pitch) dst[static_cast<int64_t>(c0 + y) * pitch + r0 + x] = t[x * (C + 1) + y];
+  }
 }
+
+// A tile's extent along r and along the other axis: no wider than r needs (32 adapters of rank
+// 16, 4096 x 4096, a step: 590 to 599 us with 64 x 64 tiles, three quarters empty, 579 so).
+struct TrCut {
+  int narrow, wide;
+  __host__ __device__ explicit TrCut(int r) : narrow(r <= 16 ? 16 : r <= 32 ? 32 : 64), wide(4096 / narrow) {}
+};
 }  // namespace
 
 // Everything that the products need beforehand and that needs nothing itself, in
@@ -174,11 +187,11 @@ __device__ __forceinline__ void ad_transpose(uint16_t *t, const uint16_t *__rest
 //   fill up dY's rows to a multiple of 64 with zeros.
 // One after the other the sort, 15 us at 8192 tokens on one compute unit, and four
 // launches would add up.  27 to 32 us with the 90 MB written for a weight of 4096 x 11008,
-// 13 with that of 4096 x 4096 (the sort then); 8 to 13 at 777 tokens, the sort's latency.
+// 14 to 17 with that of 4096 x 4096 (the sort then); 8 to 13 at 777 tokens, the sort's latency.
 __global__ __launch_bounds__(kSortThreads) void k_ad_prepare(const AdPrepare a) {
   __shared__ union {
     SortLds sort;
-    uint16_t tile[64 * 65];
+    uint16_t tile[kTrTile];
     float table[272];
   } lds;
   int b = blockIdx.x;
@@ -211,18 +224,21 @@ __global__ __launch_bounds__(kSortThreads) void k_ad_prepare(const AdPrepare a) 
     return;
   }
   b -= a.deq;
-  const int ta = (a.r + 63) / 64, tk = (a.w.K + 63) / 64, tn = (a.w.N + 63) / 64;
+  const TrCut cut(a.r);
+  const int ta = (a.r + cut.narrow - 1) / cut.narrow;
   if (b < a.trA) {
+    const int tk = (a.w.K + cut.wide - 1) / cut.wide;
     const int m = b / (ta * tk), j = b % (ta * tk);
-    ad_transpose(lds.tile, a.A + static_cast<int64_t>(m) * a.r * a.w.K, a.r, a.w.K, a.r, j / tk * 64, j % tk * 64,
-                 a.At + static_cast<int64_t>(m) * a.r * a.w.K);
+    ad_transpose(lds.tile, a.A + static_cast<int64_t>(m) * a.r * a.w.K, a.r, a.w.K, a.r, cut.narrow, cut.wide, j / tk * cut.narrow,
+                 j % tk * cut.wide, a.At + static_cast<int64_t>(m) * a.r * a.w.K);
     return;
   }
   b -= a.trA;
   if (b < a.trB) {
+    const int tn = (a.Np + cut.wide - 1) / cut.wide;
     const int m = b / (ta * tn), j = b % (ta * tn);
-    ad_transpose(lds.tile, a.B + static_cast<int64_t>(m) * a.w.N * a.r, a.w.N, a.r, a.Np, j / ta * 64, j % ta * 64,
-                 a.Bt + static_cast<int64_t>(m) * a.r * a.Np);
+    ad_transpose(lds.tile, a.B + static_cast<int64_t>(m) * a.w.N * a.r, a.w.N, a.r, a.Np, cut.wide, cut.narrow, j / ta * cut.wide,
+                 j % ta * cut.narrow, a.Bt + static_cast<int64_t>(m) * a.r * a.Np);
     return;
   }
   b -= a.trB;
@@ -672,7 +688,8 @@ __global__ __launch_bounds__(kGdWaves * 64) void k_ad_grads(AdGradArgs g, AdPlan
 
 // ---------------------------------------------------------------------------
 hipError_t launch_ad_prepare(AdPrepare a, hipStream_t s) {
-  const int ta = (a.r + 63) / 64, tk = (a.w.K + 63) / 64, tn = (a.w.N + 63) / 64;
+  const TrCut cut(a.r);
+  const int ta = (a.r + cut.narrow - 1) / cut.narrow, tk = (a.w.K + cut.wide - 1) / cut.wide, tn = (a.Np + cut.wide - 1) / cut.wide;
   const int64_t chunks = static_cast<int64_t>(a.w.N) * a.w.K / 16;
   a.deq = a.Wd ? static_cast<int>(std::min<int64_t>(2048, (chunks + kSortThreads - 1) / kSortThreads)) : 0;
   a.trA = a.At ? a.n * ta * tk : 0;
