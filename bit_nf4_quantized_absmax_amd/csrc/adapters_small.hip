@@ -16,8 +16,8 @@
 //    it are zeros of X.  16 waves a workgroup: a wave waits for one table read after
 //    another, so four share a SIMD (64 x 11008 x 4096: 43 us with 8 waves of 32 rows, 36 with 16).
 //  * Beside its first DMAs every wave takes its share of the products X A^T, 16
-//    adapter rows by 512 columns each; the first token of an adapter stands for
-//    all of its tokens, which a ballot over the indices finds.
+//    adapter rows by 512 columns each; every 16th token of an adapter stands for
+//    itself and the next 15, which a ballot over the indices finds.
 //  * k_ad_epi: 16 weight rows a workgroup; adds the slots in workgroup order, forms T
 //    from its partial sums and adds each token's product with its own adapter: the
 //    adapters in use go to the waves in turn, and a token takes the product of
@@ -94,8 +94,8 @@ struct StreamArgs {
   int M, KT, groups;
 };
 
-// One wave's share of the partial sums of T: items (leading token, 16 adapter rows, slice).
-template <int kMB>
+// One wave's share of the partial sums of T: items (token, 16 adapter rows, slice), of
+// which every 16th token of an adapter stands for itself and the next 15.
 __device__ __forceinline__ void down_items(const StreamArgs &a, int item0, int step) {
   const int lane = threadIdx.x & 63, nl = lane & 15, g = lane >> 4;
   const int M = a.M, K = a.w.K, r = a.ad.r;
@@ -105,40 +105,34 @@ __device__ __forceinline__ void down_items(const StreamArgs &a, int item0, int s
     const int m0 = it % M, jt = it / M % jts, sl = it / M / jts;
     const int ad = __builtin_amdgcn_readlane(mine, m0);
     const uint64_t mask = __ballot(mine == ad);
-    if (ad < 0 || __builtin_ctzll(mask) != m0) continue;
-    const int cnt = __popcll(mask);
+    const int cnt = __popcll(mask), t0 = __popcll(mask & ((uint64_t{1} << m0) - 1));
+    if (ad < 0 || (t0 & 15) != 0) continue;
+    // token number t0 + nl of the adapter (0 past the last: its column is not stored)
+    const int rank = __popcll(mask & ((uint64_t{1} << lane) - 1)) - t0;
+    const int sent = __builtin_amdgcn_ds_permute(4 * (mine == ad && rank >= 0 && rank < 16 ? rank : 63), lane);
+    const int tok = __builtin_amdgcn_ds_bpermute(4 * nl, sent);
     const int j = 16 * jt + nl;
     const uint16_t *arow = a.ad.A + (static_cast<int64_t>(ad) * r + min(j, r - 1)) * K;
     const int k0 = sl * kSlice, steps = min(kSlice, K - k0) >> 5;   // K % 64 == 0
     float *P = a.P + static_cast<int64_t>(sl) * M * r;
-    for (int t0 = 0; t0 < cnt; t0 += 16) {
-      // token number t0 + nl of the adapter: the (t0 + nl)-th bit of mask
-      uint64_t left = mask;
-      int tok = m0;
-      for (int i = 0; i < cnt; ++i) {
-        const int b = __builtin_ctzll(left);
-        left &= left - 1;
-        tok = i == t0 + nl ? b : tok;
-      }
-      const uint16_t *xrow = a.X + static_cast<int64_t>(tok) * K;
-      f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+    const uint16_t *xrow = a.X + static_cast<int64_t>(tok) * K;
+    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-      for (int s0 = 0; s0 < steps; s0 += 8) {
-        bf16x8_t av[8], xv[8];
+    for (int s0 = 0; s0 < steps; s0 += 8) {
+      bf16x8_t av[8], xv[8];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int k = k0 + 32 * min(s0 + u, steps - 1) + 8 * g;
-          av[u] = *reinterpret_cast<const bf16x8_t *>(arow + k);
-          xv[u] = *reinterpret_cast<const bf16x8_t *>(xrow + k);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-          if (s0 + u < steps) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av[u], xv[u], acc, 0, 0, 0);
+      for (int u = 0; u < 8; ++u) {
+        const int k = k0 + 32 * min(s0 + u, steps - 1) + 8 * g;
+        av[u] = *reinterpret_cast<const bf16x8_t *>(arow + k);
+        xv[u] = *reinterpret_cast<const bf16x8_t *>(xrow + k);
       }
-      // lane: token nl, adapter rows 16 jt + 4 g + e
-      if (t0 + nl < cnt && 16 * jt + 4 * g < r) *reinterpret_cast<f32x4_t *>(P + static_cast<int64_t>(tok) * r + 16 * jt + 4 * g) = acc;
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (s0 + u < steps) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av[u], xv[u], acc, 0, 0, 0);
     }
+    // lane: token nl, adapter rows 16 jt + 4 g + e
+    if (t0 + nl < cnt && 16 * jt + 4 * g < r) *reinterpret_cast<f32x4_t *>(P + static_cast<int64_t>(tok) * r + 16 * jt + 4 * g) = acc;
   }
 }
 
@@ -279,7 +273,7 @@ __global__ __launch_bounds__(kThreads) void k_ad_stream(const StreamArgs a) {
     issue_w();
   }
   if (tid < 256) sT8[tid] = t8v;
-  down_items<kMB>(a, wave * G + w, G * kWaves);
+  down_items(a, wave * G + w, G * kWaves);
   unit_end();
 
   f32x4_t acc[kPT][kMB];
@@ -377,9 +371,9 @@ __global__ __launch_bounds__(kThreads) void k_ad_stream(const StreamArgs a) {
 // slots, the first adapters' rows of B and the partial sums of T are all asked for
 // before the first is used.
 template <int kMB, int kPT, int kH>
-__global__ __launch_bounds__(kEpiThreads) void k_ad_epi(const StreamArgs a, int G, uint16_t *__restrict__ Y, uint16_t *__restrict__ T) {
+__global__ __launch_bounds__(kEpiThreads, 6) void k_ad_epi(const StreamArgs a, int G, uint16_t *__restrict__ Y, uint16_t *__restrict__ T) {
   constexpr int kWaves = kEpiThreads / 64;
-  constexpr int kAtOnce = kMB == 1 ? 2 : 4;            // adapters whose rows of B are in flight
+  constexpr int kAtOnce = kMB == 1 || kH == 2 ? 2 : 4;            // adapters whose rows of B are in flight
   constexpr int kSeg = 4;                              // slots likewise
   __shared__ __attribute__((aligned(16))) uint16_t sT[64 * 136];   // T, rows of r + 8
   __shared__ float sL[64][17];                         // the adapters' term
@@ -394,12 +388,6 @@ __global__ __launch_bounds__(kEpiThreads) void k_ad_epi(const StreamArgs a, int 
   const int slices = (a.w.K + kSlice - 1) / kSlice;
   const int U = a.groups * a.KT;
   const int wf = workgroup_of(group * a.KT, G, U), wl = workgroup_of(group * a.KT + a.KT - 1, G, U);
-  f32x4_t seg[kSeg];
-  if (wave < kMB) {
-#pragma unroll
-    for (int i = 0; i < kSeg; ++i)
-      seg[i] = reinterpret_cast<const f32x4_t *>(slot<kMB, kPT>(a.slots, group, t, min(wf + i, wl)))[((blockIdx.x & 3) * kMB + wave) * 64 + lane];
-  }
   // A token's number among those of its adapter (in any order: it is the row of a
   // product that its sum comes from); the first of each stands for it.
   if (wave == 0) {
@@ -452,6 +440,13 @@ __global__ __launch_bounds__(kEpiThreads) void k_ad_epi(const StreamArgs a, int 
     const uint2 b = make_uint2(pack_bf16x2(s * v[0], s * v[1]), pack_bf16x2(s * v[2], s * v[3]));
     *reinterpret_cast<uint2 *>(sT + m * pitch + j) = b;
     if (blockIdx.x == 0) *reinterpret_cast<uint2 *>(T + static_cast<int64_t>(m) * r + j) = b;
+  }
+  // not earlier: a register more and two workgroups instead of three fit a compute unit
+  f32x4_t seg[kSeg];
+  if (wave < kMB) {
+#pragma unroll
+    for (int i = 0; i < kSeg; ++i)
+      seg[i] = reinterpret_cast<const f32x4_t *>(slot<kMB, kPT>(a.slots, group, t, min(wf + i, wl)))[((blockIdx.x & 3) * kMB + wave) * 64 + lane];
   }
   __syncthreads();
   for (int i0 = wave; i0 < used; i0 += kWaves * kAtOnce) {
