@@ -95,12 +95,12 @@ struct StreamArgs {
 };
 
 // One wave's share of the partial sums of T: items (token, 16 adapter rows, slice), of
-// which every 16th token of an adapter stands for itself and the next 15.
-__device__ __forceinline__ void down_items(const StreamArgs &a, int item0, int step) {
+// which every 16th token of an adapter stands for itself and the next 15.  mine: the
+// adapter of token `lane`, -1: none.
+__device__ __forceinline__ void down_items(const StreamArgs &a, int mine, int item0, int step) {
   const int lane = threadIdx.x & 63, nl = lane & 15, g = lane >> 4;
   const int M = a.M, K = a.w.K, r = a.ad.r;
   const int jts = (r + 15) >> 4, slices = (K + kSlice - 1) / kSlice;
-  const int mine = lane < M ? adapter_of(a.ad.index, lane, a.ad.n) : -1;
   for (int it = item0; it < M * jts * slices; it += step) {
     const int m0 = it % M, jt = it / M % jts, sl = it / M / jts;
     const int ad = __builtin_amdgcn_readlane(mine, m0);
@@ -163,7 +163,9 @@ __global__ __launch_bounds__(kThreads) void k_ad_stream(const StreamArgs a) {
   const int nl = lane & 15, g = lane >> 4;
   const int M = a.M, N = a.w.N, K = a.w.K, KB = K >> 6;
   const float mean = a.w.mean[0];
-  const float t8v = u2f(cAdT8Level[tid & 255]);
+  // The index and the levels are waited for together and before the first DMA is issued:
+  // a wait behind the DMAs would be for them too.
+  const int64_t named = lane < M ? a.ad.index[lane] : -1;
   {
     // Wave w writes the bytes whose low half is w, a copy a lane: uniform loads.
     static_assert(kWaves == 16 && kLutCopies == 32, "a wave a level, two bytes at a time");
@@ -174,6 +176,8 @@ __global__ __launch_bounds__(kThreads) void k_ad_stream(const StreamArgs a) {
     for (int j = 0; j < 16; j += 2)
       dst[16 * kLutCopies * (j + (lane >> 5))] = pack_bf16x2(lo, u2f(lane < 32 ? level[j] : level[j + 1]));
   }
+
+  const int mine = named >= 0 && named < a.ad.n ? static_cast<int>(named) : -1;
 
   const uint32_t xbase = lds_addr(sX), wbase = lds_addr(sW);
   // X: instruction i fills rows 2 i and 2 i + 1 of a stage, 32 chunks each; rows past M
@@ -262,6 +266,7 @@ __global__ __launch_bounds__(kThreads) void k_ad_stream(const StreamArgs a) {
     dma_x(qx, px.kt);
     if (++qx < nq) next(px);
   };
+  if (wave < 4) dma4_far(cAdT8Level + tid, __builtin_amdgcn_readfirstlane(lds_addr(sT8) + 256 * wave));
   if constexpr (kXS == 3) {
     issue_w();
     issue_x();
@@ -272,8 +277,7 @@ __global__ __launch_bounds__(kThreads) void k_ad_stream(const StreamArgs a) {
     issue_w();
     issue_w();
   }
-  if (tid < 256) sT8[tid] = t8v;
-  down_items(a, wave * G + w, G * kWaves);
+  down_items(a, mine, wave * G + w, G * kWaves);
   unit_end();
 
   f32x4_t acc[kPT][kMB];
