@@ -2,8 +2,8 @@
 //     Y_m = X_m deq(W)^T + T_m B_a^T,   T_m = bf16(scale_a X_m A_a^T),   a = index[m]
 // Bound by the bytes of the packed weight and of the adapters in use, then by
 // latency: two launches.  64 tokens x 11008 x 4096 with 64 adapters of rank 16 take
-// 36 us (56 MB, 11 us at the rate of a copy), one token x 4096 x 4096 with rank 64 takes
-// 15 us on the device.
+// 31 us (56 MB, 11 us at the rate of a copy; 23 of k_ad_stream and 11 of k_ad_epi in a
+// trace), with one adapter 27; one token x 4096 x 4096 with rank 64 takes 9 + 4.
 //
 //  * k_ad_stream: one workgroup per CU, persistent, over equal ranges of
 //    units (kPT x 64 weight rows by 256 columns).  A unit's packed codes, block
@@ -14,7 +14,8 @@
 //    framework's other decoding kernels).  Sums of a row tile go, in fp32, to a slot
 //    for each workgroup that had a part of it.  K is any multiple of 64: columns past
 //    it are zeros of X.  16 waves a workgroup: a wave waits for one table read after
-//    another, so four share a SIMD (64 x 11008 x 4096: 43 us with 8 waves of 32 rows, 36 with 16).
+//    another, so four share a SIMD (64 x 11008 x 4096, both kernels: 43 us with 8 waves of
+//    32 rows, 37 with 16).
 //  * Beside its first DMAs every wave takes its share of the products X A^T, 16
 //    adapter rows by 512 columns each; every 16th token of an adapter stands for
 //    itself and the next 15, which a ballot over the indices finds.
@@ -372,8 +373,10 @@ __global__ __launch_bounds__(kThreads) void k_ad_stream(const StreamArgs a) {
 // turn.  An adapter's tokens are the rows of its own products, 16 at a time (lane:
 // weight row l % 16, token 4 (l / 16) + e of them), so every token's sum is written
 // by one wave.  kH: 32-column parts of B that are fetched at once (1: r <= 32).  The
-// slots, the first adapters' rows of B and the partial sums of T are all asked for
-// before the first is used.
+// first adapters' rows of B and the partial sums of T are all asked for before the first
+// is used.  Registers for three workgroups a compute unit: 688 of them (N = 11008) are one
+// round then, where two make a second (both kernels 31.6 us against 36.7; rank 64, with
+// two adapters' rows in flight instead of four, 50 against 54).
 template <int kMB, int kPT, int kH>
 __global__ __launch_bounds__(kEpiThreads, 6) void k_ad_epi(const StreamArgs a, int G, uint16_t *__restrict__ Y, uint16_t *__restrict__ T) {
   constexpr int kWaves = kEpiThreads / 64;
@@ -445,7 +448,7 @@ __global__ __launch_bounds__(kEpiThreads, 6) void k_ad_epi(const StreamArgs a, i
     *reinterpret_cast<uint2 *>(sT + m * pitch + j) = b;
     if (blockIdx.x == 0) *reinterpret_cast<uint2 *>(T + static_cast<int64_t>(m) * r + j) = b;
   }
-  // not earlier: a register more and two workgroups instead of three fit a compute unit
+  // not earlier, for the registers' sake
   f32x4_t seg[kSeg];
   if (wave < kMB) {
 #pragma unroll
