@@ -501,7 +501,7 @@ __global__ __launch_bounds__(S::kThreads, 2) void k_ad_matmul(const AdMatmul g) 
   }
 }
 
-// A tile's splits added in order, then as above (105 x 3232 x 10944: the layer takes 62 us
+// A tile's splits added in order, then as above (105 x 3232 x 10944: the layer takes 56 us
 // with the contraction split and this launch, 179 without).
 template <class S>
 __global__ __launch_bounds__(S::kThreads, 2) void k_ad_join(const AdMatmul g) {
@@ -726,19 +726,23 @@ hipError_t launch_ad_down(const uint16_t *P, int M, int D, const uint16_t *Q, co
 
 namespace {
 using gemm16::Big;
+using gemm16::Deep;
 using gemm16::Mid;
-int mid_tiles(int64_t M, int64_t cols) { return static_cast<int>((M + Mid::kBM - 1) / Mid::kBM * ((cols + Mid::kBN - 1) / Mid::kBN)); }
+template <class S>
+int tiles_of(int64_t M, int64_t cols) {
+  return static_cast<int>((M + S::kBM - 1) / S::kBM * ((cols + S::kBN - 1) / S::kBN));
+}
 }  // namespace
 
-// Splits of the contraction for products of few tiles: as many as fill the 512
-// workgroups that the chip holds at once, 8 steps each at least.
+// Splits of the contraction for products of few tiles: as many as give every
+// compute unit a workgroup, 8 steps each at least.
 int ad_matmul_splits(int64_t M, int64_t cols, int64_t Kc) {
-  if (!gemm16::use_mid(M, cols)) return 1;
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({512 / mid_tiles(M, cols), Kc / 64 / 8, 16})));
+  if (!gemm16::use_mid(M, cols) || !gemm16::use_deep(M, cols)) return 1;
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({256 / tiles_of<Deep>(M, cols), Kc / 64 / 8, 16})));
 }
 size_t ad_matmul_part_floats(int64_t M, int64_t cols, int64_t Kc) {
   const int splits = ad_matmul_splits(M, cols, Kc);
-  return splits > 1 ? static_cast<size_t>(splits) * mid_tiles(M, cols) * Mid::kBM * Mid::kBN : 0;
+  return splits > 1 ? static_cast<size_t>(splits) * tiles_of<Deep>(M, cols) * Deep::kBM * Deep::kBN : 0;
 }
 
 template <bool kNN>
@@ -746,19 +750,22 @@ static hipError_t launch_ad_matmul(AdMatmul g, hipStream_t s) {
   g.cols = kNN ? g.K : g.N;
   g.splits = ad_matmul_splits(g.M, g.cols, g.Kc);
   if (!gemm16::use_mid(g.M, g.cols)) {
-    const int tiles = ((g.M + Big::kBM - 1) / Big::kBM) * ((g.cols + Big::kBN - 1) / Big::kBN);
-    hipLaunchKernelGGL((k_ad_matmul<Big, kNN, false>), dim3(tiles), dim3(Big::kThreads), 0, s, g);
+    hipLaunchKernelGGL((k_ad_matmul<Big, kNN, false>), dim3(tiles_of<Big>(g.M, g.cols)), dim3(Big::kThreads), 0, s, g);
     return hipGetLastError();
   }
-  const int tiles = mid_tiles(g.M, g.cols);
-  if (g.splits == 1) {
+  const int tiles = tiles_of<Deep>(g.M, g.cols);
+  if (!gemm16::use_deep(g.M, g.cols)) {
     hipLaunchKernelGGL((k_ad_matmul<Mid, kNN, false>), dim3(tiles), dim3(Mid::kThreads), 0, s, g);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL((k_ad_matmul<Mid, kNN, true>), dim3(tiles * g.splits), dim3(Mid::kThreads), 0, s, g);
+  if (g.splits == 1) {
+    hipLaunchKernelGGL((k_ad_matmul<Deep, kNN, false>), dim3(tiles), dim3(Deep::kThreads), 0, s, g);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL((k_ad_matmul<Deep, kNN, true>), dim3(tiles * g.splits), dim3(Deep::kThreads), 0, s, g);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(k_ad_join<Mid>, dim3(tiles), dim3(Mid::kThreads), 0, s, g);
+  hipLaunchKernelGGL(k_ad_join<Deep>, dim3(tiles), dim3(Deep::kThreads), 0, s, g);
   return hipGetLastError();
 }
 hipError_t launch_ad_matmul_fwd(const uint16_t *X, int M, int N, int K, const uint16_t *Wd, const uint16_t *T, const uint16_t *B, int r,

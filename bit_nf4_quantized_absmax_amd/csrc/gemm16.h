@@ -5,10 +5,11 @@
 //     NN:  C[i][j] = sum_k L[i][k] R[k][j]      R row-major [contraction][cols]
 //
 //  * Tiles of kWM x kWN waves of 32 kFM x 32 kFN fp32 accumulators each: Big, 256 x
-//    256 of 8 waves, and Mid, 128 x 128 of 4, of which a compute unit holds two
-//    workgroups, for products with too few Big tiles to fill the chip.
+//    256 of 8 waves, and Mid and Deep, 128 x 128 of 4, for products with too few
+//    Big tiles to fill the chip.
 //  * Contraction step 64, both operands global -> LDS by DMA one step ahead (two
-//    stages of each).
+//    stages of each; a compute unit holds two Mid workgroups, which hide each other's
+//    waits), in Deep, for a workgroup that is alone on its compute unit, two ahead.
 //  * LDS rows of 128 bytes (L, and R of NT) and of 2 BN bytes (R of NN) with
 //    their 16-byte chunks XOR-swizzled by row; NN reads its right operand with
 //    the transposing LDS load, so that neither form needs a transposed copy.
@@ -36,21 +37,23 @@ typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kBK = 64;
 constexpr int kXcds = 8;
-constexpr int kBand = 4;   // tile rows of a band: an XCD's tiles share rows of L and columns of R in its L2
+constexpr int kBand = 4;   // tile rows of a band: an XCD's tiles share rows of L and columns of R in its L2 (2, 8 and 16: 1 to 3 % longer)
 
-template <int kWM_, int kWN_, int kFM_, int kFN_>
+template <int kWM_, int kWN_, int kFM_, int kFN_, int kStages_ = 2>
 struct Shape {
+  static constexpr int kStages = kStages_;
   static constexpr int kWM = kWM_, kWN = kWN_, kFM = kFM_, kFN = kFN_;
   static constexpr int kBM = 32 * kFM * kWM, kBN = 32 * kFN * kWN;
   static constexpr int kWaves = kWM * kWN, kThreads = 64 * kWaves;
   static constexpr int kStageL = kBM * 128, kStageR = kBN * 128;
-  static constexpr int kLds = 2 * (kStageL + kStageR);
+  static constexpr int kLds = kStages * (kStageL + kStageR);
   static constexpr int kWaveRows = 32 * kFM, kWaveCols = 32 * kFN;
   static constexpr int kDmaL = kBM / 8 / kWaves, kDmaR = kBN / 8 / kWaves;   // 1 KB instructions a wave and stage
   static_assert(kLds >= kWaves * kWaveRows * kWaveCols * 2, "the tile in bf16 fits the stages");
 };
 using Big = Shape<2, 4, 4, 2>;
 using Mid = Shape<2, 2, 2, 2>;
+using Deep = Shape<2, 2, 2, 2, 3>;
 
 // Whether a product takes Mid tiles, by the rounds that its tiles make of the 256
 // compute units.  A round of Big tiles is four Mid tiles' work; two Mid
@@ -61,6 +64,13 @@ inline bool use_mid(int64_t rows, int64_t cols) {
   const int64_t big = ((rows + 255) / 256) * ((cols + 255) / 256), mid = ((rows + 127) / 128) * ((cols + 127) / 128);
   return (mid <= 256 ? 17 : 27 * ((mid + 511) / 512)) < 40 * ((big + 255) / 256);
 }
+
+// Deep tiles instead of Mid ones where every tile has a compute unit to itself (the layer with
+// adapters, us, Mid with its contraction split for 512 workgroups and Deep for 256: 256 x
+// 4096 x 4096 52 and 45, 192 x 4096 x 4096 50 and 44, 1024 x 4096 x 4096 68 and 65, 105 x 3232 x
+// 10944 61 and 56; four stages as three; 300 Deep tiles take two rounds: 777 x 5000 x
+// 1088 40 and 54).
+inline bool use_deep(int64_t rows, int64_t cols) { return ((rows + 127) / 128) * ((cols + 127) / 128) <= 256; }
 
 // Rows of 2 BN bytes: chunk c of row r at c ^ g(r).
 template <class S>
@@ -214,7 +224,7 @@ __device__ __forceinline__ void tile(uint8_t *smem, const uint16_t *L, uint32_t 
       dma16(base, lo[j], __builtin_amdgcn_readfirstlane(lds0 + st * S::kStageL + (p.wave * S::kDmaL + j) * 1024));
   };
   auto dma_r = [&](int st, int kt) __attribute__((always_inline)) {
-    const uint32_t dst = lds0 + 2 * S::kStageL + st * S::kStageR + p.wave * S::kDmaR * 1024;
+    const uint32_t dst = lds0 + S::kStages * S::kStageL + st * S::kStageR + p.wave * S::kDmaR * 1024;
     if (kNN) {
       const uint16_t *base = R + static_cast<int64_t>(kBK) * kt * ldr;
       const int last = klast - kBK * kt;
@@ -229,9 +239,22 @@ __device__ __forceinline__ void tile(uint8_t *smem, const uint16_t *L, uint32_t 
   };
   const Offsets<S> ops = offsets<S>(p);
   clear<S>(acc);
-  dma_l(0, 0);
-  dma_r(0, 0);
-  raw_barrier<wait_imm(0, 0)>();
+  constexpr int kDma = S::kDmaL + S::kDmaR, kAhead = S::kStages - 1;   // steps that are asked for ahead
+  static_assert(kAhead <= 2, "the waits below");
+#pragma unroll
+  for (int st = 0; st < kAhead; ++st)
+    if (st < KT) {
+      dma_l(st, st);
+      dma_r(st, st);
+    }
+  // Waits until a step has landed, `behind` of the steps after it being asked for.
+  auto landed = [&](int behind) __attribute__((always_inline)) {
+    if (kAhead > 1 && behind >= 1)
+      raw_barrier<wait_imm(kDma, 0)>();
+    else
+      raw_barrier<wait_imm(0, 0)>();
+  };
+  landed(min(kAhead, KT) - 1);
   Frag<S> fa, fb;
 #pragma unroll
   for (int i = 0; i < S::kFM; ++i) fb.a[i] = bf16x8_t{};
@@ -240,14 +263,15 @@ __device__ __forceinline__ void tile(uint8_t *smem, const uint16_t *L, uint32_t 
   constexpr int kHeld = S::kFM / 2;                  // row fragments of a step's last products held back over its barrier
   auto step = [&](int cur, int kt) __attribute__((always_inline)) {
     const uint8_t *xs = smem + cur * S::kStageL;
-    const uint8_t *ws = smem + 2 * S::kStageL + cur * S::kStageR;
+    const uint8_t *ws = smem + S::kStages * S::kStageL + cur * S::kStageR;
+    const int fill = kAhead == 1 ? cur ^ 1 : cur == 0 ? kAhead : cur - 1;
     load_frag<S, kNN>(fa, xs, ws, ops, 0);
     __builtin_amdgcn_sched_barrier(0);
     mfma_rows<S, kHeld, kHeld + (S::kFM - kHeld) / 2>(fb, acc);
-    if (kt + 1 < KT) dma_l(cur ^ 1, kt + 1);
+    if (kt + kAhead < KT) dma_l(fill, kt + kAhead);
     __builtin_amdgcn_sched_barrier(0);
     mfma_rows<S, kHeld + (S::kFM - kHeld) / 2, S::kFM>(fb, acc);
-    if (kt + 1 < KT) dma_r(cur ^ 1, kt + 1);
+    if (kt + kAhead < KT) dma_r(fill, kt + kAhead);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
@@ -261,14 +285,23 @@ __device__ __forceinline__ void tile(uint8_t *smem, const uint16_t *L, uint32_t 
       if (s < 3) mfma_rows<S, kHeld, S::kFM>(now, acc);
       __builtin_amdgcn_sched_barrier(0);
     }
-    raw_barrier<wait_imm(0, 0)>();
+    landed(min(kt + kAhead, KT - 1) - (kt + 1));
   };
   int kt = 0;
-  for (; kt + 2 <= KT; kt += 2) {
-    step(0, kt);
-    step(1, kt + 1);
+  if constexpr (S::kStages == 2) {
+    for (; kt + 2 <= KT; kt += 2) {
+      step(0, kt);
+      step(1, kt + 1);
+    }
+    if (kt < KT) step(0, kt);
+  } else {
+    int cur = 0;
+#pragma unroll 1
+    for (; kt < KT; ++kt) {
+      step(cur, kt);
+      cur = cur == kAhead ? 0 : cur + 1;
+    }
   }
-  if (kt < KT) step(0, kt);
   mfma_rows<S, kHeld, S::kFM>(fb, acc);   // held back by the last step
 }
 
