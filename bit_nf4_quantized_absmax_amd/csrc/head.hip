@@ -816,6 +816,7 @@ int tiles_of(int64_t rows, int64_t cols) {
   return static_cast<int>(((rows + S::kBM - 1) / S::kBM) * ((cols + S::kBN - 1) / S::kBN));
 }
 using gemm16::Big;
+using gemm16::Deep;
 using gemm16::Mid;
 }  // namespace
 
@@ -823,7 +824,7 @@ HeadCut head_cut(int64_t M, int64_t K, int64_t words) {
   HeadCut c;
   if (M <= kHeadSmall) {
     // one or two workgroups a compute unit, as their stages allow
-    c.mid = 0;
+    c.deep = 0;
     c.bm = c.bn = 1;
     c.slots = 0;
     c.cost = 0.f;
@@ -831,14 +832,16 @@ HeadCut head_cut(int64_t M, int64_t K, int64_t words) {
     c.most = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({(M <= 32 ? 512 : 256) / cols, words / 512, 64})));
     return c;
   }
-  // Splits fill the chip with either tile; Mid ones where Big would be half empty
-  // (300 x 32000 x 4096: 280 us with Big, 317 with Mid; 100 x 32000 x 4096: 208 and 189).
-  c.mid = M <= Mid::kBM ? 1 : 0;
-  c.bm = c.mid ? Mid::kBM : Big::kBM;
-  c.bn = c.mid ? Mid::kBN : Big::kBN;
-  c.slots = c.mid ? 512 : 256;
-  // a tile's 4 bytes an element out and in at 5 TB/s, against a step of 64 words of a round: 1.7 us (Mid 0.85 of a pair)
-  c.cost = static_cast<float>(c.bm * c.bn * 8 / 5e6) / ((c.mid ? 0.85f : 1.7f) * static_cast<float>((words + 63) / 64));
+  // Splits fill the chip with either tile; 128-wide ones where Big would be half empty
+  // (300 x 32000 x 4096: 280 us with Big, 317 with Mid; 100 x 32000 x 4096: 208 and 189),
+  // Deep ones, as they are alone on their compute unit then (128 x 32000 x 4096: 160 us
+  // with Mid and 512 slots, 151 with Deep and 256).
+  c.deep = M <= Deep::kBM ? 1 : 0;
+  c.bm = c.deep ? Deep::kBM : Big::kBM;
+  c.bn = c.deep ? Deep::kBN : Big::kBN;
+  c.slots = 256;
+  // a tile's 4 bytes an element out and in at 5 TB/s, against a step of 64 words of a round: 1.7 us (Deep 0.85)
+  c.cost = static_cast<float>(c.bm * c.bn * 8 / 5e6) / ((c.deep ? 0.85f : 1.7f) * static_cast<float>((words + 63) / 64));
   // each at least 8 steps of 64 words long, their sums within 512 MB
   c.most = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({32, words / 512, (int64_t{1} << 27) / (M * K)})));
   return c;
@@ -855,10 +858,17 @@ hipError_t launch_head_gather(const uint16_t *X, int M, int K, const HeadRows &h
   return hipGetLastError();
 }
 
-template <class S, bool kE>
+// 128 x 32000 x 4096: the loss alone takes 81.5 us with Mid tiles and 74 with Deep ones, with
+// the gradient 151 and 138.
+template <bool kE>
 static hipError_t launch_head_logits(const uint16_t *X, int M, const uint16_t *W, int K, int v0, int words, const HeadRows &h,
                                      const HeadPiece &pc, hipStream_t s) {
-  hipLaunchKernelGGL((k_head_logits<S, kE>), dim3(tiles_of<S>(M, words)), dim3(S::kThreads), 0, s, X, W, K, v0, words, h, pc);
+  if (!gemm16::use_mid(M, words))
+    hipLaunchKernelGGL((k_head_logits<Big, kE>), dim3(tiles_of<Big>(M, words)), dim3(Big::kThreads), 0, s, X, W, K, v0, words, h, pc);
+  else if (gemm16::use_deep(M, words))
+    hipLaunchKernelGGL((k_head_logits<Deep, kE>), dim3(tiles_of<Deep>(M, words)), dim3(Deep::kThreads), 0, s, X, W, K, v0, words, h, pc);
+  else
+    hipLaunchKernelGGL((k_head_logits<Mid, kE>), dim3(tiles_of<Mid>(M, words)), dim3(Mid::kThreads), 0, s, X, W, K, v0, words, h, pc);
   return hipGetLastError();
 }
 
@@ -893,11 +903,7 @@ hipError_t launch_head_small_piece(const uint16_t *X, const int64_t *target, int
 
 hipError_t launch_head_piece(const uint16_t *X, int M, const uint16_t *W, int V, int K, int v0, int words, bool first, const HeadRows &h,
                              const HeadPiece &pc, const HeadCut &cut, float *C, hipStream_t s) {
-  const bool mid = gemm16::use_mid(M, words);
-  hipError_t e = C ? (mid ? launch_head_logits<Mid, true>(X, M, W, K, v0, words, h, pc, s)
-                          : launch_head_logits<Big, true>(X, M, W, K, v0, words, h, pc, s))
-                   : (mid ? launch_head_logits<Mid, false>(X, M, W, K, v0, words, h, pc, s)
-                          : launch_head_logits<Big, false>(X, M, W, K, v0, words, h, pc, s));
+  hipError_t e = C ? launch_head_logits<true>(X, M, W, K, v0, words, h, pc, s) : launch_head_logits<false>(X, M, W, K, v0, words, h, pc, s);
   if (e != hipSuccess) return e;
   // more threads a row while the rows are few (300 rows, 782 groups: 13 us with 16 threads a row)
   if (M <= 2048)
@@ -913,8 +919,8 @@ hipError_t launch_head_piece(const uint16_t *X, int M, const uint16_t *W, int V,
   int items = trows * tcols;
   for (int r = 1; r <= trows && r * tcols <= 50 * cut.slots; ++r) items = std::max(items, r * tcols * splits_for(r * tcols, cut));
   const dim3 grid(items);
-  if (cut.mid)
-    hipLaunchKernelGGL(k_head_acc<Mid>, grid, dim3(Mid::kThreads), 0, s, W, V, K, v0, cut, first ? 1 : 0, h,
+  if (cut.deep)
+    hipLaunchKernelGGL(k_head_acc<Deep>, grid, dim3(Deep::kThreads), 0, s, W, V, K, v0, cut, first ? 1 : 0, h,
                        pc, C);
   else
     hipLaunchKernelGGL(k_head_acc<Big>, grid, dim3(Big::kThreads), 0, s, W, V, K, v0, cut, first ? 1 : 0, h,

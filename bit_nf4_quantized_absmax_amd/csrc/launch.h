@@ -392,7 +392,7 @@ struct HeadPiece {
 // How the second product is cut: its tiles, workgroups at once, splits at most.
 struct HeadCut {
   int bm, bn, slots, most;
-  int mid;
+  int deep;
   float cost;      // see splits_for
 };
 constexpr int kHeadSmall = 64;   // rows up to which W's bytes count
