@@ -17,8 +17,8 @@
 // one adapter stays there.
 //
 // Bound by the wide products: 8192 x 4096 x 11008 with 8 adapters of rank 64 takes
-// 680 us (690 of 807 in a trace), a step of 8192 x 4096 x 4096 with 32 of rank 16 takes 560
-// to 580.
+// 660 to 690 us (the product 600 to 690), a step of 8192 x 4096 x 4096 with 32 of rank 16
+// takes 550 to 580.
 #include <algorithm>
 
 #include "common.h"
