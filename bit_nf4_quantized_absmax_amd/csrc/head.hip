@@ -24,7 +24,8 @@
 //    contraction, they are copied together (k_head_gather).
 //  * dW, where the head is tuned as well, makes its logits a second time, for
 //    dz needs the whole row's sum: dz^T piece by piece in bf16 (k_head_dz), then
-//    dz^T X (k_head_dw).
+//    dz^T X (k_head_dw).  p_t - 1 of a sure target comes from the loss there, too, which
+//    the row's pair for the log-sum-exp holds (RowResult).
 //  * Bound by the two (with dW four) products: 8192 x 32000 x 4096 with 6144 targets takes
 //    2770 us (1.16 PFLOP/s over the whole call), 2048 x 131072 x 4096 with dW
 //    7500 (1.17); few rows by reading W, 58 us for one of 32000 x 4096 (4.6 TB/s).
@@ -41,6 +42,8 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kBucket = 44.361419555836498f;   // 64 ln 2
 constexpr float kWide = 0x1p20f;                 // above it a multiple of kBucket has no bits left to be near anything
+constexpr float kSure = 0.5f;                    // losses below it: p_t above 0.6
+constexpr float kNoLoss = 0x1p-126f;             // stands for a loss of 0 (or below it) where a positive one is needed
 
 // e^x through the hardware's 2^x (x <= 23 here; what underflows is 0).
 __device__ __forceinline__ float exp_f(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
@@ -75,18 +78,27 @@ __host__ __device__ __forceinline__ int splits_for(int tiles, const HeadCut &cut
   return best;
 }
 
-// A row's loss and log-sum-exp (ref + rest) from the sum s of all words but the
-// target at a reference (0: there are none) and the target's logit; inv: 1 / the whole sum at that reference.
+// A row's loss and log-sum-exp from the sum s of all words but the target at a
+// reference (0: there are none) and the target's logit; inv: 1 / the whole sum at that reference.
+// The log-sum-exp is a pair that sums to it: (reference, rest), or where the target is sure
+// (loss, target's logit), from which dW takes p_t - 1 = expm1(-loss) without a
+// difference of two numbers near 1.  The loss is told from a reference by lying in (0, kSure): a
+// reference is 0, a multiple of kBucket or beyond kWide.
 struct RowResult {
-  float loss, ref, rest, inv;
-  __device__ __forceinline__ RowResult(double s, double zt, float at) : ref(at) {
+  float loss, inv, lse[2];
+  __device__ __forceinline__ RowResult(double s, float zt, float at) {
     const double u = static_cast<double>(at) - zt;
     double l = s == 0.0 ? 0.0 : u > 0.0 ? u + log(s + exp(-u)) : log1p(s * exp(u));
-    if (!(fabs(zt) < INFINITY) || !(s < INFINITY)) l = NAN;
+    if (!(fabsf(zt) < INFINITY) || !(s < INFINITY)) l = NAN;
     inv = s == 0.0 ? 0.f : static_cast<float>(exp(u - l));
-    if (s == 0.0 || zt > at + kBucket) ref = ref_of(static_cast<float>(zt));
-    rest = static_cast<float>(l + (zt - ref));
     loss = static_cast<float>(l);
+    if (loss < kSure) {
+      lse[0] = fmaxf(loss, kNoLoss);
+      lse[1] = zt;
+    } else {
+      lse[0] = static_cast<double>(zt) > static_cast<double>(at) + kBucket ? ref_of(zt) : at;
+      lse[1] = static_cast<float>(l + (static_cast<double>(zt) - lse[0]));
+    }
   }
 };
 
@@ -348,8 +360,8 @@ __global__ __launch_bounds__(256) void k_head_refs(HeadRows h, HeadPiece pc, int
     if (loss) {
       const RowResult r(all, h.zt[row], top);
       loss[blockIdx.x] = r.loss;
-      lse[2 * blockIdx.x] = r.ref;
-      lse[2 * blockIdx.x + 1] = r.rest;
+      lse[2 * blockIdx.x] = r.lse[0];
+      lse[2 * blockIdx.x + 1] = r.lse[1];
     } else {
       h.ref[row] = top;
       h.sum[row] = all;
@@ -652,7 +664,7 @@ __global__ __launch_bounds__(kSmThreads) void k_head_small_acc(const uint16_t *_
 }
 
 // ---------------------------------------------------------------------------
-// A workgroup a row of X and 2048 columns: its loss and (ref, log sum); with kGrad 1
+// A workgroup a row of X and 2048 columns: its loss and log-sum-exp; with kGrad 1
 // (bf16) or 2 (fp32) its gradient, weight (C / sum + (p_t - 1) W_t).  Bound by reading C:
 // 8192 rows x 4096, 6144 with a target, two splits: 66 to 71 us; 225 rows x 1088, 32
 // splits: 12 (31 MB, eight splits' loads of a thread at once).
@@ -662,18 +674,18 @@ __global__ __launch_bounds__(256) void k_head_finish(const uint16_t *__restrict_
                                                      float *__restrict__ lse, void *__restrict__ dX) {
   const int64_t m = blockIdx.x;
   const int at = h.place[m];
-  float l = 0.f, lg = 0.f, ref = 0.f, inv = 0.f;
+  float l = 0.f, lse0 = 0.f, lse1 = 0.f, inv = 0.f;
   if (at >= 0) {
     const RowResult r(h.sum[at], h.zt[at], h.ref[at]);
     l = r.loss;
-    ref = r.ref;
-    lg = r.rest;
+    lse0 = r.lse[0];
+    lse1 = r.lse[1];
     inv = r.inv;
   }
   if (threadIdx.x == 0 && blockIdx.y == 0) {
     loss[m] = l;
-    lse[2 * m] = ref;
-    lse[2 * m + 1] = lg;
+    lse[2 * m] = lse0;
+    lse[2 * m + 1] = lse1;
   }
   if constexpr (kGrad != 0) {
     const float g = at < 0 ? 0.f : (weight ? weight[m] : 1.f);
@@ -740,15 +752,17 @@ __global__ __launch_bounds__(256) void k_head_scale(const float *__restrict__ D,
 
 // ---------------------------------------------------------------------------
 // dz^T [word][pitch] of words v0 .. v0 + words - 1 and the listed rows, in bf16;
-// zeros in the columns count .. (count filled up to 64) - 1.  2048 rows x 65536 words x 4096:
-// 938 to 956 us (1.15 to 1.17 PFLOP/s), as k_head_dw below.
+// zeros in the columns count .. (count filled up to 64) - 1.  The target's p_t - 1 is
+// expm1(-loss) where the row's pair holds the loss (see RowResult): there p_t, from a
+// logit that another order of sums rounded otherwise, says nothing of 1 - p_t.  2048 rows x 65536
+// words x 4096: 938 to 956 us (1.15 to 1.17 PFLOP/s), as k_head_dw below.
 template <class S>
 __global__ __launch_bounds__(S::kThreads, 2) void k_head_dz(const uint16_t *__restrict__ Xc, const uint16_t *__restrict__ W, int K, int v0,
                                                               int words, HeadRows h, const float *__restrict__ lse,
                                                               const float *__restrict__ weight, int64_t pitch, uint16_t *__restrict__ Zt) {
   using namespace gemm16;
   __shared__ __attribute__((aligned(16))) uint8_t smem[S::kLds];
-  __shared__ float sRef[S::kBN], sRest[S::kBN], sG[S::kBN];
+  __shared__ float sRef[S::kBN], sRest[S::kBN], sG[S::kBN], sOwn[S::kBN];   // sOwn: the target's p - 1, above 0 where p is to be used
   __shared__ int sT[S::kBN];
   const int count = h.count[0];
   int tr, tc;
@@ -758,8 +772,11 @@ __global__ __launch_bounds__(S::kThreads, 2) void k_head_dz(const uint16_t *__re
     const int at = c0 + threadIdx.x;
     const bool live = at < count;
     const int64_t m = live ? h.list[at] : 0;
-    sRef[threadIdx.x] = live ? lse[2 * m] : 0.f;
-    sRest[threadIdx.x] = live ? lse[2 * m + 1] : 0.f;
+    const float first = live ? lse[2 * m] : 0.f, second = live ? lse[2 * m + 1] : 0.f;
+    const bool sure = first > 0.f && first < kSure;
+    sRef[threadIdx.x] = sure ? second : first;
+    sRest[threadIdx.x] = sure ? first : second;
+    sOwn[threadIdx.x] = !sure ? 1.f : first > kNoLoss ? expm1f(-first) : 0.f;
     sG[threadIdx.x] = live ? (weight ? weight[m] : 1.f) : 0.f;
     sT[threadIdx.x] = live ? h.tgt[at] - v0 : -1;
   }
@@ -774,12 +791,12 @@ __global__ __launch_bounds__(S::kThreads, 2) void k_head_dz(const uint16_t *__re
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
       const int c = w.col0() + 32 * j + 8 * (e >> 2) + 4 * lh + (e & 3);
-      const float ref = sRef[c], rest = sRest[c], g = sG[c];
+      const float ref = sRef[c], rest = sRest[c], g = sG[c], own = sOwn[c];
       const int t = sT[c];
 #pragma unroll
       for (int i = 0; i < S::kFM; ++i) {
         const float p = exp_f((acc[i][j][e] - ref) - rest);
-        acc[i][j][e] = c < top ? g * (t == w0 + w.row0() + 32 * i + lr ? p - 1.f : p) : 0.f;
+        acc[i][j][e] = c < top ? g * (t == w0 + w.row0() + 32 * i + lr ? (own > 0.f ? p - 1.f : own) : p) : 0.f;
       }
     }
   store_bf16<S>(acc, smem, [&](int row, int col, uint4 v) {

@@ -41,8 +41,8 @@ def _forward(X, W, target, weight, dX, workspace):
 def head_cross_entropy_fwd(X, W, target, workspace=None):
     """Losses log sum_j e^z_mj - z_m,target, z = X W^T, of hidden states X [M, K]
     and a head W [V, K] in bf16; target int64 [M] (outside [0, V): loss 0).
-    Returns (loss [M], lse [M, 2]), the sum of lse's pair being the log-sum-exp
-    (qlora_head_cross_entropy)."""
+    Returns (loss [M], lse [M, 2]), the sum of lse's pair being the log-sum-exp;
+    head_cross_entropy_dW takes the pairs as they are (qlora_head_cross_entropy)."""
     return _forward(X, W, target, None, None, workspace)
 
 
@@ -58,7 +58,7 @@ def head_cross_entropy(X, W, target, weight=None, dX_out=None, workspace=None):
 
 def head_cross_entropy_dW(X, W, target, lse, weight=None, dW_out=None, workspace=None):
     """The gradient [V, K] of the head for gradients weight [M] of the losses, from
-    the lse of either call above (qlora_head_cross_entropy_dW)."""
+    the lse that either call above returned (qlora_head_cross_entropy_dW)."""
     M, V, K = _checks(X, W, target, weight)
     _need(lse, torch.float32, "lse", (M, 2))
     dev = X.device

@@ -719,8 +719,9 @@ typedef enum { QLORA_HEAD_LOSS = 0, QLORA_HEAD_DX = 1, QLORA_HEAD_DW = 2 } qlora
 /* Workspace bytes of a pass (qlora_head_cross_entropy without or with dX, its _dW). */
 size_t qlora_head_workspace_bytes(int64_t M, int64_t V, int64_t K, int32_t pass);
 
-/* loss [M], and lse [M][2], a pair (reference, rest) whose sum is log sum_j e^z_mj
- * (0, 0 without a target).  dX (nullable): [M, K], of bf16 (dx_fp32 0) or fp32 (1), for
+/* loss [M], and lse [M][2], a pair whose sum is log sum_j e^z_mj (0, 0 without a
+ * target): a reference and the rest, or, below a loss of 1/2, the loss (at least 2^-126)
+ * and the target's logit.  dX (nullable): [M, K], of bf16 (dx_fp32 0) or fp32 (1), for
  * gradients weight [M] (NULL: 1) of the losses: two products where loss and gradient
  * come from one call, as with a step's weights known beforehand. */
 int qlora_head_cross_entropy(const uint16_t *X, int64_t M, const uint16_t *W, int64_t V, int64_t K, const int64_t *target,
@@ -730,7 +731,7 @@ int qlora_head_cross_entropy(const uint16_t *X, int64_t M, const uint16_t *W, in
 /* dX [M, K] bf16 = g_m D_m from that call's fp32 gradient D at weight 1. */
 int qlora_head_scale(const float *D, int64_t M, int64_t V, int64_t K, const int64_t *target, const float *g, uint16_t *dX, void *stream);
 
-/* dW [V, K] bf16, for a head that is tuned too, from that call's lse (the logits are made again).  M = 0 writes nothing. */
+/* dW [V, K] bf16, for a head that is tuned too, from the pairs lse as that call wrote them (the logits are made again).  M = 0 writes nothing. */
 int qlora_head_cross_entropy_dW(const uint16_t *X, int64_t M, const uint16_t *W, int64_t V, int64_t K, const int64_t *target,
                                 const float *lse, const float *weight, uint16_t *dW, void *ws, size_t ws_bytes, void *stream);
 
