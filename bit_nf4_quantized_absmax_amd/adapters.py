@@ -121,6 +121,14 @@ class AdapterLinear(torch.nn.Module):
         self.lora_B = torch.nn.Parameter(lora_B if lora_B is not None else
                                          torch.zeros(adapters, N, r, dtype=torch.bfloat16, device=dev))
 
+    def _apply(self, fn, recurse=True):
+        """Moves and casts as any module's, but the scales stay the float32 values that the kernels take."""
+        scale = self.scale
+        super()._apply(fn, recurse)
+        if self.scale.dtype != torch.float32:
+            self.scale = scale.to(self.scale.device)
+        return self
+
     def forward(self, x, index):
         """x [..., K]; index int64 [...], the adapter of every token."""
         lead = x.shape[:-1]
