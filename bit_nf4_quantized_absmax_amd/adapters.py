@@ -106,7 +106,9 @@ class AdapterLinearFn(torch.autograd.Function):
 
 class AdapterLinear(torch.nn.Module):
     """QLoRALinear with `adapters` LoRA pairs over one frozen NF4 weight; the
-    adapter of every token comes with the call.  alpha: one value, or one an adapter."""
+    adapter of every token comes with the call.  alpha: one value, or one an adapter.
+    Where they are not given, lora_B is zero and lora_A uniform within K^-1/2: with both
+    at zero, so would be their gradients, for ever."""
 
     def __init__(self, weight, adapters, r, alpha, lora_A=None, lora_B=None):
         super().__init__()
@@ -116,8 +118,9 @@ class AdapterLinear(torch.nn.Module):
         self.r = int(r)
         scale = torch.as_tensor(alpha, dtype=torch.float32, device=dev) / float(r)
         self.register_buffer("scale", scale.expand(adapters).contiguous())
-        self.lora_A = torch.nn.Parameter(lora_A if lora_A is not None else
-                                         torch.zeros(adapters, r, K, dtype=torch.bfloat16, device=dev))
+        if lora_A is None:
+            lora_A = torch.empty(adapters, r, K, dtype=torch.bfloat16, device=dev).uniform_(-K ** -0.5, K ** -0.5)
+        self.lora_A = torch.nn.Parameter(lora_A)
         self.lora_B = torch.nn.Parameter(lora_B if lora_B is not None else
                                          torch.zeros(adapters, N, r, dtype=torch.bfloat16, device=dev))
 

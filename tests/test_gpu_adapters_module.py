@@ -1,4 +1,4 @@
-"""AdapterLinear as a module: casts of the whole module."""
+"""AdapterLinear as a module: its defaults, and casts of the whole module."""
 
 import copy
 
@@ -40,3 +40,18 @@ def test_state_of_a_cast_module_loads():
     other.scale.zero_()
     other.bfloat16().load_state_dict(state)
     assert torch.equal(other.scale, lin.scale) and other.scale.dtype == torch.float32
+
+
+@pytest.mark.parametrize("M", [5, 90])
+def test_a_layer_without_given_pairs_learns(M):
+    """At the start the output is the base's alone, and a step's gradients move it."""
+    lin, g = _layer()
+    x = torch.randn(M, 128, generator=g).to(BF16).to(DEV)
+    idx = (torch.arange(M) % 2).to(DEV)                  # adapter 2 has no token
+    with torch.no_grad():
+        assert torch.equal(lin(x, idx), lin(x, torch.full_like(idx, -1)))
+    lin(x, idx).backward(torch.randn(M, 72, generator=g).to(BF16).to(DEV))
+    assert lin.lora_B.grad[:2].flatten(1).any(1).all() and not lin.lora_B.grad[2].any()
+    bound = 128 ** -0.5
+    assert float(lin.lora_A.abs().max()) <= bound * (1 + 2.0 ** -8) and float(lin.lora_A.float().std()) > 0.4 * bound
+    assert lin.lora_A.dtype == BF16 and not torch.equal(lin.lora_A[0], lin.lora_A[1])
