@@ -7,6 +7,7 @@ import ctypes
 
 import torch
 from torch.autograd.function import once_differentiable
+from torch.autograd.graph import increment_version
 
 from ._capi import AdaptersStruct, check, lib
 from .ops import NF4Weight, _mat, _need, _out, _ptr, _stream, _workspace
@@ -25,6 +26,14 @@ def _on(device, *tensors):
         if t is not None and t.get_device() != index:
             raise ValueError("tensors on different devices: %s and %s" % (device, t.device))
     return _SAME_DEVICE if _current_device() == index else torch.cuda.device(device)
+
+
+def _written(*tensors):
+    """The caller's tensors (or None) have new values: autograd learns it as from torch's own in-place
+    calls, and what it had saved of them raises in backward() instead of being used."""
+    given = [t for t in tensors if t is not None]
+    if given:
+        increment_version(given)
 
 
 def _checks(X, w, A, B, scale, index):
@@ -56,6 +65,7 @@ def adapter_linear_fwd(X, w, A, B, scale, index, T_out=None, out=None, workspace
     with _on(dev, w.packed, A, B, scale, index, Y, T, ws):
         check(lib().qlora_adapter_linear_fwd(_ptr(X), M, ctypes.byref(wt), ctypes.byref(st), _ptr(Y), _ptr(T), _ptr(ws), ws_bytes,
                                              _stream(X)), "qlora_adapter_linear_fwd")
+    _written(out, T_out)
     return Y, T
 
 
@@ -81,6 +91,7 @@ def adapter_linear_bwd(dY, X, T, w, A, B, scale, index, need_dX=True, need_dA=Tr
         for d in (dA, dB):
             if d is not None:
                 d.zero_()
+    _written(dX_out if need_dX else None, dA_out if need_dA else None, dB_out if need_dB else None)
     return dX, dA, dB
 
 

@@ -7,6 +7,7 @@ import struct
 from operator import attrgetter
 
 import torch
+from torch.autograd.graph import increment_version
 
 from ._capi import check, lib
 from .adapters import _on
@@ -48,8 +49,9 @@ def _call(grads, max_norm, groups, out, workspace):
                 raise ValueError("every gradient's first axis must hold %d equal parts, got shape %s" % (groups, tuple(t.shape)))
     to = ptrs
     if max_norm is not None:
+        written = grads if out is None else list(out)
         if out is not None:
-            to, to_counts, to_types, to_device = _listed(list(out), "out")
+            to, to_counts, to_types, to_device = _listed(written, "out")
             if to_types != types or to_counts != counts or to_device != device:
                 raise ValueError("out must be one tensor of the same size, type and device for every gradient")
         if len(set(to)) != len(to):
@@ -69,6 +71,7 @@ def _call(grads, max_norm, groups, out, workspace):
         else:
             check(lib().qlora_clip_grad_norm(n, table, groups, float(max_norm), _ptr(norm), _ptr(ws), ws_bytes, _stream(first)),
                   "qlora_clip_grad_norm")
+            increment_version(written)   # to autograd a change like that of torch's own in-place calls
     return norm
 
 

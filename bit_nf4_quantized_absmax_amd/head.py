@@ -7,7 +7,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from ._capi import check, lib
-from .adapters import _on
+from .adapters import _on, _written
 from .ops import _mat, _need, _out, _ptr, _stream, _workspace
 
 LOSS, DX, DW = 0, 1, 2   # qlora_head_pass
@@ -53,7 +53,9 @@ def head_cross_entropy(X, W, target, weight=None, dX_out=None, workspace=None):
     dtype = dX_out.dtype if isinstance(dX_out, torch.Tensor) and dX_out.dtype == torch.float32 else torch.bfloat16
     M, K = _mat(X, "X")
     dX = _out(dX_out, (M, K), X.device, "dX", dtype)
-    return _forward(X, W, target, weight, dX, workspace) + (dX,)
+    loss, lse = _forward(X, W, target, weight, dX, workspace)
+    _written(dX_out)
+    return loss, lse, dX
 
 
 def head_cross_entropy_dW(X, W, target, lse, weight=None, dW_out=None, workspace=None):
@@ -69,6 +71,7 @@ def head_cross_entropy_dW(X, W, target, lse, weight=None, dW_out=None, workspace
                                                 ws_bytes, _stream(X)), "qlora_head_cross_entropy_dW")
     if M == 0:   # the call above writes nothing then
         dW.zero_()
+    _written(dW_out)
     return dW
 
 
