@@ -49,9 +49,10 @@ size_t carve(void *ws, int64_t M, int64_t V, int64_t K, int32_t pass, Parts *p) 
   p->h.tgt = c.take<int>(M);
   p->h.count = c.take<int>(1);
   if (pass == QLORA_HEAD_DW) {
-    p->Xc = c.take<uint16_t>(round_up(M, 64) * K);
-    p->words = piece_words(round_up(M, 64), V, K, kPieceE);
-    p->Zt = c.take<uint16_t>(p->words * round_up(M, 64));
+    const int64_t depth = head_dw_depth(M);
+    p->Xc = c.take<uint16_t>(depth * K);
+    p->words = piece_words(depth, V, K, kPieceE);
+    p->Zt = c.take<uint16_t>(p->words * depth);
     return c.used;
   }
   p->h.zt = c.take<float>(M);

@@ -159,8 +159,8 @@ __global__ __launch_bounds__(1024) void k_head_rows(const int64_t *__restrict__ 
   if (threadIdx.x == 0) h.count[0] = base;
 }
 
-// Xc [count filled up to 64][K]: the listed rows of X, zeros behind.
-__global__ __launch_bounds__(256) void k_head_gather(const uint16_t *__restrict__ X, int K, HeadRows h, uint16_t *__restrict__ Xc) {
+// Xc [count filled up to 64][K]: the listed rows of X, zeros behind; twice: the same again behind them.
+__global__ __launch_bounds__(256) void k_head_gather(const uint16_t *__restrict__ X, int K, HeadRows h, int twice, uint16_t *__restrict__ Xc) {
   const int count = h.count[0], rows = (count + 63) / 64 * 64, per = K >> 3;
   const int64_t all = static_cast<int64_t>(rows) * per;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < all; i += static_cast<int64_t>(gridDim.x) * 256) {
@@ -168,6 +168,7 @@ __global__ __launch_bounds__(256) void k_head_gather(const uint16_t *__restrict_
     uint4 v = make_uint4(0, 0, 0, 0);
     if (row < count) v = *reinterpret_cast<const uint4 *>(X + static_cast<int64_t>(h.list[row]) * K + 8 * c);
     *reinterpret_cast<uint4 *>(Xc + static_cast<int64_t>(row) * K + 8 * c) = v;
+    if (twice) *reinterpret_cast<uint4 *>(Xc + static_cast<int64_t>(rows + row) * K + 8 * c) = v;
   }
 }
 
@@ -754,9 +755,14 @@ __global__ __launch_bounds__(256) void k_head_scale(const float *__restrict__ D,
 // dz^T [word][pitch] of words v0 .. v0 + words - 1 and the listed rows, in bf16;
 // zeros in the columns count .. (count filled up to 64) - 1.  The target's p_t - 1 is
 // expm1(-loss) where the row's pair holds the loss (see RowResult): there p_t, from a
-// logit that another order of sums rounded otherwise, says nothing of 1 - p_t.  2048 rows x 65536
-// words x 4096: 938 to 956 us (1.15 to 1.17 PFLOP/s), as k_head_dw below.
-template <class S>
+// logit that another order of sums rounded otherwise, says nothing of 1 - p_t.
+// kTwo (up to kHeadSmall rows): a second 64 columns hold what the first lost to bf16.  A word
+// that is the target of one row has that row's dz times X for its row of dW, and nothing
+// averages the roundings of few rows (one row of 17000 words: error of dW against float64
+// 1.3 times that of its own rounding, 1.0 so; 17000 to 131072 words, 1 to 64 rows: dW 5 to 10 % longer,
+// 168 to 178 us at 64 x 32000 x 4096).  More rows: 1.15 to 1.4 times, for half the product.
+// 2048 rows x 65536 words x 4096: 931 to 956 us (1.15 to 1.18 PFLOP/s), as k_head_dw below.
+template <class S, bool kTwo>
 __global__ __launch_bounds__(S::kThreads, 2) void k_head_dz(const uint16_t *__restrict__ Xc, const uint16_t *__restrict__ W, int K, int v0,
                                                               int words, HeadRows h, const float *__restrict__ lse,
                                                               const float *__restrict__ weight, int64_t pitch, uint16_t *__restrict__ Zt) {
@@ -800,18 +806,33 @@ __global__ __launch_bounds__(S::kThreads, 2) void k_head_dz(const uint16_t *__re
       }
     }
   store_bf16<S>(acc, smem, [&](int row, int col, uint4 v) {
-    if (w0 + row < words && c0 + col < pitch) *reinterpret_cast<uint4 *>(Zt + (w0 + row) * pitch + c0 + col) = v;
+    if (w0 + row < words && c0 + col < (kTwo ? 64 : pitch)) *reinterpret_cast<uint4 *>(Zt + (w0 + row) * pitch + c0 + col) = v;
   });
+  if constexpr (kTwo) {
+#pragma unroll
+    for (int i = 0; i < S::kFM; ++i)
+#pragma unroll
+      for (int j = 0; j < S::kFN; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float held = bf16_to_f32(f32_to_bf16(acc[i][j][e]));
+          acc[i][j][e] = fabsf(held) < INFINITY ? acc[i][j][e] - held : 0.f;
+        }
+    __builtin_amdgcn_wave_barrier();                   // the first store has read its region
+    store_bf16<S>(acc, smem, [&](int row, int col, uint4 v) {
+      if (w0 + row < words && c0 + col < 64) *reinterpret_cast<uint4 *>(Zt + (w0 + row) * pitch + 64 + c0 + col) = v;
+    });
+  }
 }
 
-// dW rows v0 .. v0 + words - 1 = dz^T X over the listed rows.
+// dW rows v0 .. v0 + words - 1 = dz^T X over the listed rows (twice: over both parts of dz).
 template <class S>
 __global__ __launch_bounds__(S::kThreads, 2) void k_head_dw(const uint16_t *__restrict__ Zt, int64_t pitch,
                                                               const uint16_t *__restrict__ Xc, int K, int v0, int words, HeadRows h,
-                                                              uint16_t *__restrict__ dW) {
+                                                              int twice, uint16_t *__restrict__ dW) {
   using namespace gemm16;
   __shared__ __attribute__((aligned(16))) uint8_t smem[S::kLds];
-  const int KT = (h.count[0] + kBK - 1) / kBK;
+  const int KT = (h.count[0] + kBK - 1) / kBK << twice;
   int tr, tc;
   if (!place(blockIdx.x, (words + S::kBM - 1) / S::kBM, (K + S::kBN - 1) / S::kBN, tr, tc)) return;
   const int w0 = tr * S::kBM, c0 = tc * S::kBN;
@@ -871,7 +892,8 @@ hipError_t launch_head_rows(const int64_t *target, int M, int V, const HeadRows 
 
 hipError_t launch_head_gather(const uint16_t *X, int M, int K, const HeadRows &h, uint16_t *Xc, hipStream_t s) {
   const int64_t n = (static_cast<int64_t>(M) + 63) / 64 * 64 * K / 8;
-  hipLaunchKernelGGL(k_head_gather, dim3(static_cast<int>(std::min<int64_t>(2048, (n + 255) / 256))), dim3(256), 0, s, X, K, h, Xc);
+  hipLaunchKernelGGL(k_head_gather, dim3(static_cast<int>(std::min<int64_t>(2048, (n + 255) / 256))), dim3(256), 0, s, X, K, h,
+                     M <= kHeadSmall ? 1 : 0, Xc);
   return hipGetLastError();
 }
 
@@ -965,19 +987,23 @@ hipError_t launch_head_scale(const float *D, int64_t M, int K, const int64_t *ta
 
 hipError_t launch_head_dw(const uint16_t *Xc, int M, const uint16_t *W, int K, int v0, int words, const HeadRows &h, const float *lse,
                           const float *weight, uint16_t *Zt, uint16_t *dW, hipStream_t s) {
-  const int64_t pitch = (static_cast<int64_t>(M) + 63) / 64 * 64;
-  if (gemm16::use_mid(words, M))
-    hipLaunchKernelGGL(k_head_dz<Mid>, dim3(tiles_of<Mid>(words, M)), dim3(Mid::kThreads), 0, s, Xc, W, K, v0, words, h, lse, weight, pitch,
+  const int64_t pitch = head_dw_depth(M);
+  const int twice = M <= kHeadSmall ? 1 : 0;
+  if (twice)   // one column of tiles of either shape
+    hipLaunchKernelGGL((k_head_dz<Mid, true>), dim3(tiles_of<Mid>(words, M)), dim3(Mid::kThreads), 0, s, Xc, W, K, v0, words, h, lse,
+                       weight, pitch, Zt);
+  else if (gemm16::use_mid(words, M))
+    hipLaunchKernelGGL((k_head_dz<Mid, false>), dim3(tiles_of<Mid>(words, M)), dim3(Mid::kThreads), 0, s, Xc, W, K, v0, words, h, lse, weight, pitch,
                        Zt);
   else
-    hipLaunchKernelGGL(k_head_dz<Big>, dim3(tiles_of<Big>(words, M)), dim3(Big::kThreads), 0, s, Xc, W, K, v0, words, h, lse, weight, pitch,
+    hipLaunchKernelGGL((k_head_dz<Big, false>), dim3(tiles_of<Big>(words, M)), dim3(Big::kThreads), 0, s, Xc, W, K, v0, words, h, lse, weight, pitch,
                        Zt);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (gemm16::use_mid(words, K))
-    hipLaunchKernelGGL(k_head_dw<Mid>, dim3(tiles_of<Mid>(words, K)), dim3(Mid::kThreads), 0, s, Zt, pitch, Xc, K, v0, words, h, dW);
+    hipLaunchKernelGGL(k_head_dw<Mid>, dim3(tiles_of<Mid>(words, K)), dim3(Mid::kThreads), 0, s, Zt, pitch, Xc, K, v0, words, h, twice, dW);
   else
-    hipLaunchKernelGGL(k_head_dw<Big>, dim3(tiles_of<Big>(words, K)), dim3(Big::kThreads), 0, s, Zt, pitch, Xc, K, v0, words, h, dW);
+    hipLaunchKernelGGL(k_head_dw<Big>, dim3(tiles_of<Big>(words, K)), dim3(Big::kThreads), 0, s, Zt, pitch, Xc, K, v0, words, h, twice, dW);
   return hipGetLastError();
 }
 

@@ -398,7 +398,9 @@ struct HeadCut {
 constexpr int kHeadSmall = 64;   // rows up to which W's bytes count
 HeadCut head_cut(int64_t M, int64_t K, int64_t words);
 hipError_t launch_head_rows(const int64_t *target, int M, int V, const HeadRows &h, hipStream_t s);
-// Xc [M filled up to 64, K]
+// Contraction of dW: the rows filled up to 64, twice that up to kHeadSmall of them (see k_head_dz).
+inline int64_t head_dw_depth(int64_t M) { return M <= kHeadSmall ? 128 : (M + 63) / 64 * 64; }
+// Xc [head_dw_depth, K]
 hipError_t launch_head_gather(const uint16_t *X, int M, int K, const HeadRows &h, uint16_t *Xc, hipStream_t s);
 // Words v0 .. v0 + words - 1; C [cut.most][M][K] fp32, or nullptr without a gradient.
 hipError_t launch_head_piece(const uint16_t *X, int M, const uint16_t *W, int V, int K, int v0, int words, bool first, const HeadRows &h,
@@ -412,7 +414,7 @@ hipError_t launch_head_small_piece(const uint16_t *X, const int64_t *target, int
 hipError_t launch_head_finish(const uint16_t *W, int64_t M, int K, const float *weight, const HeadRows &h, const HeadCut &cut, const float *C,
                               float *loss, float *lse, void *dX, int grad, hipStream_t s);
 hipError_t launch_head_scale(const float *D, int64_t M, int K, const int64_t *target, int V, const float *g, uint16_t *dX, hipStream_t s);
-// Rows v0 .. v0 + words - 1 of dW; Zt [words, M filled up to 64].
+// Rows v0 .. v0 + words - 1 of dW; Zt [words, head_dw_depth].
 hipError_t launch_head_dw(const uint16_t *Xc, int M, const uint16_t *W, int K, int v0, int words, const HeadRows &h, const float *lse,
                           const float *weight, uint16_t *Zt, uint16_t *dW, hipStream_t s);
 

@@ -709,8 +709,10 @@ int qlora_adapter_linear_bwd(const uint16_t *dY, const uint16_t *X, const uint16
  *   dz_mj  = weight_m (p_mj - [j = t]),  p = softmax(z);   dX = dz W,   dW = dz^T X
  * A target outside [0, V) (prompt, padding) is no target: loss 0 and gradient 0,
  * whatever X and weight hold there; such rows cost nothing.  The vocabulary is taken in
- * pieces; e^z (dW: dz) is rounded to bf16 between the two products, except the
- * target's own term; sums are fp32, over words 64 bits.  A NaN or an infinity of a row of X
+ * pieces; e^z except the target's own term, and for dW all of dz, is rounded to bf16
+ * between the two products (dz up to 64 rows to two bf16 numbers); sums are fp32,
+ * over words 64 bits.  The target's p - 1 is formed from the loss, so that it is right for
+ * sure targets, too.  A NaN or an infinity of a row of X
  * makes that row's loss and dX NaN.  Logits stay below 2^127 in size.  Outputs overlap
  * no input, but for dX, which may be X itself.  K % 64 == 0, M <= 2^22, M K < 2^31, K <= 2^18, V < 2^31. */
 
